@@ -40,7 +40,16 @@ BFQ_W_PACKED16 = 1
 BFQ_SCALE_FP32 = 0
 BFQ_SCALE_UE8M0 = 1
 
+# activations of the gated product (bfq_activation)
+BFQ_ACT_SILU = 0
+BFQ_ACT_GELU_TANH = 1
+# what one gate value of the norm step covers (bfq_gate_kind)
+BFQ_GATE_NONE, BFQ_GATE_CHANNEL, BFQ_GATE_TOKEN, BFQ_GATE_FULL = range(4)
+
 DEFAULT_EPS = 1e-10
+NORM_EPS = 1e-6
+# Maximum K of the norm step (a row stays in a workgroup's registers).
+NORM_MAX_K = 16384
 BLOCK_SHAPE = (128, 128)
 # Maximum K of the per-token x per-channel format (block_shape (1, K)).
 CHANNEL_MAX_K = 32768
@@ -61,6 +70,10 @@ EXPORTED = (
     "bfq_moe_gemm_workspace_bytes", "bfq_moe_block_gemm", "bfq_moe_num_tile_candidates",
     "bfq_moe_get_tile_candidate", "bfq_block_gemm_noalloc", "bfq_noalloc_scratch_bytes",
     "bfq_probe_mfma_peak", "bfq_probe_mfma_flops",
+    "bfq_gated_gemm", "bfq_gated_select_tile", "bfq_gated_gemm_workspace_bytes",
+    "bfq_gated_num_tile_candidates", "bfq_gated_get_tile_candidate", "bfq_gated_backward",
+    "bfq_transpose_weights", "bfq_norm_residual", "bfq_norm_residual_backward",
+    "bfq_norm_residual_backward_workspace_bytes",
 )
 
 
@@ -138,6 +151,19 @@ def _load():
         "bfq_noalloc_scratch_bytes": (sz, []),
         "bfq_probe_mfma_peak": (i32, [i64, i64, p, p]),
         "bfq_probe_mfma_flops": (ctypes.c_double, [i64, i64]),
+        "bfq_gated_gemm": (i32, [p, p, i32, i64, p, p, i32, i32, i32, p, p, i32, i64, f32, p, i64,
+                                 i64, i64, bs, i32, i32, tp, p, sz, p]),
+        "bfq_gated_select_tile": (i32, [i64, i64, i64, i32, i32, i32, tp]),
+        "bfq_gated_gemm_workspace_bytes": (sz, [i64, i64, i64, i32, i32, i32, tp]),
+        "bfq_gated_num_tile_candidates": (i32, [i32, i32]),
+        "bfq_gated_get_tile_candidate": (i32, [i32, i32, i32, tp]),
+        "bfq_gated_backward": (i32, [p, p, i32, p, p, i32, p, i32, i64, f32, i32, p, i64, i64, p]),
+        "bfq_transpose_weights": (i32, [p, p, i64, i64, i32, p, p, p]),
+        "bfq_norm_residual": (i32, [p, p, i32, p, p, i32, f32, p, f32, p, p, p, i32, i32, p, i32,
+                                    i64, f32, i32, i64, i64, p]),
+        "bfq_norm_residual_backward_workspace_bytes": (sz, [i64, i64]),
+        "bfq_norm_residual_backward": (i32, [p, p, i32, p, p, i32, f32, p, f32, p, p, p, p, p, p, p,
+                                             i64, i64, p, sz, p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -595,6 +621,222 @@ def bfq_debug_encode(x, codes, q_dtype=BFQ_E4M3FN, stream=None) -> int:
     return _check(st, "bfq_debug_encode")
 
 
+# ------------------------------------------------------------- feed-forward operators
+
+def _workspace_arg(workspace, workspace_bytes):
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return workspace_bytes
+
+
+def bfq_gated_select_tile(M, F, K, out_dtype=BFQ_BF16, w_layout=BFQ_W_ROW_MAJOR,
+                          scale_fmt=BFQ_SCALE_FP32) -> bfq_tile:
+    """The tile bfq_gated_gemm takes (bn = output columns of a workgroup)."""
+    t = bfq_tile()
+    _check(lib.bfq_gated_select_tile(M, F, K, out_dtype, w_layout, scale_fmt, ctypes.byref(t)),
+           "bfq_gated_select_tile")
+    return t
+
+
+def bfq_gated_gemm_workspace_bytes(M, F, K, out_dtype=BFQ_BF16, w_layout=BFQ_W_ROW_MAJOR,
+                                   scale_fmt=BFQ_SCALE_FP32, tile=None) -> int:
+    return int(lib.bfq_gated_gemm_workspace_bytes(M, F, K, out_dtype, w_layout, scale_fmt,
+                                                  ctypes.byref(tile) if tile else None))
+
+
+def bfq_gated_num_tile_candidates(w_layout=BFQ_W_ROW_MAJOR, scale_fmt=BFQ_SCALE_FP32) -> int:
+    return int(lib.bfq_gated_num_tile_candidates(w_layout, scale_fmt))
+
+
+def bfq_gated_get_tile_candidate(index, w_layout=BFQ_W_ROW_MAJOR,
+                                 scale_fmt=BFQ_SCALE_FP32) -> bfq_tile:
+    t = bfq_tile()
+    _check(lib.bfq_gated_get_tile_candidate(w_layout, scale_fmt, index, ctypes.byref(t)),
+           "bfq_gated_get_tile_candidate")
+    return t
+
+
+def bfq_gated_gemm(a_q, a_scales, w_q, w_scales, out, act=BFQ_ACT_SILU,
+                   a_layout=BFQ_SCALES_ROW_MAJOR, a_scale_ld=None, out_scales=None,
+                   out_layout=BFQ_SCALES_ROW_MAJOR, out_scale_ld=None, out_eps=DEFAULT_EPS,
+                   preact=None, tile=None, workspace=None, workspace_bytes=None, stream=None,
+                   w_layout=BFQ_W_ROW_MAJOR, scale_fmt=BFQ_SCALE_FP32) -> int:
+    """out[m][f] = act(g) * u, both factors block-scaled products of token row m (a_q [M, K]) with
+    rows f and F + f of w_q [2F, K] (row-major or packed), w_scales [2F/128, K/128]. out [M, F]
+    bf16 / fp16 / fp32, or e4m3fn codes (uint8 / float8_e4m3fn) with out_scales, one per 128
+    columns, in out_layout. preact: bf16 [M, 2F] that receives (g, u)."""
+    M, K = _shape2(a_q, "a_q")
+    rows = _shape2(w_q, "w_q")[0]
+    if rows % 2 != 0:
+        raise BfqArgumentError(f"w_q has {rows} rows; expected the gate rows and as many up rows")
+    F = rows // 2
+    _rows(a_q, "a_q", U8_CODES, M, K)
+    _rows(w_q, "w_q", U8_CODES, 2 * F, K)
+    if a_scale_ld is None:
+        a_scale_ld = a_scales.stride(0)
+    _scales(a_scales, "a_scales", a_layout, a_scale_ld, M, K // 128, write=False)
+    _flat(w_scales, "w_scales", ("float32",), (2 * F // 128) * (K // 128))
+    _rows(out, "out", OUT_DTYPES + U8_CODES, M, F)
+    codes = not isinstance(out, int) and _dt(out) in U8_CODES
+    if codes != (out_scales is not None):
+        raise BfqArgumentError("out_scales goes with an out of codes, and only with it")
+    if codes:
+        if out_scale_ld is None:
+            out_scale_ld = out_scales.stride(0)
+        _scales(out_scales, "out_scales", out_layout, out_scale_ld, M, F // 128, write=True)
+    if preact is not None:
+        _rows(preact, "preact", ("bfloat16",), M, 2 * F)
+    workspace_bytes = _workspace_arg(workspace, workspace_bytes)
+    _workspace(workspace, workspace_bytes)
+    _devices(a_q=a_q, a_scales=a_scales, w_q=w_q, w_scales=w_scales, out=out,
+             out_scales=out_scales, preact=preact, workspace=workspace)
+    st = lib.bfq_gated_gemm(_ptr(a_q), _ptr(a_scales), a_layout, a_scale_ld, _ptr(w_q),
+                            _ptr(w_scales), w_layout, scale_fmt, act, _ptr(out), _ptr(out_scales),
+                            out_layout, out_scale_ld or 0, out_eps, _ptr(preact), M, F, K,
+                            _block_shape(BLOCK_SHAPE), BFQ_E4M3FN,
+                            BFQ_E4M3FN if codes else _odtype(out),
+                            ctypes.byref(tile) if tile else None, _ptr(workspace),
+                            workspace_bytes, _stream(stream))
+    return _check(st, "bfq_gated_gemm")
+
+
+def bfq_gated_backward(preact, dh, act=BFQ_ACT_SILU, dpre=None, q=None, scales=None,
+                       layout=BFQ_SCALES_ROW_MAJOR, scale_ld=None, q_eps=DEFAULT_EPS,
+                       scale_fmt=BFQ_SCALE_FP32, h=None, stream=None) -> int:
+    """Gradient of act(g) * u at preact = (g, u) bf16 [M, 2F], for dh bf16 [M, F]: dpre bf16
+    [M, 2F], and / or q (codes [M, 2F]) with scales (one per 128 columns); h bf16 [M, F] receives
+    the product again."""
+    M, F = _shape2(dh, "dh")
+    _rows(preact, "preact", ("bfloat16",), M, 2 * F)
+    _rows(dh, "dh", ("bfloat16",), M, F)
+    if dpre is not None:
+        _rows(dpre, "dpre", ("bfloat16",), M, 2 * F)
+    if h is not None:
+        _rows(h, "h", ("bfloat16",), M, F)
+    if (q is None) != (scales is None):
+        raise BfqArgumentError("q and scales go together")
+    if q is not None:
+        _rows(q, "q", CODE_DTYPES, M, 2 * F)
+        if scale_ld is None:
+            scale_ld = scales.stride(0)
+        _scales(scales, "scales", layout, scale_ld, M, 2 * F // 128, write=True)
+    _devices(preact=preact, dh=dh, dpre=dpre, q=q, scales=scales, h=h)
+    st = lib.bfq_gated_backward(_ptr(preact), _ptr(dh), act, _ptr(dpre), _ptr(q),
+                                _qdtype(q) if q is not None else BFQ_E4M3FN, _ptr(scales), layout,
+                                scale_ld or 0, q_eps, scale_fmt, _ptr(h), M, F, _stream(stream))
+    return _check(st, "bfq_gated_backward")
+
+
+def bfq_transpose_weights(w_q, w_scales, wt_q, wt_scales, stream=None) -> int:
+    """w_q: row-major codes [N, K] with w_scales [N/128, K/128]; wt_q [K, N] and wt_scales
+    [K/128, N/128] receive the transpose (row-major)."""
+    N, K = _shape2(w_q, "w_q")
+    _rows(w_q, "w_q", CODE_DTYPES, N, K)
+    _rows(wt_q, "wt_q", CODE_DTYPES, K, N)
+    _same_codes(w_q, wt_q)
+    _flat(w_scales, "w_scales", ("float32",), (N // 128) * (K // 128))
+    _flat(wt_scales, "wt_scales", ("float32",), (N // 128) * (K // 128))
+    _devices(w_q=w_q, w_scales=w_scales, wt_q=wt_q, wt_scales=wt_scales)
+    st = lib.bfq_transpose_weights(_ptr(w_q), _ptr(w_scales), N, K, _qdtype(w_q), _ptr(wt_q),
+                                   _ptr(wt_scales), _stream(stream))
+    return _check(st, "bfq_transpose_weights")
+
+
+RES_DTYPES = ("bfloat16", "float32")
+
+
+def _norm_operands(residual, name, y, w_post, gate, gate_kind, w_pre):
+    """Checks of what the norm step and its gradients share; returns (M, K, res_dtype)."""
+    M, K = _shape2(residual, name)
+    _rows(residual, name, RES_DTYPES, M, K)
+    if y is not None:
+        _rows(y, "y", ("bfloat16",), M, K)
+    for n, w in (("w_post", w_post), ("w_pre", w_pre)):
+        if w is not None:
+            _flat(w, n, ("bfloat16",), K)
+    if (gate is None) != (gate_kind == BFQ_GATE_NONE):
+        raise BfqArgumentError("gate goes with a gate_kind other than BFQ_GATE_NONE, and only with it")
+    if gate is not None:
+        if gate_kind == BFQ_GATE_FULL:
+            _rows(gate, "gate", ("bfloat16",), M, K)
+        else:
+            _flat(gate, "gate", ("bfloat16",), M if gate_kind == BFQ_GATE_TOKEN else K)
+    return M, K, BFQ_BF16 if _dt(residual) == "bfloat16" else BFQ_FP32
+
+
+def bfq_norm_residual(residual, y=None, w_post=None, gate=None, gate_kind=BFQ_GATE_NONE,
+                      res_scale=1.0, w_pre=None, norm_eps=NORM_EPS, res_out=None, normed=None,
+                      q=None, scales=None, layout=BFQ_SCALES_ROW_MAJOR, scale_ld=None,
+                      q_eps=DEFAULT_EPS, group_size=128, scale_fmt=BFQ_SCALE_FP32,
+                      stream=None) -> int:
+    """One step of the residual stream: r' = residual + res_scale * gate * z with z = y or the
+    RMS norm of y times w_post, stored in res_out (which may be residual); then the RMS norm of r'
+    times w_pre, as normed (bf16 [M, K]) and / or codes q with scales. residual bf16 or fp32
+    [M, K], y bf16 [M, K] or None, gate bf16 [K], [M] or [M, K] by gate_kind."""
+    M, K, rt = _norm_operands(residual, "residual", y, w_post, gate, gate_kind, w_pre)
+    if res_out is not None:
+        _rows(res_out, "res_out", (_dt(residual),), M, K)
+    if normed is not None:
+        _rows(normed, "normed", ("bfloat16",), M, K)
+    if (q is None) != (scales is None):
+        raise BfqArgumentError("q and scales go together")
+    if q is not None:
+        _rows(q, "q", CODE_DTYPES, M, K)
+        if scale_ld is None:
+            scale_ld = scales.stride(0)
+        if group_size > 0 and K % group_size == 0:
+            _scales(scales, "scales", layout, scale_ld, M, K // group_size, write=True)
+    _devices(residual=residual, y=y, w_post=w_post, gate=gate, w_pre=w_pre, res_out=res_out,
+             normed=normed, q=q, scales=scales)
+    st = lib.bfq_norm_residual(_ptr(y), _ptr(residual), rt, _ptr(w_post), _ptr(gate), gate_kind,
+                               res_scale, _ptr(w_pre), norm_eps, _ptr(res_out), _ptr(normed),
+                               _ptr(q), _qdtype(q) if q is not None else BFQ_E4M3FN, group_size,
+                               _ptr(scales), layout, scale_ld or 0, q_eps, scale_fmt, M, K,
+                               _stream(stream))
+    return _check(st, "bfq_norm_residual")
+
+
+def bfq_norm_residual_backward_workspace_bytes(M, K) -> int:
+    return int(lib.bfq_norm_residual_backward_workspace_bytes(M, K))
+
+
+def bfq_norm_residual_backward(res_out, d_res, y=None, w_post=None, gate=None,
+                               gate_kind=BFQ_GATE_NONE, res_scale=1.0, w_pre=None,
+                               norm_eps=NORM_EPS, d_normed=None, d_res_out=None, d_y=None,
+                               d_w_pre=None, d_w_post=None, d_gate=None, workspace=None,
+                               workspace_bytes=None, stream=None) -> int:
+    """Gradients of bfq_norm_residual from the stored sum res_out, the gradient d_normed (bf16) of
+    its normed output and d_res_out (res_out's dtype) of the sum: d_res (res_out's dtype; may be
+    d_res_out), d_y (bf16), and where wanted d_w_pre, d_w_post (fp32 [K]) and d_gate (fp32 [K] or
+    [M], bf16 [M, K] for a full gate)."""
+    M, K, rt = _norm_operands(res_out, "res_out", y, w_post, gate, gate_kind, w_pre)
+    _rows(d_res, "d_res", (_dt(res_out),), M, K)
+    if d_res_out is not None:
+        _rows(d_res_out, "d_res_out", (_dt(res_out),), M, K)
+    for n, t in (("d_normed", d_normed), ("d_y", d_y)):
+        if t is not None:
+            _rows(t, n, ("bfloat16",), M, K)
+    for n, t in (("d_w_pre", d_w_pre), ("d_w_post", d_w_post)):
+        if t is not None:
+            _flat(t, n, ("float32",), K)
+    if d_gate is not None:
+        if gate_kind == BFQ_GATE_FULL:
+            _rows(d_gate, "d_gate", ("bfloat16",), M, K)
+        else:
+            _flat(d_gate, "d_gate", ("float32",), M if gate_kind == BFQ_GATE_TOKEN else K)
+    workspace_bytes = _workspace_arg(workspace, workspace_bytes)
+    _workspace(workspace, workspace_bytes)
+    _devices(res_out=res_out, y=y, w_post=w_post, gate=gate, w_pre=w_pre, d_normed=d_normed,
+             d_res_out=d_res_out, d_res=d_res, d_y=d_y, d_w_pre=d_w_pre, d_w_post=d_w_post,
+             d_gate=d_gate, workspace=workspace)
+    st = lib.bfq_norm_residual_backward(_ptr(y), _ptr(res_out), rt, _ptr(w_post), _ptr(gate),
+                                        gate_kind, res_scale, _ptr(w_pre), norm_eps,
+                                        _ptr(d_normed), _ptr(d_res_out), _ptr(d_res), _ptr(d_y),
+                                        _ptr(d_w_pre), _ptr(d_w_post), _ptr(d_gate), M, K,
+                                        _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check(st, "bfq_norm_residual_backward")
+
+
 # ------------------------------------------------------------ allocating conveniences
 
 def quant_tokens(x, q_dtype=BFQ_E4M3FN, layout=BFQ_SCALES_ROW_MAJOR, eps=DEFAULT_EPS,
@@ -703,3 +945,114 @@ def block_gemm(a_q, a_scales, w_q, w_scales, out_dtype=None, a_layout=BFQ_SCALES
                    workspace=ws, workspace_bytes=ws_bytes, stream=stream, w_layout=w_layout,
                    scale_fmt=scale_fmt, block_shape=bs)
     return out
+
+
+def _alloc_scales(M, groups, layout, device):
+    """An empty scale tensor of the quantizers' output in `layout`."""
+    import torch
+    if layout == BFQ_SCALES_PACKED_UE8M0:
+        return torch.empty(((groups + 3) // 4, (M + 3) // 4 * 4), dtype=torch.int32, device=device)
+    shape = (M, groups) if layout == BFQ_SCALES_ROW_MAJOR else (groups, M)
+    return torch.empty(shape, dtype=torch.float32, device=device)
+
+
+def gated_gemm(a_q, a_scales, w_q, w_scales, act=BFQ_ACT_SILU, out_dtype=None, codes=False,
+               keep_preact=False, a_layout=BFQ_SCALES_ROW_MAJOR, out_layout=BFQ_SCALES_ROW_MAJOR,
+               tile=None, stream=None, w_layout=BFQ_W_ROW_MAJOR, scale_fmt=BFQ_SCALE_FP32):
+    """Allocate and run bfq_gated_gemm. Returns out, or (codes, scales) with `codes`; with
+    keep_preact followed by the bf16 pre-activations [M, 2F]."""
+    import torch
+    M, K = a_q.shape
+    F, dev = w_q.shape[0] // 2, a_q.device
+    out = torch.empty((M, F), dtype=torch.uint8 if codes else out_dtype or torch.bfloat16, device=dev)
+    scales = _alloc_scales(M, F // 128, out_layout, dev) if codes else None
+    pre = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dev) if keep_preact else None
+    n = bfq_gated_gemm_workspace_bytes(M, F, K, BFQ_E4M3FN if codes else _odtype(out), w_layout,
+                                       scale_fmt, tile)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    bfq_gated_gemm(a_q, a_scales, w_q, w_scales, out, act=act, a_layout=a_layout,
+                   out_scales=scales, out_layout=out_layout, preact=pre, tile=tile, workspace=ws,
+                   stream=stream, w_layout=w_layout, scale_fmt=scale_fmt)
+    res = ((out, scales) if codes else (out,)) + ((pre,) if keep_preact else ())
+    return res if len(res) > 1 else out
+
+
+def gated_backward(preact, dh, act=BFQ_ACT_SILU, codes=False, want_h=False,
+                   layout=BFQ_SCALES_ROW_MAJOR, q_dtype=BFQ_E4M3FN, scale_fmt=BFQ_SCALE_FP32,
+                   stream=None):
+    """Allocate and run bfq_gated_backward. Returns dpre (bf16), or (codes, scales) with `codes`;
+    with want_h followed by the product act(g) * u."""
+    import torch
+    M, F = dh.shape
+    dev = dh.device
+    q = scales = dpre = None
+    if codes:
+        q = torch.empty((M, 2 * F), dtype=torch.uint8 if q_dtype == BFQ_E4M3FN else torch.int8,
+                        device=dev)
+        scales = _alloc_scales(M, 2 * F // 128, layout, dev)
+    else:
+        dpre = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dev)
+    h = torch.empty((M, F), dtype=torch.bfloat16, device=dev) if want_h else None
+    bfq_gated_backward(preact, dh, act=act, dpre=dpre, q=q, scales=scales, layout=layout,
+                       scale_fmt=scale_fmt, h=h, stream=stream)
+    res = ((q, scales) if codes else (dpre,)) + ((h,) if want_h else ())
+    return res if len(res) > 1 else dpre
+
+
+def transpose_weights(w_q, w_scales, stream=None):
+    """Allocate and run bfq_transpose_weights: (codes [K, N], scales [K/128, N/128])."""
+    import torch
+    N, K = w_q.shape
+    wt = torch.empty((K, N), dtype=w_q.dtype, device=w_q.device)
+    st = torch.empty((K // 128, N // 128), dtype=torch.float32, device=w_q.device)
+    bfq_transpose_weights(w_q, w_scales, wt, st, stream=stream)
+    return wt, st
+
+
+def norm_residual(residual, y=None, w_post=None, gate=None, gate_kind=BFQ_GATE_NONE, res_scale=1.0,
+                  w_pre=None, norm_eps=NORM_EPS, codes=False, q_dtype=BFQ_E4M3FN, per_token=False,
+                  layout=BFQ_SCALES_ROW_MAJOR, scale_fmt=BFQ_SCALE_FP32, stream=None):
+    """Allocate and run bfq_norm_residual. Returns a tuple: the new residual (with y), then (with
+    w_pre) the normed bf16 rows or, with `codes`, their codes and scales."""
+    import torch
+    M, K = residual.shape
+    dev = residual.device
+    res_out = torch.empty_like(residual) if y is not None else None
+    q = scales = normed = None
+    group = K if per_token else 128
+    if w_pre is not None and codes:
+        q = torch.empty((M, K), dtype=torch.uint8 if q_dtype == BFQ_E4M3FN else torch.int8, device=dev)
+        scales = _alloc_scales(M, K // group, layout, dev)
+    elif w_pre is not None:
+        normed = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    bfq_norm_residual(residual, y=y, w_post=w_post, gate=gate, gate_kind=gate_kind,
+                      res_scale=res_scale, w_pre=w_pre, norm_eps=norm_eps, res_out=res_out,
+                      normed=normed, q=q, scales=scales, layout=layout, group_size=group,
+                      scale_fmt=scale_fmt, stream=stream)
+    return tuple(t for t in (res_out, normed, q, scales) if t is not None)
+
+
+def norm_residual_backward(res_out, y=None, w_post=None, gate=None, gate_kind=BFQ_GATE_NONE,
+                           res_scale=1.0, w_pre=None, norm_eps=NORM_EPS, d_normed=None,
+                           d_res_out=None, stream=None) -> dict:
+    """Allocate and run bfq_norm_residual_backward for every gradient its operands have. Returns
+    {"d_res", "d_y", "d_w_pre", "d_w_post", "d_gate"}, without those whose operand is absent."""
+    import torch
+    M, K = res_out.shape
+    dev = res_out.device
+    g = {"d_res": torch.empty_like(res_out)}
+    if y is not None:
+        g["d_y"] = torch.empty_like(y)
+    for n, w in (("d_w_pre", w_pre), ("d_w_post", w_post)):
+        if w is not None:
+            g[n] = torch.empty(K, dtype=torch.float32, device=dev)
+    if gate is not None:
+        g["d_gate"] = torch.empty(gate.shape, device=dev,
+                                  dtype=torch.bfloat16 if gate_kind == BFQ_GATE_FULL else torch.float32)
+    n = bfq_norm_residual_backward_workspace_bytes(M, K)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    bfq_norm_residual_backward(res_out, y=y, w_post=w_post, gate=gate, gate_kind=gate_kind,
+                               res_scale=res_scale, w_pre=w_pre, norm_eps=norm_eps,
+                               d_normed=d_normed, d_res_out=d_res_out, workspace=ws, stream=stream,
+                               **g)
+    return g

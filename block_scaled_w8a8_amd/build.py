@@ -19,8 +19,8 @@ LIB_PATH = os.path.join(HERE, "libbfq.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["quant.hip", "gemm_std.hip", "gemm_swapab.hip", "moe.hip", "probe.hip", "api.cpp",
-           "tile_table.cpp"]
+SOURCES = ["quant.hip", "gemm_std.hip", "gemm_swapab.hip", "moe.hip", "gated.hip", "norm.hip",
+           "probe.hip", "api.cpp", "api_ffn.cpp", "tile_table.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
           "-I" + os.path.join(REPO, "include")]
@@ -64,7 +64,7 @@ def build(jobs: int = 8) -> str:
 # BFQ_TILE_TABLE (TABLE_PATH).
 ASAN_LIB_PATH = os.path.join(REPO, "_build", "sanitize", "libbfq_asan.so")
 TABLE_PATH = os.path.join(HERE, "tables", "gfx950.json")
-HOST_SOURCES = ("api.cpp", "tile_table.cpp")
+HOST_SOURCES = ("api.cpp", "api_ffn.cpp", "tile_table.cpp")
 SANITIZE = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
             "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer",
             "-Xarch_host", "-O1"]

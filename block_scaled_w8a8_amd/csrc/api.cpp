@@ -18,7 +18,7 @@
 #include <sstream>
 #include <string>
 
-#include "bfq_internal.h"
+#include "api_common.h"
 #include "tile_table.h"
 
 using namespace bfq;
@@ -27,24 +27,24 @@ using namespace bfq;
 constexpr size_t kNoAllocScratchBytes = size_t(32) << 20;
 static __device__ __align__(256) uint8_t scratch[kNoAllocScratchBytes];
 
-namespace {
+static thread_local std::string g_last_error;
 
-thread_local std::string g_last_error;
-
-bfq_status fail(bfq_status s, const std::string& msg) {
+bfq_status bfq::fail(bfq_status s, const std::string& msg) {
     g_last_error = msg;
     return s;
 }
 
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
+static int g_batch_invariant = -1;   // -1: not yet read from the environment
 
-// Largest output count (M * N, grouped: T * topk * N) the GEMMs take: 2^40 elements, far past
-// any device memory, keeps split-K workspace sizes (256 splits of fp32) and the reduce
-// kernel's one-dimensional grid within range.
-constexpr int64_t kMaxOutputs = int64_t(1) << 40;
+bool bfq::batch_invariant() {
+    if (g_batch_invariant < 0) {
+        const char* e = std::getenv("BFQ_BATCH_INVARIANT");
+        g_batch_invariant = (e && e[0] == '1') ? 1 : 0;
+    }
+    return g_batch_invariant == 1;
+}
 
-// a * b >= kMaxOutputs for positive a, b, without overflow
-bool too_many_outputs(int64_t a, int64_t b) { return a > 0 && b > 0 && a > (kMaxOutputs - 1) / b; }
+namespace {
 
 // ------------------------------------------------------------------ tile table ----
 std::mutex g_table_mu;
@@ -159,10 +159,6 @@ const KernelEntry* find_kernel(const bfq_tile& t, int qtype, int otype, int wlay
     return nullptr;
 }
 
-constexpr int64_t kNumCUs = 256;   // MI355X: 8 XCDs x 32 CUs
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // Compiled-in default ([CONFIG] §4.1: no tuned entry -> a fixed default config). Below 32
 // tokens the swap-AB streaming kernel ([HELION]: the Hopper rule dispatches swap-AB for
 // M < 32), else the standard kernel with the largest tile that still yields one workgroup
@@ -249,16 +245,6 @@ bfq_tile invariant_tile(int64_t M, int wlayout, int sfmt) {
     return t;
 }
 
-int g_batch_invariant = -1;   // -1: not yet read from the environment
-
-bool batch_invariant() {
-    if (g_batch_invariant < 0) {
-        const char* e = std::getenv("BFQ_BATCH_INVARIANT");
-        g_batch_invariant = (e && e[0] == '1') ? 1 : 0;
-    }
-    return g_batch_invariant == 1;
-}
-
 // Grouped (MoE) default: the tile follows the average rows per active expert, r = pairs /
 // min(E, pairs) (a stand-in for the per-expert M): streaming swap-AB up to 128 rows (each
 // expert's weights are read once; tokens per wave up to 16, shared through LDS above), then
@@ -284,10 +270,6 @@ bfq_tile moe_default_tile(int64_t T, int64_t topk, int64_t E, int sfmt) {
     }
     return t;
 }
-
-int qtype_of(bfq_dtype d) { return d == BFQ_E4M3FN ? Q_FP8 : Q_INT8; }
-
-int otype_of(bfq_dtype d) { return d == BFQ_BF16 ? O_BF16 : d == BFQ_FP16 ? O_FP16 : O_FP32; }
 
 bfq_status select_tile(int64_t M, int64_t N, int64_t K, int qtype, int wlayout, int sfmt,
                        bfq_tile* out) {
@@ -357,10 +339,6 @@ bool block_shape_ok(const int32_t* bs) { return bs && bs[0] == 128 && bs[1] == 1
 
 const char* kBlockShapeMsg =
     "block_shape must be {128, 128} or {1, K} (per-channel, K a multiple of 128 up to 32768)";
-
-bool wlayout_ok(bfq_weight_layout w) { return w == BFQ_W_ROW_MAJOR || w == BFQ_W_PACKED16; }
-
-bool sfmt_ok(bfq_scale_format f) { return f == BFQ_SCALE_FP32 || f == BFQ_SCALE_UE8M0; }
 
 size_t workspace_for(int64_t M, int64_t N, const bfq_tile& t) {
     if (too_many_outputs(M, N)) return SIZE_MAX;   // a shape the GEMM rejects

@@ -9,7 +9,7 @@
 namespace bfq {
 
 enum QType { Q_FP8 = 0, Q_INT8 = 1 };
-enum OType { O_BF16 = 0, O_FP16 = 1, O_FP32 = 2 };
+enum OType { O_BF16 = 0, O_FP16 = 1, O_FP32 = 2, O_CODES = 3 };   // O_CODES: gated product only
 enum WLayout { W_ROW = 0, W_PACKED16 = 1 };   // bfq_weight_layout
 // How a kernel applies scales: per 128-wide K block, any fp32 values (S_FP32) or powers of two
 // only (S_UE8M0, bfq_scale_format); or one scale per token and per output channel after the
@@ -39,6 +39,59 @@ hipError_t launch_pack_weights(const void* w, void* packed, int64_t N, int64_t K
                                hipStream_t stream);
 hipError_t launch_debug_encode(const float* x, int64_t n, int qtype, void* out,
                                hipStream_t stream);
+
+// Norms around a block of the residual stream and their gradients (csrc/norm.hip). Unused
+// pointers are NULL; K a multiple of 8 (of 128 with 1x128 groups), at most kNormMaxK.
+constexpr int64_t kNormMaxK = 16384;
+struct NormArgs {
+    const void* y;          // [M][K] bf16: the block's output
+    const void* residual;   // [M][K] bf16 / fp32 (backward: the stored sum)
+    const void* w_post;     // [K] bf16
+    const void* gate;       // bf16: [K], [M] or [M][K] by gate_kind
+    const void* w_pre;      // [K] bf16
+    int gate_kind;          // bfq_gate_kind
+    float res_scale, norm_eps;
+    int64_t M, K;
+    // forward
+    void* res_out;          // [M][K] as the residual
+    void* normed;           // [M][K] bf16
+    void* q;                // [M][K] codes
+    float* scales;
+    int64_t s_stride_m, s_stride_g;   // scale strides of a token and of a group (packed: word row)
+    int qtype, per_token, ue8m0, packed;
+    float q_eps;
+    // backward
+    const void* d_normed;   // [M][K] bf16
+    const void* d_res_out;  // [M][K] as the residual
+    void* d_res;            // [M][K] as the residual
+    void* d_y;              // [M][K] bf16
+    float* d_w_pre;         // [K]
+    float* d_w_post;        // [K]
+    void* d_gate;           // fp32 [K] or [M], bf16 [M][K]
+    int columns;            // a gradient summed over the rows is wanted:
+    float* partials;        // [norm_bwd_groups(M, K)][2][K]
+};
+hipError_t launch_norm_residual(const NormArgs& a, int res_f32, hipStream_t stream);
+int64_t norm_bwd_groups(int64_t M, int64_t K);
+hipError_t launch_norm_residual_bwd(const NormArgs& a, int res_f32, hipStream_t stream);
+
+// Gradient of a gated product at its pre-activations (csrc/gated.hip).
+struct GatedBwdArgs {
+    const void* pre;        // [M][2F] bf16: gate columns, then up columns
+    const void* dh;         // [M][F] bf16
+    void* dpre;             // [M][2F] bf16 or NULL
+    void* q;                // [M][2F] codes or NULL
+    float* scales;
+    void* h;                // [M][F] bf16 or NULL
+    int64_t M, F, s_stride_m, s_stride_g;
+    float c1, c3;           // the activation's constants (gated_activation)
+    int qtype, ue8m0, packed;
+    float q_eps;
+};
+hipError_t launch_gated_bwd(const GatedBwdArgs& a, hipStream_t stream);
+// Weight codes [N][K] and 128x128 block scales transposed to [K][N].
+hipError_t launch_transpose_weights(const void* w, const float* s, void* wt, float* st, int64_t N,
+                                    int64_t K, hipStream_t stream);
 
 // Arguments of one block-GEMM launch, shared by every kernel variant.
 struct GemmArgs {
@@ -78,6 +131,31 @@ inline int64_t moe_max_tiles(int64_t pairs, int64_t E, int64_t bm) {
 }
 
 typedef hipError_t (*GemmLaunchFn)(const GemmArgs& args, hipStream_t stream);
+
+// Arguments of a gated-product launch (csrc/gated.hip): N = F output columns, w = [2F][K] codes
+// (gate rows, then up rows), partials = fp32 [split][M][2F] when the tile does not finish its
+// outputs itself, else NULL.
+struct GatedArgs : GemmArgs {
+    float c1, c3;           // the activation g / (1 + exp(-g (c1 + c3 g^2)))
+    void* pre;              // [M][2F] bf16 pre-activations, or NULL
+    int otype;              // O_BF16 / O_FP16 / O_FP32, or O_CODES
+    float* out_scales;      // O_CODES: one scale per 128 outputs of a token
+    int64_t os_stride_m, os_stride_g;
+    int os_ue8m0, os_packed;
+    float os_eps;
+};
+typedef hipError_t (*GatedLaunchFn)(const GatedArgs& args, hipStream_t stream);
+// bfq_tile of a gated kernel: bn = output columns of a workgroup (2 * bn weight rows).
+struct GatedKernel {
+    bfq_tile tile;
+    int wlayout, sfmt;
+    GatedLaunchFn launch;
+};
+const GatedKernel* gated_kernels(int* count);
+// out (and pre) from the partials of `split` K ranges: sums in range order, activation, product.
+hipError_t launch_gated_reduce(const GatedArgs& a, hipStream_t stream);
+// The activation's constants.
+void gated_activation(int act, float* c1, float* c3);
 
 // A compiled kernel configuration. split_k, group_m and raster are launch arguments.
 struct KernelEntry {

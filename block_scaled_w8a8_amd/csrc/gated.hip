@@ -1,0 +1,462 @@
+// The gated product of a feed-forward block and its gradient.
+//
+// Forward: out[m][f] = act(g) * u with g = sum_k a[m][k] w[f][k] and u = sum_k a[m][k] w[F+f][k]
+// (block-scaled e4m3 operands, as the block GEMM), both products, the activation and the product
+// in one kernel: a workgroup takes the gate rows and the up rows of the same output columns, so a
+// lane's accumulators hold both factors of each of its outputs and the 2F-wide product is never
+// stored. The tile routines are the block GEMM's (gemm_std_tile.h, gemm_swapab_body.h).
+// Outputs are bf16 / fp16 / fp32, or e4m3 codes with one scale per 128 columns, which is what the
+// down projection's GEMM reads: a workgroup that covers 128 output columns holds whole groups.
+// A tile whose K range is split, or that covers less than a group when codes are wanted, writes
+// fp32 partials of the 2F-wide product instead and gated_reduce_kernel finishes them.
+//
+// What bounds the forward kernels is what bounds the block GEMM's: the weight stream at decode
+// sizes, the operand bytes through a CU's L1 and the scale step at large M.
+#include "activation.h"
+#include "gemm_std_tile.h"
+#include "gemm_swapab_body.h"
+#include "quant_device.h"
+
+namespace bfq {
+
+// out element type of four consecutive outputs, chosen at run time (uniform)
+__device__ __forceinline__ void store4_any(int otype, void* out, int64_t idx, const v4f& v) {
+    if (otype == O_BF16) store4<O_BF16>(out, idx, v);
+    else if (otype == O_FP16) store4<O_FP16>(out, idx, v);
+    else store4<O_FP32>(out, idx, v);
+}
+
+// One scale of group g of token m; packed: its byte of the word, and by the last group the zero
+// bytes after it.
+__device__ __forceinline__ void store_scale(float* scales, int64_t sm, int64_t sg, int packed,
+                                            int64_t m, int64_t g, int64_t groups, float s) {
+    if (!packed) {
+        scales[m * sm + g * sg] = s;
+        return;
+    }
+    uint8_t* word = reinterpret_cast<uint8_t*>(scales) + ((g >> 2) * sg + m) * 4;
+    word[g & 3] = (uint8_t)e8m0_of(s);
+    if (g == groups - 1)
+        for (int j = (int)(g & 3) + 1; j < 4; ++j) word[j] = 0;
+}
+
+// Stores of a tile whose lane holds, for sub-tile row sm, token row(sm) (or none, < 0) and output
+// columns n + 16*sn + 4*(lane/16) .. +3: gate in acc[sm][sn], up in acc[sm][sn + SG].
+template <int SM, int SG, typename RowFn>
+__device__ __forceinline__ void gated_partials(const GatedArgs& p, const v4f (&acc)[SM][2 * SG],
+                                               int64_t n, RowFn row) {
+    const int64_t F = p.N, base = (int64_t)blockIdx.z * p.M;
+#pragma unroll
+    for (int sm = 0; sm < SM; ++sm) {
+        const int64_t m = row(sm);
+        if (m < 0) continue;
+#pragma unroll
+        for (int sn = 0; sn < SG; ++sn) {
+            float* o = p.partials + (base + m) * 2 * F + n + sn * 16;
+            *reinterpret_cast<v4f*>(o) = acc[sm][sn];
+            *reinterpret_cast<v4f*>(o + F) = acc[sm][sn + SG];
+        }
+    }
+}
+
+// Pre-activations to p.pre and act(g) * u into acc[sm][0..SG).
+template <int SM, int SG, typename RowFn>
+__device__ __forceinline__ void gated_combine(const GatedArgs& p, v4f (&acc)[SM][2 * SG], int64_t n,
+                                              RowFn row) {
+    const int64_t F = p.N;
+#pragma unroll
+    for (int sm = 0; sm < SM; ++sm) {
+        const int64_t m = row(sm);
+#pragma unroll
+        for (int sn = 0; sn < SG; ++sn) {
+            if (p.pre && m >= 0) {
+                store4<O_BF16>(p.pre, m * 2 * F + n + sn * 16, acc[sm][sn]);
+                store4<O_BF16>(p.pre, m * 2 * F + F + n + sn * 16, acc[sm][sn + SG]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[sm][sn][i] = act_f32(acc[sm][sn][i], p.c1, p.c3) * acc[sm][sn + SG][i];
+        }
+    }
+}
+
+// Largest magnitudes (bits) of each token's outputs in this wave's columns, in every lane of the
+// token (lanes l, l + 16, l + 32, l + 48).
+template <int SM, int SG>
+__device__ __forceinline__ void gated_amax(const v4f (&acc)[SM][2 * SG], uint32_t (&mx)[SM]) {
+#pragma unroll
+    for (int sm = 0; sm < SM; ++sm) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int sn = 0; sn < SG; ++sn)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = max(m, abs_bits(acc[sm][sn][i]));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+        mx[sm] = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+    }
+}
+
+// Codes of a group's four outputs, given the group's largest magnitude and scale.
+__device__ __forceinline__ uint32_t codes4(const v4f& v, uint32_t mx, float s) {
+    const float x[8] = {v.x, v.y, v.z, v.w, 0.f, 0.f, 0.f, 0.f};
+    return encode8_group<Q_FP8>(x, mx, s).x;
+}
+
+// ---------------------------------------------------------------- standard tiles ----
+
+// One workgroup per (tile of BM tokens x BN / 2 output columns, K split).
+template <int BM, int BN, int WM, int WN, int SCHED, int WL>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_gated_std_kernel(GatedArgs p) {
+    using Shape = StdShape<BM, BN, WM, WN, SCHED>;
+    constexpr int TM = Shape::TM, SM = Shape::SM, SG = Shape::SN / 2, BNO = BN / 2, TNO = BNO / WN;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const int64_t M = p.M, F = p.N, KB = p.K / 128;
+    const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (F + BNO - 1) / BNO;
+    int64_t pid_m, pid_n;
+    tile_coords(blockIdx.x, tiles_m, tiles_n, p.group_m, p.raster, pid_m, pid_n);
+    const int64_t m0 = pid_m * BM, n0 = pid_n * BNO;
+    const int split = p.split, z = blockIdx.z;
+    typename Shape::AccT acc[SM][2 * SG];
+    std_tile<BM, BN, WM, WN, Q_FP8, SCHED, 2, WL, 0, 1>(p, lds, m0, n0, (int64_t)z * KB / split,
+                                                        (int64_t)(z + 1) * KB / split, acc);
+    const int lane = threadIdx.x & 63, frow = lane & 15, fgrp = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int64_t mw = m0 + wm * TM + frow, n = n0 + wn * TNO + 4 * fgrp;
+    auto row = [&](int sm) { return mw + sm * 16 < M ? mw + sm * 16 : (int64_t)-1; };
+    if (p.partials) {
+        gated_partials<SM, SG>(p, acc, n, row);
+        return;
+    }
+    gated_combine<SM, SG>(p, acc, n, row);
+    if (p.otype != O_CODES) {
+#pragma unroll
+        for (int sm = 0; sm < SM; ++sm) {
+            const int64_t m = row(sm);
+            if (m < 0) continue;
+#pragma unroll
+            for (int sn = 0; sn < SG; ++sn) store4_any(p.otype, p.out, m * F + n + sn * 16, acc[sm][sn]);
+        }
+        return;
+    }
+    if constexpr (BNO == 128) {
+        // the tile's 128 columns are one group: largest magnitudes over its WN waves through LDS
+        // (std_tile ends on a barrier), [wn][tile row]
+        uint32_t mx[SM];
+        gated_amax<SM, SG>(acc, mx);
+        uint32_t* red = reinterpret_cast<uint32_t*>(lds);
+        if (fgrp == 0)
+#pragma unroll
+            for (int sm = 0; sm < SM; ++sm) red[wn * BM + wm * TM + sm * 16 + frow] = mx[sm];
+        __syncthreads();
+        const int64_t g = n0 / 128, G = F / 128;
+#pragma unroll
+        for (int sm = 0; sm < SM; ++sm) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int w = 0; w < WN; ++w) m = max(m, red[w * BM + wm * TM + sm * 16 + frow]);
+            const float s = group_scale<Q_FP8>(m, p.os_eps, p.os_ue8m0);
+            const int64_t r = mw + sm * 16;
+            // packed words have rows up to a multiple of four tokens, zero past the last
+            if (wn == 0 && fgrp == 0 && r < (p.os_packed ? (M + 3) / 4 * 4 : M))
+                store_scale(p.out_scales, p.os_stride_m, p.os_stride_g, p.os_packed, r, g, G,
+                            r < M ? s : 0.f);
+            if (r >= M) continue;
+#pragma unroll
+            for (int sn = 0; sn < SG; ++sn)
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + r * F + n + sn * 16) =
+                    codes4(acc[sm][sn], m, s);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- swap-AB strips ----
+
+template <int MT, int NWO, int NWAVES, int SM, int SG, typename Args>
+__device__ __forceinline__ void gated_finish(const Args& p, v4f (&acc)[SM][2 * SG], int64_t m0,
+                                             int64_t n0, int64_t rows, int wn, int wk, int lane) {
+    const int frow = lane & 15, fgrp = lane >> 4;
+    const int64_t F = p.N, n = n0 + 4 * fgrp;
+    const bool mine = wk == 0 && n0 < F;     // the waves that hold the sums
+    auto row = [&](int sm) { return sm * 16 + frow < rows ? m0 + sm * 16 + frow : (int64_t)-1; };
+    if (p.partials) {
+        if (mine) gated_partials<SM, SG>(p, acc, n, row);
+        return;
+    }
+    if (mine) gated_combine<SM, SG>(p, acc, n, row);
+    if (p.otype != O_CODES) {
+        if (!mine) return;
+#pragma unroll
+        for (int sm = 0; sm < SM; ++sm) {
+            const int64_t m = row(sm);
+            if (m < 0) continue;
+#pragma unroll
+            for (int sn = 0; sn < SG; ++sn) store4_any(p.otype, p.out, m * F + n + sn * 16, acc[sm][sn]);
+        }
+        return;
+    }
+    if constexpr (NWAVES * NWO == 128) {
+        __shared__ uint32_t red[NWAVES][MT];
+        uint32_t mx[SM];
+        gated_amax<SM, SG>(acc, mx);
+        if (mine && fgrp == 0)
+#pragma unroll
+            for (int sm = 0; sm < SM; ++sm) red[wn][sm * 16 + frow] = mx[sm];
+        __syncthreads();
+        if (!mine) return;
+        const int64_t g = n0 / 128, G = F / 128;
+#pragma unroll
+        for (int sm = 0; sm < SM; ++sm) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int w = 0; w < NWAVES; ++w) m = max(m, red[w][sm * 16 + frow]);
+            const float s = group_scale<Q_FP8>(m, p.os_eps, p.os_ue8m0);
+            const int64_t r = m0 + sm * 16 + frow;
+            if (wn == 0 && fgrp == 0 && r < (p.os_packed ? (p.M + 3) / 4 * 4 : p.M))
+                store_scale(p.out_scales, p.os_stride_m, p.os_stride_g, p.os_packed, r, g, G,
+                            r < p.M ? s : 0.f);
+            if (r >= p.M) continue;
+#pragma unroll
+            for (int sn = 0; sn < SG; ++sn)
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + r * F + n + sn * 16) =
+                    codes4(acc[sm][sn], m, s);
+        }
+    }
+}
+
+template <int MT, int NWR, int NWAVES, int KW, int D, int WL, int CH>
+__global__ __launch_bounds__(64 * NWAVES * KW) void gemm_gated_swapab_kernel(GatedArgs p) {
+    swapab_body<MT, NWR, NWAVES, KW, D, Q_FP8, O_FP32, WL, CH, 0, 1>(p);
+}
+
+template <int MT, int NWR, int NWAVES, int KW, int D, int WL, int CH>
+__global__ __launch_bounds__(64 * NWAVES * KW) void gemm_gated_swapab_lds_kernel(GatedArgs p) {
+    swapab_lds_body<MT, NWR, NWAVES, KW, D, Q_FP8, O_FP32, WL, CH, 0, 1>(p);
+}
+
+// ---------------------------------------------------------------- reduce ----
+
+// Eight columns a thread: g and u summed over the K ranges in order, then as the epilogues above.
+// Groups of 128 columns are 16 lanes; the grid's rows past M (packed words only) write zeros.
+__global__ __launch_bounds__(256) void gated_reduce_kernel(GatedArgs p) {
+    const int lane = threadIdx.x & 63;
+    const int64_t m = blockIdx.x, F = p.N, c = (int64_t)blockIdx.y * 256 + threadIdx.x;
+    const bool live = c * 8 < F, real = m < p.M;
+    float h[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (live && real) {
+        const float* s = p.partials + m * 2 * F + c * 8;
+        v4f g0{}, g1{}, u0{}, u1{};
+        for (int z = 0; z < p.split; ++z, s += p.M * 2 * F) {
+            const v4f a = *reinterpret_cast<const v4f*>(s), b = *reinterpret_cast<const v4f*>(s + 4);
+            const v4f d = *reinterpret_cast<const v4f*>(s + F), e = *reinterpret_cast<const v4f*>(s + F + 4);
+            if (z == 0) { g0 = a; g1 = b; u0 = d; u1 = e; }
+            else { g0 += a; g1 += b; u0 += d; u1 += e; }
+        }
+        float g[8], u[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { g[i] = g0[i]; g[i + 4] = g1[i]; u[i] = u0[i]; u[i + 4] = u1[i]; }
+        if (p.pre) {
+            static_cast<uint4*>(p.pre)[(m * 2 * F) / 8 + c] = pack8(g);
+            static_cast<uint4*>(p.pre)[(m * 2 * F + F) / 8 + c] = pack8(u);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = act_f32(g[i], p.c1, p.c3) * u[i];
+    }
+    if (p.otype != O_CODES) {
+        if (live && real) {
+            store4_any(p.otype, p.out, m * F + c * 8, v4f{h[0], h[1], h[2], h[3]});
+            store4_any(p.otype, p.out, m * F + c * 8 + 4, v4f{h[4], h[5], h[6], h[7]});
+        }
+        return;
+    }
+    const uint32_t mx = max16(amax8(h));
+    const float s = group_scale<Q_FP8>(mx, p.os_eps, p.os_ue8m0);
+    if (!live) return;
+    if (real) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + m * F + c * 8) = encode8_group<Q_FP8>(h, mx, s);
+    if ((lane & 15) == 0)
+        store_scale(p.out_scales, p.os_stride_m, p.os_stride_g, p.os_packed, m, c >> 4, F / 128,
+                    real ? s : 0.f);
+}
+
+hipError_t launch_gated_reduce(const GatedArgs& a, hipStream_t stream) {
+    const int64_t rows = a.otype == O_CODES && a.os_packed ? (a.M + 3) / 4 * 4 : a.M;
+    hipLaunchKernelGGL(gated_reduce_kernel, dim3((unsigned)rows, (unsigned)((a.N / 8 + 255) / 256)),
+                       dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+void gated_activation(int act, float* c1, float* c3) {
+    const double t = 1.5957691216057307117597842397375;     // 2 sqrt(2 / pi)
+    *c1 = act == BFQ_ACT_SILU ? 1.f : (float)t;
+    *c3 = act == BFQ_ACT_SILU ? 0.f : (float)(0.044715 * t);
+}
+
+// ---------------------------------------------------------------- registry ----
+
+template <int BM, int BN, int WM, int WN, int SCHED, int WL>
+hipError_t launch_gated_std(const GatedArgs& a, hipStream_t stream) {
+    constexpr int LDS_BYTES = StdShape<BM, BN, WM, WN, SCHED>::lds_bytes(2);
+    const int64_t tiles = ((a.M + BM - 1) / BM) * ((a.N + BN / 2 - 1) / (BN / 2));
+    static bool attr_set = false;   // one-time opt-in to more than 64 KB of LDS
+    if (!attr_set) {
+        hipError_t e = hipFuncSetAttribute(
+            reinterpret_cast<const void*>(&gemm_gated_std_kernel<BM, BN, WM, WN, SCHED, WL>),
+            hipFuncAttributeMaxDynamicSharedMemorySize, LDS_BYTES);
+        if (e != hipSuccess) return e;
+        attr_set = true;
+    }
+    hipLaunchKernelGGL((gemm_gated_std_kernel<BM, BN, WM, WN, SCHED, WL>),
+                       dim3((unsigned)tiles, 1, (unsigned)a.split), dim3(64 * WM * WN), LDS_BYTES,
+                       stream, a);
+    return hipGetLastError();
+}
+
+template <int MT, int NWR, int NWAVES, int KW, int D, int WL, int CH, int LDS>
+hipError_t launch_gated_swapab(const GatedArgs& a, hipStream_t stream) {
+    const int64_t cols = NWR / 2 * NWAVES, strips = (a.N + cols - 1) / cols;
+    const dim3 grid((unsigned)strips, (unsigned)((a.M + MT - 1) / MT), (unsigned)a.split);
+    const dim3 block(64 * NWAVES * KW);
+    if constexpr (LDS)
+        hipLaunchKernelGGL((gemm_gated_swapab_lds_kernel<MT, NWR, NWAVES, KW, D, WL, CH>), grid,
+                           block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((gemm_gated_swapab_kernel<MT, NWR, NWAVES, KW, D, WL, CH>), grid, block,
+                           0, stream, a);
+    return hipGetLastError();
+}
+
+#define BFQ_GATED_STD(BM, BN, WM, WN, SC, WL)                                                   \
+    GatedKernel{bfq_tile{0, BM, (BN) / 2, 128, 1, WM, WN, 2, 8, SC, 0, 0}, WL,                  \
+                (SC) == 3 ? S_UE8M0 : S_FP32, &launch_gated_std<BM, BN, WM, WN, SC, WL>}
+#define BFQ_GATED_SAB(MT, NWR, NW, KW, D, WL, CH, L)                                            \
+    GatedKernel{bfq_tile{1, MT, (NWR) / 2 * (NW), 128, 1, KW, NW, D, 1, L, 0, 0}, WL,           \
+                (CH) == 2 ? S_PACKED : S_FP32, &launch_gated_swapab<MT, NWR, NW, KW, D, WL, CH, L>}
+#define BFQ_GATED_STD2(...) BFQ_GATED_STD(__VA_ARGS__, W_ROW), BFQ_GATED_STD(__VA_ARGS__, W_PACKED16)
+#define BFQ_GATED_SAB4(MT, NWR, NW, KW, D, L)                                                   \
+    BFQ_GATED_SAB(MT, NWR, NW, KW, D, W_ROW, 0, L), BFQ_GATED_SAB(MT, NWR, NW, KW, D, W_PACKED16, 0, L), \
+        BFQ_GATED_SAB(MT, NWR, NW, KW, D, W_ROW, 2, L), BFQ_GATED_SAB(MT, NWR, NW, KW, D, W_PACKED16, 2, L)
+
+static const GatedKernel kGatedKernels[] = {
+    BFQ_GATED_STD2(256, 256, 4, 2, 0),
+    BFQ_GATED_STD2(256, 256, 4, 2, 1),
+    BFQ_GATED_STD2(256, 256, 4, 2, 3),
+    BFQ_GATED_STD2(128, 256, 2, 2, 0),
+    BFQ_GATED_STD2(128, 256, 2, 2, 3),
+    BFQ_GATED_STD2(128, 128, 2, 2, 0),
+    BFQ_GATED_STD2(128, 128, 2, 2, 3),
+    BFQ_GATED_STD2(64, 128, 1, 2, 0),
+    BFQ_GATED_SAB4(16, 32, 1, 8, 4, 0),
+    BFQ_GATED_SAB4(16, 32, 1, 4, 4, 0),
+    BFQ_GATED_SAB4(16, 32, 8, 1, 4, 0),
+    BFQ_GATED_SAB4(16, 32, 8, 1, 4, 1),
+    BFQ_GATED_SAB4(32, 32, 8, 1, 4, 1),
+    BFQ_GATED_SAB4(32, 32, 4, 2, 4, 1),
+    BFQ_GATED_SAB4(64, 32, 8, 1, 4, 1),
+    BFQ_GATED_SAB4(64, 32, 4, 2, 4, 1),
+    BFQ_GATED_SAB4(128, 32, 8, 1, 4, 1),
+    BFQ_GATED_SAB4(128, 32, 4, 1, 4, 1),
+};
+
+const GatedKernel* gated_kernels(int* count) {
+    *count = (int)(sizeof(kGatedKernels) / sizeof(kGatedKernels[0]));
+    return kGatedKernels;
+}
+
+// ---------------------------------------------------------------- backward ----
+
+// With a = act(g): dg = dh * u * act'(g), du = dh * a, and the product h = a * u again. Eight
+// columns a thread, read once and written once (bytes bound it). Codes: 128-column groups of the
+// 2F-wide row, one scale each, 16 lanes a group; rows past M (packed words only) write zeros.
+template <int Q>
+__global__ __launch_bounds__(256) void gated_bwd_kernel(GatedBwdArgs p) {
+    const int lane = threadIdx.x & 63;
+    const int64_t m = blockIdx.x, F = p.F, c = (int64_t)blockIdx.y * 256 + threadIdx.x;
+    const bool live = c * 8 < F, real = m < p.M;
+    float dg[8], du[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dg[i] = du[i] = 0.f;
+    if (live && real) {
+        const uint4* pre = static_cast<const uint4*>(p.pre) + m * 2 * F / 8;
+        const uint4 gc = pre[c], uc = pre[F / 8 + c];
+        const uint4 dc = static_cast<const uint4*>(p.dh)[m * F / 8 + c];
+        float g[8], u[8], dh[8], h[8];
+        unpack8(gc, g);
+        unpack8(uc, u);
+        unpack8(dc, dh);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float slope;
+            const float a = act_slope_f32(g[i], p.c1, p.c3, slope);
+            h[i] = a * u[i];
+            dg[i] = dh[i] * u[i] * slope;
+            du[i] = dh[i] * a;
+        }
+        if (p.h) static_cast<uint4*>(p.h)[m * F / 8 + c] = pack8(h);
+        if (p.dpre) {
+            uint4* d = static_cast<uint4*>(p.dpre) + m * 2 * F / 8;
+            d[c] = pack8(dg);
+            d[F / 8 + c] = pack8(du);
+        }
+    }
+    if constexpr (Q >= 0) {
+        const uint32_t mg = max16(amax8(dg)), mu = max16(amax8(du));
+        if (!live) return;
+        const float sg = group_scale<Q>(mg, p.q_eps, p.ue8m0), su = group_scale<Q>(mu, p.q_eps, p.ue8m0);
+        if (real) {
+            uint2* q = static_cast<uint2*>(p.q) + m * 2 * F / 8;
+            q[c] = encode8_group<Q>(dg, mg, sg);
+            q[F / 8 + c] = encode8_group<Q>(du, mu, su);
+        }
+        if ((lane & 15) == 0) {
+            const int64_t G = 2 * F / 128, g = c >> 4;
+            store_scale(p.scales, p.s_stride_m, p.s_stride_g, p.packed, m, g, G, real ? sg : 0.f);
+            store_scale(p.scales, p.s_stride_m, p.s_stride_g, p.packed, m, F / 128 + g, G, real ? su : 0.f);
+        }
+    }
+}
+
+hipError_t launch_gated_bwd(const GatedBwdArgs& a, hipStream_t stream) {
+    const int64_t rows = a.q && a.packed ? (a.M + 3) / 4 * 4 : a.M;
+    const dim3 grid((unsigned)rows, (unsigned)((a.F / 8 + 255) / 256));
+    if (!a.q) hipLaunchKernelGGL(gated_bwd_kernel<-1>, grid, dim3(256), 0, stream, a);
+    else if (a.qtype == Q_FP8) hipLaunchKernelGGL(gated_bwd_kernel<Q_FP8>, grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL(gated_bwd_kernel<Q_INT8>, grid, dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+// Codes [N][K] and their 128x128 block scales to [K][N]: one 64 x 64 tile a workgroup through LDS,
+// 16-byte rows in and out; the first workgroup of a block moves its scale. An offline step.
+__global__ __launch_bounds__(256) void transpose_weights_kernel(const uint8_t* __restrict__ w,
+                                                                const float* __restrict__ s,
+                                                                uint8_t* __restrict__ wt,
+                                                                float* __restrict__ st, int64_t N,
+                                                                int64_t K) {
+    __shared__ uint8_t tile[64][64 + 4];
+    const int t = threadIdx.x, r = t >> 2, c = (t & 3) * 16;
+    const int64_t k0 = (int64_t)blockIdx.x * 64, n0 = (int64_t)blockIdx.y * 64;
+    const uint4 v = *reinterpret_cast<const uint4*>(w + (n0 + r) * K + k0 + c);
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(&tile[r][c + 4 * i]) = in[i];
+    __syncthreads();
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        out[i] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) out[i] |= (uint32_t)tile[c + 4 * i + j][r] << (8 * j);
+    }
+    *reinterpret_cast<uint4*>(wt + (k0 + r) * N + n0 + c) = make_uint4(out[0], out[1], out[2], out[3]);
+    if (t == 0 && ((blockIdx.x | blockIdx.y) & 1) == 0)
+        st[(k0 / 128) * (N / 128) + n0 / 128] = s[(n0 / 128) * (K / 128) + k0 / 128];
+}
+
+hipError_t launch_transpose_weights(const void* w, const float* s, void* wt, float* st, int64_t N,
+                                    int64_t K, hipStream_t stream) {
+    hipLaunchKernelGGL(transpose_weights_kernel, dim3((unsigned)(K / 64), (unsigned)(N / 64)),
+                       dim3(256), 0, stream, static_cast<const uint8_t*>(w), s,
+                       static_cast<uint8_t*>(wt), st, N, K);
+    return hipGetLastError();
+}
+
+}  // namespace bfq

@@ -21,6 +21,7 @@
 // makes a NaN anywhere in the group win the reduction, then reduced over the 16 lanes.
 #include "bfq_internal.h"
 #include "device_common.h"
+#include "quant_device.h"
 
 namespace bfq {
 
@@ -28,70 +29,6 @@ constexpr int kQuantWaves = 4;        // waves per workgroup
 constexpr int kQuantPasses = 2;       // 4-group passes per wave (loads issued together)
 constexpr int kGroupsPerWave = 4 * kQuantPasses;
 constexpr int kGroupsPerBlock = kQuantWaves * kGroupsPerWave;
-
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-    typedef unsigned short us2 __attribute__((ext_vector_type(2)));
-    us2 x = __builtin_bit_cast(us2, a), y = __builtin_bit_cast(us2, b);
-    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(x, y));
-}
-
-// Encode 8 values x[0..7] divided by scale s; finite-amax groups only (|x| <= amax of the
-// group or row that s was formed from). The quotient is taken as q = x * r with r = 1 / s,
-// one IEEE division per lane instead of one per value, then corrected once by the exact
-// remainder e = x - q * s (a fused multiply-add): q + e * r, with the sign of x (the
-// correction never changes the sign of a nonzero value; it restores -0, which q + e * r would
-// turn into +0). For every finite bf16 amax and every bf16 x with |x| <= amax, with fp32 or
-// power-of-two scales and either code type, the code of this value equals the code of the
-// IEEE quotient x / s (checked exhaustively on the CPU: tests/native/quotient_codes.c); where
-// the two fp32 values differ at all (subnormal x in a group whose amax is below eps) both
-// encode to zero. (r names the return value below; rs is the reciprocal.)
-template <int QT>
-__device__ __forceinline__ uint2 encode8(const float* x, float s) {
-    const float rs = 1.0f / s;                         // IEEE division, once per lane
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float q = x[i] * rs;
-        const float e = __builtin_fmaf(-q, s, x[i]);   // exact
-        y[i] = __builtin_copysignf(__builtin_fmaf(e, rs, q), x[i]);
-    }
-    uint2 r;
-    if constexpr (QT == Q_FP8) {
-        r.x = enc_fp8x4(y[0], y[1], y[2], y[3]);
-        r.y = enc_fp8x4(y[4], y[5], y[6], y[7]);
-    } else {
-        r.x = enc_i8x4(y[0], y[1], y[2], y[3]);
-        r.y = enc_i8x4(y[4], y[5], y[6], y[7]);
-    }
-    return r;
-}
-
-// Groups whose amax is Inf or NaN. NaN amax: every code is NaN (0x7F) / 0 (int8).
-// Inf amax: the scale is Inf, finite values divide to a signed zero, +-Inf to NaN.
-template <int QT>
-__device__ __forceinline__ uint2 encode8_special(const float* x, bool nan_group) {
-    uint32_t b[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t code;
-        if (nan_group || __builtin_isinf(x[i])) code = (QT == Q_FP8) ? 0x7Fu : 0u;
-        else code = (QT == Q_FP8) ? ((__float_as_uint(x[i]) >> 24) & 0x80u) : 0u;
-        b[i] = code;
-    }
-    uint2 r;
-    r.x = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
-    r.y = b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24);
-    return r;
-}
-
-// UE8M0 scale format ([BENCH] §4.1, use_ue8m0): the smallest power of two >= s, for a
-// positive normal fp32 s (s >= eps / Qmax keeps it normal; s <= FLT_MAX / 127 keeps the
-// next power finite). A power of two stays; otherwise the mantissa is cleared and the
-// exponent stepped up by one.
-__device__ __forceinline__ float pow2_ceil(float s) {
-    const uint32_t u = __float_as_uint(s);
-    return (u & 0x007FFFFFu) ? __uint_as_float((u & 0xFF800000u) + 0x00800000u) : s;
-}
 
 // packed != 0 (BFQ_SCALES_PACKED_UE8M0, UE8M0 scales): instead of one fp32 per group, the
 // E8M0 codes of groups 4w .. 4w+3 go to one 32-bit word at words[w * s_stride_g + m]. A

@@ -107,6 +107,26 @@ typedef enum {
     BFQ_SCALE_INT32_RANGE_ = 0x7FFFFFFF
 } bfq_scale_format;
 
+/* Activation of a gated product, act(g) * u. SILU: g / (1 + exp(-g)). GELU_TANH: the tanh form,
+ * 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))). */
+typedef enum {
+    BFQ_ACT_SILU = 0,
+    BFQ_ACT_GELU_TANH = 1,
+    BFQ_ACT_INT32_MIN_ = -0x7FFFFFFF - 1,   /* every int32 is representable, as above */
+    BFQ_ACT_INT32_RANGE_ = 0x7FFFFFFF
+} bfq_activation;
+
+/* What one value of a block's gate covers: nothing (no gate), a channel ([K]), a token ([M]) or
+ * one element ([M][K]). */
+typedef enum {
+    BFQ_GATE_NONE = 0,
+    BFQ_GATE_CHANNEL = 1,
+    BFQ_GATE_TOKEN = 2,
+    BFQ_GATE_FULL = 3,
+    BFQ_GATE_INT32_MIN_ = -0x7FFFFFFF - 1,
+    BFQ_GATE_INT32_RANGE_ = 0x7FFFFFFF
+} bfq_gate_kind;
+
 /* One launch configuration of the block GEMM ([CONFIG] §2: per-M launch parameters).
  *   variant 0 "standard": bm x bn output tile per workgroup, A and W tiles staged through
  *             LDS (double-buffered), waves_m x waves_n waves, group_m = grouped tile order.
@@ -324,6 +344,114 @@ bfq_status bfq_moe_block_gemm(const void* a_q, const float* a_scales, bfq_scale_
 int32_t    bfq_moe_num_tile_candidates(bfq_weight_layout w_layout, bfq_scale_format scale_fmt);
 bfq_status bfq_moe_get_tile_candidate(bfq_weight_layout w_layout, bfq_scale_format scale_fmt,
                                       int32_t index, bfq_tile* tile_out);
+
+/* --------------------------------------------- feed-forward blocks: gated product ----
+ * The operators between the GEMMs of a feed-forward block y = (act(x Wg^T) * (x Wu^T)) Wd^T:
+ * bfq_norm_residual gives the codes of x, bfq_gated_gemm both projections with the activation and
+ * the product (as the codes that the down projection's bfq_block_gemm reads), bfq_norm_residual
+ * adds the block's output to the residual stream. Backward: the gradient of the down projection's
+ * input is bfq_block_gemm of the quantized gradient with the transposed weights
+ * (bfq_transpose_weights), bfq_gated_backward carries it to the pre-activations, and another
+ * bfq_block_gemm to x. The weights are codes: no gradient of theirs is defined. */
+
+/* Gated product: for each token m and column f < F
+ *   g = sum_k a[m][k] w[f][k],  u = sum_k a[m][k] w[F + f][k],  out[m][f] = act(g) * u
+ * with both sums as bfq_block_gemm forms them (e4m3fn codes, block_shape {128, 128}) and kept in
+ * fp32 until out is rounded once. w_q holds 2F rows, the gate projection's and then the up
+ * projection's (row-major, or the 2F x K matrix packed by bfq_pack_weights); w_scales
+ * [2F/128][K/128].
+ *   out_dtype BF16 | FP16 | FP32: out [M][F]. out_dtype BFQ_E4M3FN: out [M][F] codes and
+ *   out_scales, one per 128 columns of a token, in out_layout / out_scale_ld and scale_fmt with
+ *   floor out_eps: the token quantizer's formats, formed from the fp32 products (out_scales,
+ *   out_layout, out_scale_ld and out_eps are not read otherwise).
+ *   preact: bf16 [M][2F] = (g, u), what bfq_gated_backward reads, or NULL.
+ * M >= 0, F and K positive multiples of 128; the limits of bfq_block_gemm with N = 2F, and
+ * F * K < 2^40. tile NULL -> bfq_gated_select_tile. The workspace holds
+ * bfq_gated_gemm_workspace_bytes bytes (NULL when that is 0). */
+bfq_status bfq_gated_gemm(const void* a_q, const float* a_scales, bfq_scale_layout a_layout,
+                          int64_t a_scale_ld, const void* w_q, const float* w_scales,
+                          bfq_weight_layout w_layout, bfq_scale_format scale_fmt,
+                          bfq_activation act, void* out, float* out_scales,
+                          bfq_scale_layout out_layout, int64_t out_scale_ld, float out_eps,
+                          void* preact, int64_t M, int64_t F, int64_t K,
+                          const int32_t block_shape[2] /* host */, bfq_dtype in_dtype,
+                          bfq_dtype out_dtype, const bfq_tile* tile /* host */, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* The tile that bfq_gated_gemm takes: a rule on M, F, K, the layout, the scale format and whether
+ * codes are wanted (bn counts output columns: 2 * bn weight rows). Batch-invariant mode applies
+ * as in bfq_select_tile. */
+bfq_status bfq_gated_select_tile(int64_t M, int64_t F, int64_t K, bfq_dtype out_dtype,
+                                 bfq_weight_layout w_layout, bfq_scale_format scale_fmt,
+                                 bfq_tile* tile_out);
+/* split_k * M * 2F * 4 bytes when the tile's split_k > 1, or when codes are wanted and the tile's
+ * bn is not 128; else 0. tile NULL -> the selected one. SIZE_MAX for shapes bfq_gated_gemm
+ * rejects as too large. */
+size_t     bfq_gated_gemm_workspace_bytes(int64_t M, int64_t F, int64_t K, bfq_dtype out_dtype,
+                                          bfq_weight_layout w_layout, bfq_scale_format scale_fmt,
+                                          const bfq_tile* tile);
+/* Compiled gated kernels usable for (w_layout, scale_fmt) (split_k = 1). */
+int32_t    bfq_gated_num_tile_candidates(bfq_weight_layout w_layout, bfq_scale_format scale_fmt);
+bfq_status bfq_gated_get_tile_candidate(bfq_weight_layout w_layout, bfq_scale_format scale_fmt,
+                                        int32_t index, bfq_tile* tile_out);
+
+/* Gradient of h = act(g) * u at (g, u), from the pre-activations that bfq_gated_gemm kept and the
+ * gradient dh of h: dg = dh * u * act'(g), du = dh * act(g), in fp32.
+ *   preact bf16 [M][2F]; dh bf16 [M][F]. At least one output, the others NULL:
+ *   dpre bf16 [M][2F] = (dg, du); q [M][2F] codes with scales, one per 128 columns (the gradient
+ *   as the next bfq_block_gemm reads it; layout, scale_ld, q_eps, scale_fmt as in
+ *   bfq_quant_tokens with K = 2F, quantized from the fp32 values); h bf16 [M][F], the product
+ *   again. F a positive multiple of 8, of 128 with q. q_dtype is read only with q. */
+bfq_status bfq_gated_backward(const void* preact, const void* dh, bfq_activation act, void* dpre,
+                              void* q, bfq_dtype q_dtype, float* scales, bfq_scale_layout layout,
+                              int64_t scale_ld, float q_eps, bfq_scale_format scale_fmt, void* h,
+                              int64_t M, int64_t F, void* stream);
+
+/* Row-major weight codes [N][K] and their block scales [N/128][K/128] transposed: wt_q [K][N],
+ * wt_scales [K/128][N/128]. An offline step like bfq_pack_weights (which may follow it); separate
+ * buffers. N, K multiples of 128. */
+bfq_status bfq_transpose_weights(const void* w_q, const float* w_scales, int64_t N, int64_t K,
+                                 bfq_dtype q_dtype, void* wt_q, float* wt_scales, void* stream);
+
+/* ----------------------------------------------- feed-forward blocks: norms, residual ----
+ * One step of the residual stream, per token row of K channels, in fp32:
+ *   z  = w_post ? y * rms(y) * w_post : y        rms(x) = 1 / sqrt(mean(x^2) + norm_eps)
+ *   r' = residual + res_scale * gate * z
+ *   n  = r' * rms(r') * w_pre
+ *   residual [M][K] of res_dtype BF16 | FP32. y bf16 [M][K], or NULL: r' = residual (w_post, gate
+ *   and res_out must then be NULL). gate bf16: [K] (CHANNEL), [M] (TOKEN), [M][K] (FULL) or NULL
+ *   (NONE); w_post, w_pre bf16 [K] or NULL.
+ *   res_out [M][K] of res_dtype receives r' (may be `residual` itself).
+ *   With w_pre, n is stored as normed bf16 [M][K], as codes q [M][K] with scales (the formats of
+ *   bfq_quant_tokens: group_size 128 or K, q_dtype E4M3FN | INT8), or both; both are formed from
+ *   the fp32 n, and n from the fp32 r'. Without w_pre, normed and q must be NULL.
+ * K a positive multiple of 8 (of 128 with q), at most 16384; norm_eps positive and finite. Row
+ * sums of squares are fp32: values past about 1e17 overflow them. */
+bfq_status bfq_norm_residual(const void* y, const void* residual, bfq_dtype res_dtype,
+                             const void* w_post, const void* gate, bfq_gate_kind gate_kind,
+                             float res_scale, const void* w_pre, float norm_eps, void* res_out,
+                             void* normed, void* q, bfq_dtype q_dtype, int32_t group_size,
+                             float* scales, bfq_scale_layout layout, int64_t scale_ld, float q_eps,
+                             bfq_scale_format scale_fmt, int64_t M, int64_t K, void* stream);
+
+/* Gradients of bfq_norm_residual. res_out is the stored r' (without y: the residual itself);
+ * d_normed bf16 [M][K] the gradient at n (with w_pre, else NULL), d_res_out [M][K] of res_dtype
+ * the one that reaches r' along the stream, or NULL for zero. Outputs:
+ *   d_res [M][K] of res_dtype, the gradient of `residual` (may be d_res_out itself);
+ *   d_y bf16 [M][K] with y, else NULL;
+ *   d_w_pre, d_w_post fp32 [K], and d_gate (CHANNEL fp32 [K], TOKEN fp32 [M], FULL bf16 [M][K]):
+ *   any may be NULL when it is not wanted, and must be when its operand is absent. They are
+ *   overwritten, not added to; with M = 0 the column sums become zero.
+ * Sums are fp32 in a fixed order: equal calls give equal bits. workspace of
+ * bfq_norm_residual_backward_workspace_bytes bytes when a [K] gradient is wanted, else NULL. */
+size_t     bfq_norm_residual_backward_workspace_bytes(int64_t M, int64_t K);
+bfq_status bfq_norm_residual_backward(const void* y, const void* res_out, bfq_dtype res_dtype,
+                                      const void* w_post, const void* gate,
+                                      bfq_gate_kind gate_kind, float res_scale, const void* w_pre,
+                                      float norm_eps, const void* d_normed, const void* d_res_out,
+                                      void* d_res, void* d_y, float* d_w_pre, float* d_w_post,
+                                      void* d_gate, int64_t M, int64_t K, void* workspace,
+                                      size_t workspace_bytes, void* stream);
 
 const char* bfq_status_string(bfq_status s);
 const char* bfq_last_error(void);
