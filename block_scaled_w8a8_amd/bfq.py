@@ -195,15 +195,16 @@ def _check(status: int, where: str, warn_key=None) -> int:
     return status
 
 
+_BLOCK_128 = (ctypes.c_int32 * 2)(*BLOCK_SHAPE)      # read only by the library
+
+
 def _block_shape(block_shape=BLOCK_SHAPE):
-    return (ctypes.c_int32 * 2)(*block_shape)
+    return _BLOCK_128 if block_shape is BLOCK_SHAPE else (ctypes.c_int32 * 2)(*block_shape)
 
 
 def _ptr(t) -> int:
     """Device address of a tensor (or an int address / None)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
@@ -224,15 +225,29 @@ class BfqArgumentError(ValueError):
 U8_CODES = ("uint8", "float8_e4m3fn")
 
 
+_torch = None          # torch, once a tensor has been seen (importing the binding does not need it)
+_DTYPE_NAMES: dict = {}
+
+
+def _torch_module():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _dt(t) -> str:
-    return str(t.dtype).replace("torch.", "")
+    name = _DTYPE_NAMES.get(t.dtype)
+    if name is None:
+        name = _DTYPE_NAMES[t.dtype] = str(t.dtype).replace("torch.", "")
+    return name
 
 
 def _tensor(t, name, dtypes):
     if isinstance(t, int):
         return False
-    import torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, (_torch or _torch_module()).Tensor):
         raise BfqArgumentError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if _dt(t) not in dtypes:
         raise BfqArgumentError(f"{name} has dtype {_dt(t)}; expected one of {', '.join(dtypes)}")
@@ -241,27 +256,26 @@ def _tensor(t, name, dtypes):
 
 def _devices(**tensors):
     """Last check of a wrapper: every tensor argument is on the current GPU."""
+    cur = None
     for name, t in tensors.items():
         if t is not None and not isinstance(t, int):
-            _on_device(t, name)
-
-
-def _on_device(t, name):
-    import torch
-    if not t.is_cuda:
-        raise BfqArgumentError(f"{name} is on device {t.device}; the kernels need a GPU tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise BfqArgumentError(f"{name} is on {t.device}, not the current device "
-                               f"cuda:{torch.cuda.current_device()}")
+            if t.get_device() < 0:
+                raise BfqArgumentError(f"{name} is on device {t.device}; the kernels need a GPU tensor")
+            if cur is None:
+                cur = (_torch or _torch_module()).cuda.current_device()
+            if t.get_device() != cur:
+                raise BfqArgumentError(f"{name} is on {t.device}, not the current device cuda:{cur}")
 
 
 def _rows(t, name, dtypes, rows, cols):
     """A [rows, cols] matrix whose rows are packed at stride cols (what the kernels index)."""
     if not _tensor(t, name, dtypes):
         return
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
-        raise BfqArgumentError(f"{name} has shape {tuple(t.shape)}; expected ({rows}, {cols})")
-    if rows > 0 and cols > 0 and (t.stride(1) != 1 or (rows > 1 and t.stride(0) != cols)):
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
+        raise BfqArgumentError(f"{name} has shape {tuple(shape)}; expected ({rows}, {cols})")
+    if not t.is_contiguous() and rows > 0 and cols > 0 and (
+            t.stride(1) != 1 or (rows > 1 and t.stride(0) != cols)):
         raise BfqArgumentError(f"{name} has strides {t.stride()}; its rows must be contiguous "
                                f"at stride {cols} (call .contiguous())")
 
@@ -290,22 +304,22 @@ def _scales(t, name, layout, ld, m, groups, write):
         if not _tensor(t, name, ("float32",)):
             return
         need = (m, groups) if layout == BFQ_SCALES_ROW_MAJOR else (groups, m)
-    if t.dim() != 2:
-        raise BfqArgumentError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
-    if t.shape[0] < need[0] or t.shape[1] < need[1]:
-        raise BfqArgumentError(f"{name} has shape {tuple(t.shape)}; the layout needs at least "
+    shape = t.shape
+    if len(shape) != 2:
+        raise BfqArgumentError(f"{name} must be 2-D, got shape {tuple(shape)}")
+    if shape[0] < need[0] or shape[1] < need[1]:
+        raise BfqArgumentError(f"{name} has shape {tuple(shape)}; the layout needs at least "
                                f"{need}")
-    if t.shape[0] > 1 and t.stride(0) != ld:
+    if shape[0] > 1 and t.stride(0) != ld:
         raise BfqArgumentError(f"{name} has row stride {t.stride(0)} but scale_ld is {ld}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if shape[1] > 1 and t.stride(1) != 1:
         raise BfqArgumentError(f"{name} must have unit stride along its second dimension")
 
 
 def _workspace(t, nbytes):
     if t is None or isinstance(t, int):
         return
-    import torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, (_torch or _torch_module()).Tensor):
         raise BfqArgumentError("workspace must be a torch.Tensor")
     if t.numel() * t.element_size() < nbytes or not t.is_contiguous():
         raise BfqArgumentError(f"workspace holds {t.numel() * t.element_size()} bytes "
@@ -317,9 +331,10 @@ OUT_DTYPES = ("bfloat16", "float16", "float32")
 
 
 def _shape2(t, name):
-    if not hasattr(t, "dim") or t.dim() != 2:
+    shape = getattr(t, "shape", ())
+    if not hasattr(t, "dim") or len(shape) != 2:
         raise BfqArgumentError(f"{name} must be a 2-D tensor")
-    return int(t.shape[0]), int(t.shape[1])
+    return int(shape[0]), int(shape[1])
 
 
 def _same_codes(a, w):
@@ -332,23 +347,25 @@ def _same_codes(a, w):
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        cuda = (_torch or _torch_module()).cuda
+        raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)   # the handle without a Stream object
+        return raw(cuda.current_device()) if raw else cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+_CODE_TYPES = {"uint8": BFQ_E4M3FN, "float8_e4m3fn": BFQ_E4M3FN, "int8": BFQ_INT8}
+_OUT_TYPES = {"bfloat16": BFQ_BF16, "float16": BFQ_FP16, "float32": BFQ_FP32}
+
+
 def _qdtype(t) -> int:
-    import torch
-    if t.dtype in (torch.uint8, torch.float8_e4m3fn):
-        return BFQ_E4M3FN
-    if t.dtype == torch.int8:
-        return BFQ_INT8
-    raise BfqArgumentError(f"code tensor dtype {t.dtype} is neither e4m3fn/uint8 nor int8")
+    q = _CODE_TYPES.get(_dt(t))
+    if q is None:
+        raise BfqArgumentError(f"code tensor dtype {t.dtype} is neither e4m3fn/uint8 nor int8")
+    return q
 
 
 def _odtype(t) -> int:
-    import torch
-    return {torch.bfloat16: BFQ_BF16, torch.float16: BFQ_FP16, torch.float32: BFQ_FP32}[t.dtype]
+    return _OUT_TYPES[_dt(t)]
 
 
 # ----------------------------------------------------------------------- entry points

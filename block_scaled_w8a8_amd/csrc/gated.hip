@@ -86,11 +86,12 @@ template <int SM, int SG>
 __device__ __forceinline__ void gated_amax(const v4f (&acc)[SM][2 * SG], uint32_t (&mx)[SM]) {
 #pragma unroll
     for (int sm = 0; sm < SM; ++sm) {
-        uint32_t m = 0;
+        float a = 0.f;
 #pragma unroll
         for (int sn = 0; sn < SG; ++sn)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m = max(m, abs_bits(acc[sm][sn][i]));
+            for (int i = 0; i < 4; ++i) a = max_abs(a, acc[sm][sn][i]);
+        uint32_t m = __float_as_uint(a) & 0x7FFFFFFFu;
         m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
         mx[sm] = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
     }

@@ -15,156 +15,197 @@
 
 namespace bfq {
 
-// Eight values of the residual stream: one 16-byte chunk of bf16 or two of fp32.
+// Row tensors go through buffer resources over one row: a lane past the row's end, and every lane
+// of an operand that is absent, reads zero and stores nothing, so the row code has no branches and
+// its loads stay in flight until they are used.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void* p, int64_t m, uint32_t bytes) {
+    const uint8_t* base = static_cast<const uint8_t*>(p) + (p ? m * bytes : 0);
+    return make_rsrc(base, p ? bytes : 0);
+}
+__device__ __forceinline__ v4u load16(__amdgpu_buffer_rsrc_t r, uint32_t voff) {
+    return __builtin_amdgcn_raw_buffer_load_b128(r, voff, 0, 0);
+}
+__device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t r, uint32_t voff, const v4u& v) {
+    __builtin_amdgcn_raw_buffer_store_b128(v, r, voff, 0, 0);
+}
+__device__ __forceinline__ void unpack(const v4u& v, float* x) {
+    unpack8(make_uint4(v.x, v.y, v.z, v.w), x);
+}
+__device__ __forceinline__ v4u pack(const float* x) {
+    return v4u{pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])};
+}
+
+// Eight values of the residual stream at byte offset voff of a bf16 row (twice that of fp32).
 template <int F32> struct Chunk;
 template <> struct Chunk<0> {
-    uint4 v;
-    __device__ __forceinline__ void load(const void* p, int64_t i) { v = static_cast<const uint4*>(p)[i]; }
-    __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float* x) const { unpack8(v, x); }
-    static __device__ __forceinline__ void store(void* p, int64_t i, const float* x) {
-        static_cast<uint4*>(p)[i] = pack8(x);
+    v4u v;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t voff) { v = load16(r, voff); }
+    __device__ __forceinline__ void get(float* x) const { unpack(v, x); }
+    static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t voff, const float* x) {
+        store16(r, voff, pack(x));
     }
 };
 template <> struct Chunk<1> {
     v4f a, b;
-    __device__ __forceinline__ void load(const void* p, int64_t i) {
-        a = static_cast<const v4f*>(p)[2 * i];
-        b = static_cast<const v4f*>(p)[2 * i + 1];
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t voff) {
+        a = buf_load_v4f(r, 2 * voff, 0);
+        b = buf_load_v4f(r, 2 * voff, 16);
     }
-    __device__ __forceinline__ void clear() { a = b = v4f{0.f, 0.f, 0.f, 0.f}; }
     __device__ __forceinline__ void get(float* x) const {
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
         x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     }
-    static __device__ __forceinline__ void store(void* p, int64_t i, const float* x) {
-        static_cast<v4f*>(p)[2 * i] = v4f{x[0], x[1], x[2], x[3]};
-        static_cast<v4f*>(p)[2 * i + 1] = v4f{x[4], x[5], x[6], x[7]};
+    static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t voff, const float* x) {
+        buf_store_v4f(r, v4f{x[0], x[1], x[2], x[3]}, 2 * voff, 0);
+        buf_store_v4f(r, v4f{x[4], x[5], x[6], x[7]}, 2 * voff, 16);
     }
 };
 
-// The gate of 8 elements of row m (chunk c), times alpha.
-__device__ __forceinline__ void gate8(const NormArgs& p, int64_t m, int64_t c, int64_t chunks,
-                                      float* g) {
-    if (p.gate_kind == BFQ_GATE_CHANNEL || p.gate_kind == BFQ_GATE_FULL) {
-        unpack8(static_cast<const uint4*>(p.gate)[(p.gate_kind == BFQ_GATE_FULL ? m * chunks : 0) + c], g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] *= p.res_scale;
-    } else {
-        float a = p.res_scale;
-        if (p.gate_kind == BFQ_GATE_TOKEN)
-            a *= __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.gate)[m] << 16);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = a;
-    }
+// An absent vector operand (zeros from its empty resource) as bf16 ones.
+__device__ __forceinline__ v4u ones_unless(const v4u& v, bool present) {
+    const uint32_t o = present ? 0u : 0x3F803F80u;
+    return v4u{v.x | o, v.y | o, v.z | o, v.w | o};
 }
 
-// Q: -1 no codes, else Q_FP8 / Q_INT8. Rows M .. (packed scale words: up to a multiple of 4)
-// exist only to write zero words.
-template <int T, int P, int RF32, int Q>
-__global__ __launch_bounds__(T) void norm_residual_kernel(NormArgs p) {
-    const int t = threadIdx.x, lane = t & 63;
-    const int64_t m = blockIdx.x, K = p.K, chunks = K / 8;
-    __shared__ float red[2][T / 64];
-    __shared__ uint32_t redmax[T / 64];
+// alpha, times the row's gate value if there is one a token.
+__device__ __forceinline__ float row_scale(const NormArgs& p, int64_t m) {
+    if (p.gate_kind != BFQ_GATE_TOKEN) return p.res_scale;
+    return p.res_scale * __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.gate)[m] << 16);
+}
+
+__device__ __forceinline__ float rms_of(float sum_sq, float K, float eps) {
+    return 1.0f / __builtin_sqrtf(sum_sq / K + eps);
+}
+
+// Most threads of a workgroup that keeps P chunks a thread (K <= kNormMaxK = 8 * 2048).
+template <int P> constexpr int kNormThreads = P == 4 ? 512 : 1024;
+
+// One row a workgroup. Q: -1 no codes, else Q_FP8 / Q_INT8. Rows M .. (packed scale words: up to a
+// multiple of 4) exist only to write zero words.
+template <int P, int RF32, int Q>
+__global__ __launch_bounds__(kNormThreads<P>) void norm_residual_kernel(NormArgs p) {
+    const int t = threadIdx.x, lane = t & 63, T = blockDim.x;
+    const int64_t m = blockIdx.x, K = p.K;
+    const uint32_t row16 = (uint32_t)(2 * K), row_res = RF32 ? 2 * row16 : row16;   // bytes of a row
+    const float fK = (float)K;
+    __shared__ __attribute__((aligned(16))) float red[2][16];
+    __shared__ uint32_t redmax[16];
     if constexpr (Q >= 0) {
         if (m >= p.M) {                                   // uniform: a padding row of packed words
             for (int64_t w = t; w < (K / 128 + 3) / 4; w += T) p.scales[w * p.s_stride_g + m] = 0.f;
             return;
         }
     }
-    float r[P][8];
+    block_sum_init(red[0], 32);
+    const bool channel = p.gate_kind == BFQ_GATE_CHANNEL, elements = p.gate_kind == BFQ_GATE_FULL;
+    const __amdgpu_buffer_rsrc_t r_res = row_rsrc(p.residual, m, row_res), r_y = row_rsrc(p.y, m, row16),
+                                 r_gate = row_rsrc(channel || elements ? p.gate : nullptr,
+                                                   elements ? m : 0, row16),
+                                 r_post = row_rsrc(p.w_post, 0, row16), r_pre = row_rsrc(p.w_pre, 0, row16),
+                                 r_out = row_rsrc(p.res_out, m, row_res), r_n = row_rsrc(p.normed, m, row16);
+    // P = 1 (few rows): every load up front, one trip to memory. Else the channel vectors, which
+    // hit L2, come only when they are needed: fewer registers, more rows in flight on a CU.
+    uint32_t voff[P];
     Chunk<RF32> rc[P];
-    uint4 yc[P];
+    v4u yc[P], gc[P], wpost[P], wpre[P];
 #pragma unroll
     for (int u = 0; u < P; ++u) {
-        const int64_t c = (int64_t)u * T + t;
-        rc[u].clear();
-        yc[u] = make_uint4(0, 0, 0, 0);
-        if (c < chunks) {
-            rc[u].load(p.residual, m * chunks + c);
-            if (p.y) yc[u] = static_cast<const uint4*>(p.y)[m * chunks + c];
-        }
+        voff[u] = (uint32_t)(u * T + t) * 16;
+        yc[u] = load16(r_y, voff[u]);
+        rc[u].load(r_res, voff[u]);
     }
-    float iy = 1.f;
+    auto load_post = [&]() {
+#pragma unroll
+        for (int u = 0; u < P; ++u) {
+            wpost[u] = load16(r_post, voff[u]);
+            gc[u] = load16(r_gate, voff[u]);
+        }
+    };
+    auto load_pre = [&]() {
+#pragma unroll
+        for (int u = 0; u < P; ++u) wpre[u] = load16(r_pre, voff[u]);
+    };
+    if constexpr (P == 1) {
+        load_post();
+        load_pre();
+    }
+    float c = row_scale(p, m);
     if (p.w_post) {
         float s[1] = {0.f};
 #pragma unroll
         for (int u = 0; u < P; ++u) {
             float y[8];
-            unpack8(yc[u], y);
+            unpack(yc[u], y);
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[0] = __builtin_fmaf(y[i], y[i], s[0]);
         }
-        block_sum<T, 1>(s, red[0]);
-        iy = 1.0f / __builtin_sqrtf(s[0] / (float)K + p.norm_eps);
+        block_sum<1>(s, red[0]);
+        c *= rms_of(s[0], fK, p.norm_eps);
     }
+    if constexpr (P > 1) {
+        __builtin_amdgcn_sched_barrier(0);
+        load_post();
+    }
+    float r[P][8], s[1] = {0.f};
 #pragma unroll
     for (int u = 0; u < P; ++u) {
-        const int64_t c = (int64_t)u * T + t;
+        float y[8], g[8], w[8];
         rc[u].get(r[u]);
-        if (p.y && c < chunks) {
-            float y[8], g[8];
-            unpack8(yc[u], y);
-            gate8(p, m, c, chunks, g);
-            if (p.w_post) {
-                float w[8];
-                unpack8(static_cast<const uint4*>(p.w_post)[c], w);
+        unpack(yc[u], y);
+        unpack(ones_unless(gc[u], channel || elements), g);
+        unpack(ones_unless(wpost[u], p.w_post != nullptr), w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = y[i] * iy * w[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[u][i] = __builtin_fmaf(g[i], y[i], r[u][i]);
-            Chunk<RF32>::store(p.res_out, m * chunks + c, r[u]);
+        for (int i = 0; i < 8; ++i) {
+            r[u][i] = __builtin_fmaf(y[i] * c * w[i], g[i], r[u][i]);
+            s[0] = __builtin_fmaf(r[u][i], r[u][i], s[0]);
         }
+        Chunk<RF32>::store(r_out, voff[u], r[u]);
     }
     if (!p.w_pre) return;                                 // uniform
-
-    float s[1] = {0.f};
-#pragma unroll
-    for (int u = 0; u < P; ++u)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] = __builtin_fmaf(r[u][i], r[u][i], s[0]);
-    block_sum<T, 1>(s, red[1]);
-    const float ir = 1.0f / __builtin_sqrtf(s[0] / (float)K + p.norm_eps);
-    uint32_t rowmax = 0;
+    if constexpr (P > 1) {
+        __builtin_amdgcn_sched_barrier(0);
+        load_pre();
+    }
+    block_sum<1>(s, red[1]);
+    const float ir = rms_of(s[0], fK, p.norm_eps);
 #pragma unroll
     for (int u = 0; u < P; ++u) {
-        const int64_t c = (int64_t)u * T + t;
-        if (c < chunks) {
-            float w[8];
-            unpack8(static_cast<const uint4*>(p.w_pre)[c], w);
+        float w[8];
+        unpack(wpre[u], w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r[u][i] = r[u][i] * ir * w[i];
-            if (p.normed) static_cast<uint4*>(p.normed)[m * chunks + c] = pack8(r[u]);
-            if constexpr (Q >= 0) rowmax = max(rowmax, amax8(r[u]));
-        }
+        for (int i = 0; i < 8; ++i) r[u][i] = r[u][i] * ir * w[i];
+        store16(r_n, voff[u], pack(r[u]));
     }
     if constexpr (Q >= 0) {
+        const __amdgpu_buffer_rsrc_t r_q = row_rsrc(p.q, m, (uint32_t)K);
+        auto store_codes = [&](int u, uint32_t mx, float sc) {
+            const uint2 q = encode8_group<Q>(r[u], mx, sc);
+            typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+            __builtin_amdgcn_raw_buffer_store_b64(v2u{q.x, q.y}, r_q, voff[u] / 2, 0, 0);
+        };
+        // lanes past the row hold zeros: they join the reductions and store nothing
         if (p.per_token) {
+            uint32_t mx = 0;
 #pragma unroll
-            for (int off = 32; off >= 1; off >>= 1)
-                rowmax = max(rowmax, (uint32_t)__shfl_xor((int)rowmax, off, 64));
-            if (lane == 0) redmax[t >> 6] = rowmax;
-            __syncthreads();
+            for (int u = 0; u < P; ++u) mx = max(mx, amax8(r[u]));
 #pragma unroll
-            for (int w = 0; w < T / 64; ++w) rowmax = max(rowmax, redmax[w]);
-            const float sc = group_scale<Q>(rowmax, p.q_eps, p.ue8m0);
+            for (int off = 32; off >= 1; off >>= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, off, 64));
+            if (lane == 0) redmax[t >> 6] = mx;
+            lds_barrier();
+            for (int w = 0; w < T / 64; ++w) mx = max(mx, redmax[w]);
+            const float sc = group_scale<Q>(mx, p.q_eps, p.ue8m0);
 #pragma unroll
-            for (int u = 0; u < P; ++u) {
-                const int64_t c = (int64_t)u * T + t;
-                if (c < chunks) static_cast<uint2*>(p.q)[m * chunks + c] = encode8_group<Q>(r[u], rowmax, sc);
-            }
+            for (int u = 0; u < P; ++u) store_codes(u, mx, sc);
             if (t == 0) p.scales[m * p.s_stride_m] = sc;
             return;
         }
 #pragma unroll
         for (int u = 0; u < P; ++u) {
-            const int64_t c = (int64_t)u * T + t, g = c >> 4;   // 16 lanes own group g
-            const bool live = c < chunks;                        // the same for all 16
-            const uint32_t mx = max16(live ? amax8(r[u]) : 0u);
+            const int64_t g = voff[u] >> 8;              // 16 lanes (256 bytes of bf16) own group g
+            const bool live = voff[u] < row16;
+            const uint32_t mx = max16(amax8(r[u]));
             const float sc = group_scale<Q>(mx, p.q_eps, p.ue8m0);
-            if (live) static_cast<uint2*>(p.q)[m * chunks + c] = encode8_group<Q>(r[u], mx, sc);
+            store_codes(u, mx, sc);
             if (p.packed) {
                 // a wave's slot holds the four groups of one word; E8M0 has no Inf: code 255
                 const uint32_t word = e8m0_word(live ? e8m0_of(sc) : 0u, lane);
@@ -183,58 +224,72 @@ __global__ __launch_bounds__(T) void norm_residual_kernel(NormArgs p) {
 //   dw_pre = sum_m dn * r^,  dw_post = sum_m dz * y^,  dgate = alpha * dr * z, summed over the
 //   rows (CHANNEL) or the row (TOKEN).
 // Two reductions a row: {sum r'^2, sum y^2, sum w_pre*dn*r'} together (the means are these times
-// powers of rms), then {sum dz*w_post*y}. A workgroup walks rows blockIdx.x, + gridDim.x, ... and
-// keeps its share of the column sums in registers, 16 a chunk: dn * r^, and alpha*dr*y^ (CHANNEL:
-// times w_post it is the gate's gradient, times the gate w_post's) or dz*y^ (else). Each
-// workgroup writes its shares once; norm_columns_kernel adds them in workgroup order, so equal
-// inputs give equal sums.
-template <int T, int P, int RF32>
-__global__ __launch_bounds__(T) void norm_residual_bwd_kernel(NormArgs p) {
-    constexpr int W = T / 64;
-    const int t = threadIdx.x;
-    const int64_t K = p.K, chunks = K / 8;
+// powers of rms), then {sum dz*z, sum dgate}. A workgroup walks rows blockIdx.x, + gridDim.x, ...
+// with the next row's loads in flight (P = 1; a second chunk a thread leaves no registers for
+// them), and keeps its share of the column sums in registers, 16 a chunk: dn * r^, and
+// alpha*dr*y^ (CHANNEL: times w_post it is the gate's gradient, times the gate w_post's) or dz*y^
+// (else). Each workgroup writes its shares once; norm_columns_kernel adds them in workgroup order,
+// so equal inputs give equal sums. The channel vectors wait in LDS.
+template <int P, int RF32>
+__global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
+    const int t = threadIdx.x, T = blockDim.x;
+    const int64_t K = p.K;
+    const uint32_t row16 = (uint32_t)(2 * K), row_res = RF32 ? 2 * row16 : row16;
     const float fK = (float)K;
-    __shared__ float red[2][5 * W];
-    const bool channel = p.gate_kind == BFQ_GATE_CHANNEL;
+    __shared__ __attribute__((aligned(16))) float red[2][5 * 16];
+    extern __shared__ v4u vec[];                         // [3][T * P]: w_pre, w_post, channel gate
+    const bool channel = p.gate_kind == BFQ_GATE_CHANNEL, elements = p.gate_kind == BFQ_GATE_FULL;
+    const bool post = p.w_post != nullptr;
+    struct Row {
+        Chunk<RF32> r, d;       // the stored sum, the stream's gradient
+        v4u y, n;               // the block's output, the gradient at its normed successor
+    };
+    // element gates of row m
+    auto gate_rsrc = [&](int64_t m) { return row_rsrc(elements && m < p.M ? p.gate : nullptr, m, row16); };
     float apre[P][8], apost[P][8];
-    uint4 wpre[P], wpost[P];
+    block_sum_init(red[0], 160);
+    auto load = [&](Row (&x)[P], int64_t m) {
+        const bool in = m < p.M;
+        const __amdgpu_buffer_rsrc_t rr = row_rsrc(in && p.w_pre ? p.residual : nullptr, m, row_res),
+                                     rd = row_rsrc(in ? p.d_res_out : nullptr, m, row_res),
+                                     ry = row_rsrc(in ? p.y : nullptr, m, row16),
+                                     rn = row_rsrc(in ? p.d_normed : nullptr, m, row16);
 #pragma unroll
-    for (int u = 0; u < P; ++u) {
-        const int64_t c = (int64_t)u * T + t;
-        wpre[u] = wpost[u] = make_uint4(0, 0, 0, 0);
-        if (c < chunks && p.w_pre) wpre[u] = static_cast<const uint4*>(p.w_pre)[c];
-        if (c < chunks && p.w_post) wpost[u] = static_cast<const uint4*>(p.w_post)[c];
+        for (int u = 0; u < P; ++u) {
+            const uint32_t voff = (uint32_t)(u * T + t) * 16;
+            x[u].r.load(rr, voff);
+            x[u].n = load16(rn, voff);
+            x[u].y = load16(ry, voff);
+            x[u].d.load(rd, voff);
+        }
+    };
+    Row cur[P];
+    load(cur, blockIdx.x);
+    {
+        const __amdgpu_buffer_rsrc_t r0 = row_rsrc(p.w_pre, 0, row16), r1 = row_rsrc(p.w_post, 0, row16),
+                                     r2 = row_rsrc(channel ? p.gate : nullptr, 0, row16);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) apre[u][i] = apost[u][i] = 0.f;
+        for (int u = 0; u < P; ++u) {
+            const int i = u * T + t;
+            vec[i] = load16(r0, (uint32_t)i * 16);
+            vec[T * P + i] = ones_unless(load16(r1, (uint32_t)i * 16), post);
+            vec[2 * T * P + i] = load16(r2, (uint32_t)i * 16);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) apre[u][j] = apost[u][j] = 0.f;
+        }
     }
     int par = 0;
     for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x, par ^= 1) {
-        Chunk<RF32> rc[P], dc[P];
-        uint4 yc[P], nc[P];
+        Row next[P];
+        if constexpr (P == 1) load(next, m + gridDim.x);
         float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
         for (int u = 0; u < P; ++u) {
-            const int64_t c = (int64_t)u * T + t;
-            rc[u].clear();
-            dc[u].clear();
-            yc[u] = nc[u] = make_uint4(0, 0, 0, 0);
-            if (c < chunks) {
-                const int64_t i = m * chunks + c;
-                if (p.w_pre) {
-                    rc[u].load(p.residual, i);
-                    nc[u] = static_cast<const uint4*>(p.d_normed)[i];
-                }
-                if (p.d_res_out) dc[u].load(p.d_res_out, i);
-                if (p.y) yc[u] = static_cast<const uint4*>(p.y)[i];
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < P; ++u) {
             float r[8], y[8], dn[8], w[8];
-            rc[u].get(r);
-            unpack8(yc[u], y);
-            unpack8(nc[u], dn);
-            unpack8(wpre[u], w);
+            cur[u].r.get(r);
+            unpack(cur[u].y, y);
+            unpack(cur[u].n, dn);
+            unpack(vec[u * T + t], w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 s[0] = __builtin_fmaf(r[i], r[i], s[0]);
@@ -242,91 +297,87 @@ __global__ __launch_bounds__(T) void norm_residual_bwd_kernel(NormArgs p) {
                 s[2] = __builtin_fmaf(w[i] * dn[i], r[i], s[2]);
             }
         }
-        block_sum<T, 3>(s, red[par]);
-        const float ir = 1.0f / __builtin_sqrtf(s[0] / fK + p.norm_eps);
-        const float iy = p.w_post ? 1.0f / __builtin_sqrtf(s[1] / fK + p.norm_eps) : 1.f;
+        block_sum<3>(s, red[par]);
+        const float ir = rms_of(s[0], fK, p.norm_eps), iy = post ? rms_of(s[1], fK, p.norm_eps) : 1.f;
         const float cr = ir * ir * s[2] / fK;      // r^ * mean(w_pre * dn * r^) = r' * cr
+        const float alpha = p.res_scale, a_row = row_scale(p, m);
+        const __amdgpu_buffer_rsrc_t rg = gate_rsrc(m), o_r = row_rsrc(p.d_res, m, row_res), o_y = row_rsrc(p.d_y, m, row16),
+                                     o_g = row_rsrc(elements ? p.d_gate : nullptr, m, row16);
         float dz[P][8], q[2] = {0.f, 0.f};
 #pragma unroll
         for (int u = 0; u < P; ++u) {
-            const int64_t c = (int64_t)u * T + t;
-            float r[8], dr[8];
-            rc[u].get(r);
-            dc[u].get(dr);
-            if (p.w_pre) {
-                float dn[8], w[8];
-                unpack8(nc[u], dn);
-                unpack8(wpre[u], w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dr[i] += ir * (w[i] * dn[i] - r[i] * cr);
-                    apre[u][i] = __builtin_fmaf(dn[i], r[i] * ir, apre[u][i]);
-                }
-            }
-            if (c >= chunks) continue;
-            Chunk<RF32>::store(p.d_res, m * chunks + c, dr);
-            if (!p.y) continue;
-            float y[8], g[8], w[8], dg[8];
-            gate8(p, m, c, chunks, g);
-            unpack8(yc[u], y);
-            unpack8(wpost[u], w);
+            const uint32_t voff = (uint32_t)(u * T + t) * 16;
+            float r[8], dr[8], dn[8], w[8], y[8], g[8], dg[8];
+            cur[u].r.get(r);
+            cur[u].d.get(dr);
+            unpack(cur[u].n, dn);
+            unpack(vec[u * T + t], w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float yn = y[i] * iy, z = p.w_post ? yn * w[i] : yn;
-                const float ad = p.res_scale * dr[i];
-                dz[u][i] = g[i] * dr[i];
+                dr[i] = __builtin_fmaf(ir, __builtin_fmaf(-r[i], cr, w[i] * dn[i]), dr[i]);
+                apre[u][i] = __builtin_fmaf(dn[i], r[i] * ir, apre[u][i]);
+            }
+            Chunk<RF32>::store(o_r, voff, dr);
+            unpack(cur[u].y, y);
+            unpack(ones_unless(channel ? vec[2 * T * P + u * T + t] : load16(rg, voff), channel || elements), g);
+            unpack(vec[T * P + u * T + t], w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float yn = y[i] * iy, z = yn * w[i], ad = alpha * dr[i];
+                dz[u][i] = a_row * dr[i] * g[i];
                 dg[i] = ad * z;
                 q[0] = __builtin_fmaf(dz[u][i], z, q[0]);
                 q[1] += dg[i];
                 apost[u][i] = __builtin_fmaf(channel ? ad : dz[u][i], yn, apost[u][i]);
             }
-            if (p.gate_kind == BFQ_GATE_FULL && p.d_gate)
-                static_cast<uint4*>(p.d_gate)[m * chunks + c] = pack8(dg);
+            store16(o_g, voff, pack(dg));
         }
-        if (!p.y) continue;                                 // uniform
-        block_sum<T, 2>(q, red[par] + 3 * W);
+        block_sum<2>(q, red[par] + 3 * 16);
         if (p.gate_kind == BFQ_GATE_TOKEN && p.d_gate && t == 0) static_cast<float*>(p.d_gate)[m] = q[1];
-        const float cy = p.w_post ? iy * q[0] / fK : 0.f;
+        const float cy = post ? iy * q[0] / fK : 0.f;
 #pragma unroll
         for (int u = 0; u < P; ++u) {
-            const int64_t c = (int64_t)u * T + t;
-            if (c >= chunks) continue;
-            if (p.w_post) {
-                float y[8], w[8];
-                unpack8(yc[u], y);
-                unpack8(wpost[u], w);
+            float y[8], w[8];
+            unpack(cur[u].y, y);
+            unpack(vec[T * P + u * T + t], w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dz[u][i] = iy * (w[i] * dz[u][i] - y[i] * cy);
-            }
-            static_cast<uint4*>(p.d_y)[m * chunks + c] = pack8(dz[u]);
+            for (int i = 0; i < 8; ++i) dz[u][i] = iy * __builtin_fmaf(-y[i], cy, w[i] * dz[u][i]);
+            store16(o_y, (uint32_t)(u * T + t) * 16, pack(dz[u]));
         }
+        if constexpr (P == 1) cur[0] = next[0];
+        else load(cur, m + gridDim.x);
     }
     if (!p.columns) return;
-    float* mine = p.partials + (int64_t)blockIdx.x * 2 * K;
+    const uint32_t row32 = (uint32_t)(4 * K);
+    const __amdgpu_buffer_rsrc_t s0 = row_rsrc(p.partials, 2 * (int64_t)blockIdx.x, row32),
+                                 s1 = row_rsrc(p.partials, 2 * (int64_t)blockIdx.x + 1, row32);
 #pragma unroll
     for (int u = 0; u < P; ++u) {
-        const int64_t c = (int64_t)u * T + t;
-        if (c < chunks) {
-            Chunk<1>::store(mine, c, apre[u]);
-            Chunk<1>::store(mine + K, c, apost[u]);
-        }
+        Chunk<1>::store(s0, (uint32_t)(u * T + t) * 16, apre[u]);
+        Chunk<1>::store(s1, (uint32_t)(u * T + t) * 16, apost[u]);
     }
 }
 
-// Column sums of the workgroups' shares [rows][2][K]: 64 columns a workgroup, 16 threads a column
-// each adding every 16th share, then the 16 in order.
-__global__ __launch_bounds__(1024) void norm_columns_kernel(NormArgs p, int rows) {
-    const int64_t K = p.K, col = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
-    const int part = threadIdx.x >> 6;
-    __shared__ float sums[16][64];
-    float s = 0.f;
-    if (col < 2 * K)
-        for (int g = part; g < rows; g += 16) s += p.partials[(int64_t)g * 2 * K + col];
-    sums[part][threadIdx.x & 63] = s;
+// Column sums of the workgroups' shares [rows][2][K]: 64 columns a workgroup, four a thread; its 16
+// rows of threads each add every 16th share (several loads in flight), then the 16 in order.
+__global__ __launch_bounds__(256) void norm_columns_kernel(NormArgs p, int rows) {
+    const int64_t K = p.K;
+    const int t = threadIdx.x, part = t >> 4;
+    const int64_t c4 = (int64_t)blockIdx.x * 64 + (t & 15) * 4;       // 2K is a multiple of 4
+    __shared__ v4f sums[16][16];
+    v4f a = {0.f, 0.f, 0.f, 0.f};
+    if (c4 < 2 * K) {
+        const float* src = p.partials + c4;
+#pragma unroll 8
+        for (int g = part; g < rows; g += 16) a += *reinterpret_cast<const v4f*>(src + (int64_t)g * 2 * K);
+    }
+    sums[part][t & 15] = a;
     __syncthreads();
-    if (part != 0 || col >= 2 * K) return;
+    const int64_t col = (int64_t)blockIdx.x * 64 + t;
+    if (t >= 64 || col >= 2 * K) return;
+    float s = 0.f;
 #pragma unroll
-    for (int g = 1; g < 16; ++g) s += sums[g][threadIdx.x];
+    for (int g = 0; g < 16; ++g) s += sums[g][t >> 2][t & 3];
     if (col < K) {
         if (p.d_w_pre) p.d_w_pre[col] = s;
         return;
@@ -342,70 +393,61 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(NormArgs p, int rows
 
 // ---------------------------------------------------------------- launchers ----
 
-template <int T, int P, int RF32>
+static unsigned threads_for(int64_t K, int P) {
+    return (unsigned)((K / 8 + 64 * P - 1) / (64 * P) * 64);
+}
+
+template <int P, int RF32>
 static hipError_t launch_norm_q(const NormArgs& a, hipStream_t stream) {
     const int64_t rows = a.packed ? (a.M + 3) / 4 * 4 : a.M;
-    const dim3 grid((unsigned)rows);
+    const dim3 grid((unsigned)rows), block(threads_for(a.K, P));
     if (!a.q)
-        hipLaunchKernelGGL((norm_residual_kernel<T, P, RF32, -1>), grid, dim3(T), 0, stream, a);
+        hipLaunchKernelGGL((norm_residual_kernel<P, RF32, -1>), grid, block, 0, stream, a);
     else if (a.qtype == Q_FP8)
-        hipLaunchKernelGGL((norm_residual_kernel<T, P, RF32, Q_FP8>), grid, dim3(T), 0, stream, a);
+        hipLaunchKernelGGL((norm_residual_kernel<P, RF32, Q_FP8>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((norm_residual_kernel<T, P, RF32, Q_INT8>), grid, dim3(T), 0, stream, a);
+        hipLaunchKernelGGL((norm_residual_kernel<P, RF32, Q_INT8>), grid, block, 0, stream, a);
     return hipGetLastError();
 }
 
+// Chunks a thread. Few waves a row start and reduce sooner (one row of 1536: 3.4 us with one chunk
+// a thread, 3.8 with two); fewer, fatter threads leave room for more rows on a CU (4096 rows of
+// 7168: 62.5 us with one chunk, 47.8 with two, 47.2 with four; 1024 rows of 16384: 29.2 with two,
+// 25.8 with four).
 template <int RF32>
 static hipError_t launch_norm_p(const NormArgs& a, hipStream_t stream) {
-    const int64_t slots = (a.K / 8 + 255) / 256;
-    if (slots <= 1) return launch_norm_q<256, 1, RF32>(a, stream);
-    if (slots <= 2) return launch_norm_q<256, 2, RF32>(a, stream);
-    if (slots <= 4) return launch_norm_q<256, 4, RF32>(a, stream);
-    if (slots <= 8) return launch_norm_q<256, 8, RF32>(a, stream);
-    return hipErrorInvalidValue;                            // K beyond kNormMaxK (rejected before)
+    if (a.K <= 2048) return launch_norm_q<1, RF32>(a, stream);
+    if (a.K <= 8192 || a.M <= 256) return launch_norm_q<2, RF32>(a, stream);
+    return launch_norm_q<4, RF32>(a, stream);
 }
 
 hipError_t launch_norm_residual(const NormArgs& a, int res_f32, hipStream_t stream) {
     return res_f32 ? launch_norm_p<1>(a, stream) : launch_norm_p<0>(a, stream);
 }
 
-// Workgroups of the backward kernel: one for each row up to a fixed number, whose column sums a
-// second kernel adds.
-static int64_t bwd_threads(int64_t K) { return K <= 2048 ? 256 : K <= 4096 ? 512 : 1024; }
-
+// Workgroups of the backward kernel: one for each row up to what the CUs hold at once (16 waves
+// each at its register count).
 int64_t norm_bwd_groups(int64_t M, int64_t K) {
-    const int64_t most = 256 * (1024 / bwd_threads(K));
+    const int64_t most = 256 * (1024 / threads_for(K, K <= 8192 ? 1 : 2));
     return M < most ? M : most;
-}
-
-template <int RF32>
-static void launch_bwd(const NormArgs& a, dim3 grid, hipStream_t stream) {
-    switch (bwd_threads(a.K)) {
-        case 256:
-            hipLaunchKernelGGL((norm_residual_bwd_kernel<256, 1, RF32>), grid, dim3(256), 0, stream, a);
-            break;
-        case 512:
-            hipLaunchKernelGGL((norm_residual_bwd_kernel<512, 1, RF32>), grid, dim3(512), 0, stream, a);
-            break;
-        default:
-            if (a.K <= 8192)
-                hipLaunchKernelGGL((norm_residual_bwd_kernel<1024, 1, RF32>), grid, dim3(1024), 0, stream, a);
-            else
-                hipLaunchKernelGGL((norm_residual_bwd_kernel<1024, 2, RF32>), grid, dim3(1024), 0, stream, a);
-    }
 }
 
 hipError_t launch_norm_residual_bwd(const NormArgs& a, int res_f32, hipStream_t stream) {
     const int64_t groups = norm_bwd_groups(a.M, a.K);
     if (groups > 0) {
-        if (res_f32) launch_bwd<1>(a, dim3((unsigned)groups), stream);
-        else launch_bwd<0>(a, dim3((unsigned)groups), stream);
+        const int P = a.K <= 8192 ? 1 : 2;
+        const dim3 grid((unsigned)groups), block(threads_for(a.K, P));
+        const unsigned lds = block.x * P * 3 * sizeof(v4u);
+        if (P == 1 && res_f32) hipLaunchKernelGGL((norm_residual_bwd_kernel<1, 1>), grid, block, lds, stream, a);
+        else if (P == 1) hipLaunchKernelGGL((norm_residual_bwd_kernel<1, 0>), grid, block, lds, stream, a);
+        else if (res_f32) hipLaunchKernelGGL((norm_residual_bwd_kernel<2, 1>), grid, block, lds, stream, a);
+        else hipLaunchKernelGGL((norm_residual_bwd_kernel<2, 0>), grid, block, lds, stream, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (a.columns) {
         const int64_t wg = (2 * a.K + 63) / 64;
-        hipLaunchKernelGGL(norm_columns_kernel, dim3((unsigned)wg), dim3(1024), 0, stream, a, (int)groups);
+        hipLaunchKernelGGL(norm_columns_kernel, dim3((unsigned)wg), dim3(256), 0, stream, a, (int)groups);
     }
     return hipGetLastError();
 }

@@ -72,18 +72,23 @@ __device__ __forceinline__ float pow2_ceil(float s) {
     return (u & 0x007FFFFFu) ? __uint_as_float((u & 0xFF800000u) + 0x00800000u) : s;
 }
 
-// Encode 8 fp32 values of a finite group (|x| <= amax of the group that s was formed from). The
-// quotient as in encode8, one reciprocal and one remainder correction: q = x * r is within
-// 1.5 units of x / s, e = x - q * s is exact while s is normal and away from the range's ends,
-// and q + e * r rounds the quotient to within a hair of half a unit, so a code differs from that
-// of the IEEE quotient only where x / s lies within 2^-46 of a midpoint between two codes.
+// Encode 8 fp32 values of a finite group (|x| <= amax of the group that s was formed from): the
+// product with the reciprocal, which is within 2 units of the quotient x / s, the size of the
+// roundings x itself carries when it comes out of fp32 arithmetic. (encode8 above corrects that
+// product, 3 operations a value more, so that codes of given bf16 inputs are the IEEE quotient's.)
 // Scales outside [2^-100, 2^100] (a tiny eps, or amax near the range's ends) take the division.
 template <int QT>
 __device__ __forceinline__ uint2 encode8_f32(const float* x, float s) {
-    if (s >= 0x1p-100f && s <= 0x1p100f) return encode8<QT>(x, s);
     float y[8];
+    if (s >= 0x1p-100f && s <= 0x1p100f) {
+        const float r0 = __builtin_amdgcn_rcpf(s);
+        const float rs = __builtin_fmaf(__builtin_fmaf(-s, r0, 1.f), r0, r0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = x[i] / s;
+        for (int i = 0; i < 8; ++i) y[i] = x[i] * rs;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[i] / s;
+    }
     uint2 r;
     if constexpr (QT == Q_FP8) {
         r.x = enc_fp8x4(y[0], y[1], y[2], y[3]);
@@ -97,12 +102,21 @@ __device__ __forceinline__ uint2 encode8_f32(const float* x, float s) {
 
 // The scale of a group whose largest magnitude has the fp32 bits `mx` (NaN > Inf > finite as
 // unsigned integers): max(amax, eps) / Qmax, rounded up to a power of two for UE8M0; NaN or
-// Inf for a group that holds one.
+// Inf for a group that holds one. The quotient is the IEEE one: a product with the correctly
+// rounded 1 / Qmax and one remainder step round correctly while nothing in them is subnormal
+// (Markstein's theorem); the range's ends divide.
 template <int QT>
 __device__ __forceinline__ float group_scale(uint32_t mx, float eps, int ue8m0) {
     if (mx >= 0x7F800000u) return __uint_as_float(mx > 0x7F800000u ? 0x7FC00000u : 0x7F800000u);
-    const float amax = __uint_as_float(mx);
-    const float s = (amax > eps ? amax : eps) / qmax<QT>();
+    const float a = __builtin_fmaxf(__uint_as_float(mx), eps);
+    float s;
+    if (a >= 0x1p-90f && a <= 0x1p120f) {
+        constexpr float r = 1.0f / (QT == Q_FP8 ? kFp8Max : kInt8Max);
+        const float q = a * r;
+        s = __builtin_fmaf(__builtin_fmaf(-q, qmax<QT>(), a), r, q);
+    } else {
+        s = a / qmax<QT>();
+    }
     return ue8m0 ? pow2_ceil(s) : s;
 }
 
@@ -112,14 +126,17 @@ __device__ __forceinline__ uint2 encode8_group(const float* x, uint32_t mx, floa
     return mx < 0x7F800000u ? encode8_f32<QT>(x, s) : encode8_special<QT>(x, mx > 0x7F800000u);
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+// The larger of m and |x|, a NaN where either is one.
+__device__ __forceinline__ float max_abs(float m, float x) {
+    return __builtin_elementwise_maximum(m, __builtin_fabsf(x));
+}
 
-// Largest magnitude (bits) of 8 values.
+// Largest magnitude (bits) of 8 values; a NaN among them wins.
 __device__ __forceinline__ uint32_t amax8(const float* x) {
-    uint32_t m = abs_bits(x[0]);
+    float m = __builtin_fabsf(x[0]);
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = max(m, abs_bits(x[i]));
-    return m;
+    for (int i = 1; i < 8; ++i) m = max_abs(m, x[i]);
+    return __float_as_uint(m) & 0x7FFFFFFFu;
 }
 
 // The value of another lane of the same 16-lane row, through the DPP operand path (no LDS): the
@@ -150,26 +167,40 @@ __device__ __forceinline__ float wave_sum(float x) {
     return x + __shfl_xor(x, 32, 64);
 }
 
-// Sums of N values over a workgroup of T threads, in every thread, added in a fixed order.
-// `slot` holds N * T / 64 floats of LDS that no thread still reads from an earlier call.
-template <int T, int N>
+// Barrier that orders LDS accesses only. __syncthreads() also waits for every outstanding global
+// load and store of the wave, which would drain the next row's loads and stall on the last stores.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Sums of N values over a workgroup of up to 1024 threads (blockDim.x a multiple of 64), in every
+// thread, added in a fixed order. `slot` is 16 * N floats of LDS, 16-byte aligned, that no thread
+// still reads from an earlier call; block_sum_init clears the slots of waves that do not exist, so
+// that the sum always takes 16 in four wide reads (a loop over the waves would wait for LDS once
+// a wave).
+__device__ __forceinline__ void block_sum_init(float* slots, int n) {
+    const int W = blockDim.x >> 6;
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        if ((i & 15) >= W) slots[i] = 0.f;
+}
+template <int N>
 __device__ __forceinline__ void block_sum(float (&v)[N], float* slot) {
-    constexpr int W = T / 64;
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-    if constexpr (W > 1) {
-        if ((threadIdx.x & 63) == 0) {
+    if (blockDim.x == 64) return;
+    if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) slot[i * W + (threadIdx.x >> 6)] = v[i];
-        }
-        __syncthreads();
+        for (int i = 0; i < N; ++i) slot[16 * i + (threadIdx.x >> 6)] = v[i];
+    }
+    lds_barrier();
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float s = slot[i * W];
-#pragma unroll
-            for (int w = 1; w < W; ++w) s += slot[i * W + w];
-            v[i] = s;
-        }
+    for (int i = 0; i < N; ++i) {
+        const v4f* q = reinterpret_cast<const v4f*>(slot + 16 * i);
+        const v4f a = q[0], b = q[1], c = q[2], d = q[3];
+        const v4f e = (a + b) + (c + d);
+        v[i] = (e.x + e.y) + (e.z + e.w);
     }
 }
 
@@ -188,13 +219,13 @@ __device__ __forceinline__ void unpack8(const uint4& v, float* x) {
     x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
     x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z); x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
 }
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));   // RNE
+}
 __device__ __forceinline__ uint4 pack8(const float* x) {
-    uint4 v;
-    v.x = f32_to_bf16_bits(x[0]) | (f32_to_bf16_bits(x[1]) << 16);
-    v.y = f32_to_bf16_bits(x[2]) | (f32_to_bf16_bits(x[3]) << 16);
-    v.z = f32_to_bf16_bits(x[4]) | (f32_to_bf16_bits(x[5]) << 16);
-    v.w = f32_to_bf16_bits(x[6]) | (f32_to_bf16_bits(x[7]) << 16);
-    return v;
+    return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
 }
 
 }  // namespace bfq
