@@ -1,6 +1,8 @@
 // C-ABI entry points of the feed-forward operators (include/bfq.h): the gated product, its
 // gradient, the weight transpose, and the norms around a block with their gradients. Arguments
 // are validated before any launch, as in api.cpp.
+#include <cmath>
+
 #include "api_common.h"
 
 using namespace bfq;
@@ -62,51 +64,76 @@ const GatedKernel* find_gated(const bfq_tile& t, int wlayout, int sfmt) {
     return nullptr;
 }
 
-bfq_tile std_gated(int bm, int bn, int sched) {
-    bfq_tile t{};
-    t.variant = 0; t.bm = bm; t.bn = bn; t.bk = 128; t.split_k = 1; t.stages = 2; t.group_m = 8;
-    t.waves_m = bm / 64;
-    t.waves_n = 2;
-    t.sched = sched;
-    return t;
+// The tile of (bm, bn, sched) among the kernels built for a weight layout.
+bfq_tile gated_tile(int variant, int bm, int bn, int sched, int wlayout) {
+    int n = 0;
+    const GatedKernel* k = gated_kernels(&n);
+    for (int i = 0; i < n; ++i) {
+        const bfq_tile& t = k[i].tile;
+        if (k[i].wlayout == wlayout && t.variant == variant && t.bm == bm && t.bn == bn && t.sched == sched)
+            return t;
+    }
+    return bfq_tile{};
 }
 
-bfq_tile strip_gated(int bm, int waves_m, int waves_n, int lds) {
-    bfq_tile t{};
-    t.variant = 1; t.bm = bm; t.bn = 16 * waves_n; t.bk = 128; t.split_k = 1; t.stages = 4;
-    t.group_m = 1;
-    t.waves_m = waves_m;
-    t.waves_n = waves_n;
-    t.sched = lds;
-    return t;
+// Microseconds that a gated product is expected to take with kernel k and its K range in `split`
+// parts. The grid runs in rounds of 256 CUs times the workgroups a CU holds; a round's K block
+// takes the longer of a workgroup's own latency and the CU's throughput over the workgroups it
+// holds (joined smoothly), the whole no less than the weight stream; partials cost a second
+// launch and their bytes twice. The constants, here and beside the kernels, are a fit to 768
+// measured (M, F, K, layout, format, output) points of 9 to 60 configurations each, M 1 to 2048
+// on six (F, K); over them the pick is on average 3.3 % slower than the fastest configuration.
+float gated_us(const GatedKernel& k, int64_t M, int64_t F, int64_t K, bool codes, int split) {
+    const bfq_tile& t = k.tile;
+    const int64_t groups = ceil_div(M, t.bm) * ceil_div(F, t.bn) * split;
+    const int64_t slots = kNumCUs * k.occupancy, full = groups / slots, rest = groups % slots;
+    const int kw = t.variant == 1 ? t.waves_m : 1;         // waves that share a strip's K range
+    const float blocks = (float)ceil_div(ceil_div(K / 128, split), kw);
+    auto round = [&](int64_t held) {
+        const float a = k.lat * blocks, b = (float)held * k.thr * blocks * kw;
+        return std::sqrt(std::sqrt(a * a * a * a + b * b * b * b)) + k.fix;
+    };
+    float us = (float)full * round(k.occupancy) + (rest ? round(ceil_div(rest, kNumCUs)) : 0.f);
+    const float stream = 2.f * (float)F * (float)K / (k.wlayout == W_PACKED16 ? 6.11e6f : 4.62e6f);
+    const float x = us > stream ? stream / us : us / stream, x2 = x * x, x4 = x2 * x2;
+    us = (us > stream ? us : stream) * std::sqrt(std::sqrt(std::sqrt(1.f + x4 * x4)));
+    if (split > 1 || (codes && t.bn != 128)) us += 2.74f + (float)split * (float)M * (float)F * 16.f / 5.54e6f;
+    return us;
 }
 
-// The rule. Strips (the weight stream) up to 128 tokens, else the standard tile that fills the
-// CUs; a K split where the grid would leave CUs idle, at least four K blocks each.
-bfq_tile select_gated(int64_t M, int64_t F, int64_t K, int wlayout, int sfmt) {
+// The rule: the kernel and K split with the least expected time. Strips read the weights again
+// for every bm tokens, so they are left out where that is many times.
+bfq_tile select_gated(int64_t M, int64_t F, int64_t K, bool codes, int wlayout, int sfmt) {
     const int64_t KB = K / 128;
     if (batch_invariant()) {
         // one MFMA per K block and fp32 scale FMAs in ascending order, whatever M
         if (wlayout == W_PACKED16 && M <= 128)
-            return M <= 16 ? strip_gated(16, 1, 8, 0)
-                           : strip_gated(M <= 32 ? 32 : M <= 64 ? 64 : 128, 1, 8, 1);
-        return M <= 64 ? std_gated(64, 64, 0) : M <= 512 ? std_gated(128, 64, 0) : std_gated(256, 128, 0);
+            return gated_tile(1, M <= 32 ? 32 : M <= 64 ? 64 : 128, 128, 1, wlayout);
+        if (M <= 64) return gated_tile(0, 64, 64, 0, wlayout);
+        return M <= 512 ? gated_tile(0, 128, 64, 0, wlayout) : gated_tile(0, 256, 128, 0, wlayout);
     }
-    bfq_tile t;
-    int64_t groups;
-    if (M <= 128) {
-        t = M <= 16 ? strip_gated(16, 8, 1, 0)
-                    : strip_gated(M <= 32 ? 32 : M <= 64 ? 64 : 128, 1, 8, 1);
-        groups = ceil_div(F, t.bn) * ceil_div(M, t.bm);
-    } else {
-        const int s3 = sfmt == S_UE8M0 ? 3 : 0;
-        t = std_gated(256, 128, s3);
-        if (ceil_div(M, 256) * ceil_div(F, 128) < kNumCUs) t = std_gated(128, 128, s3);
-        if (ceil_div(M, 128) * ceil_div(F, 128) < kNumCUs) t = std_gated(128, 64, s3);
-        groups = ceil_div(F, t.bn) * ceil_div(M, t.bm);
+    int n = 0;
+    const GatedKernel* k = gated_kernels(&n);
+    bfq_tile best{};
+    float best_us = 3.0e38f;
+    for (int i = 0; i < n; ++i) {
+        const bfq_tile& t = k[i].tile;
+        if (k[i].wlayout != wlayout || k[i].sfmt == S_PACKED || (k[i].sfmt == S_UE8M0 && sfmt != S_UE8M0))
+            continue;
+        if (t.variant == 1 ? M > 512 || M > 4 * t.bm : M < 24 || M < t.bm / 4) continue;
+        const int64_t groups = ceil_div(M, t.bm) * ceil_div(F, t.bn);
+        for (int split : {1, 2, 3, 4, 6, 8, 12}) {
+            // at least two K blocks a part, and no parts beyond those that fill the CUs
+            if (split > 1 && (split * 2 > KB || groups * (split - 1) >= kNumCUs * k[i].occupancy)) break;
+            const float us = gated_us(k[i], M, F, K, codes, split);
+            if (us < best_us) {
+                best_us = us;
+                best = t;
+                best.split_k = split;
+            }
+        }
     }
-    while (groups * t.split_k < kNumCUs && KB / (t.split_k * 2) >= 4) t.split_k *= 2;
-    return t;
+    return best;
 }
 
 // A tile finishes its outputs itself unless its K range is split or codes need whole groups.
@@ -132,7 +159,7 @@ bfq_status bfq_gated_select_tile(int64_t M, int64_t F, int64_t K, bfq_dtype out_
     if (M < 0 || F <= 0 || K <= 0 || F % 128 != 0 || K % 128 != 0)
         return fail(BFQ_ERR_SHAPE, "need M >= 0 and F, K positive multiples of 128");
     if (gated_too_large(M, F, K)) return fail(BFQ_ERR_SHAPE, "gated product: shape too large");
-    *tile_out = select_gated(M, F, K, (int)w_layout, (int)scale_fmt);
+    *tile_out = select_gated(M, F, K, out_dtype == BFQ_E4M3FN, (int)w_layout, (int)scale_fmt);
     return BFQ_OK;
 }
 
@@ -141,8 +168,10 @@ size_t bfq_gated_gemm_workspace_bytes(int64_t M, int64_t F, int64_t K, bfq_dtype
                                       const bfq_tile* tile) {
     if (M <= 0 || F <= 0 || K <= 0) return 0;
     if (gated_too_large(M, F, K)) return SIZE_MAX;
-    const bfq_tile t = tile ? *tile : select_gated(M, F, K, (int)w_layout, (int)scale_fmt);
-    if (!needs_partials(t, out_dtype == BFQ_E4M3FN) || t.split_k < 1) return 0;
+    if (!tile && (!wlayout_ok(w_layout) || F % 128 != 0 || K % 128 != 0)) return 0;
+    const bool codes = out_dtype == BFQ_E4M3FN;
+    const bfq_tile t = tile ? *tile : select_gated(M, F, K, codes, (int)w_layout, (int)scale_fmt);
+    if (!needs_partials(t, codes) || t.split_k < 1) return 0;
     return (size_t)t.split_k * (size_t)M * 2 * (size_t)F * sizeof(float);
 }
 
@@ -226,7 +255,7 @@ bfq_status bfq_gated_gemm(const void* a_q, const float* a_scales, bfq_scale_layo
         if (s != BFQ_OK) return s;
     }
     const int wl = (int)w_layout;
-    bfq_tile t = tile ? *tile : select_gated(M, F, K, wl, (int)scale_fmt);
+    bfq_tile t = tile ? *tile : select_gated(M, F, K, codes, wl, (int)scale_fmt);
     const GatedKernel* gk = find_gated(t, wl, apacked ? S_PACKED : (int)scale_fmt);
     if (!gk || (gk->sfmt == S_UE8M0 && scale_fmt != BFQ_SCALE_UE8M0))
         return fail(BFQ_ERR_TILE, "tile does not name a compiled gated kernel for this weight layout "

@@ -145,11 +145,15 @@ struct GatedArgs : GemmArgs {
     float os_eps;
 };
 typedef hipError_t (*GatedLaunchFn)(const GatedArgs& args, hipStream_t stream);
-// bfq_tile of a gated kernel: bn = output columns of a workgroup (2 * bn weight rows).
+// bfq_tile of a gated kernel: bn = output columns of a workgroup (2 * bn weight rows). For the
+// rule that picks one: the workgroups a CU holds, the microseconds a K block takes a workgroup
+// alone (lat) and a CU in its share of a full one (thr), and those around the K loop (fix).
 struct GatedKernel {
     bfq_tile tile;
     int wlayout, sfmt;
     GatedLaunchFn launch;
+    int occupancy;
+    float lat, thr, fix;
 };
 const GatedKernel* gated_kernels(int* count);
 // out (and pre) from the partials of `split` K ranges: sums in range order, activation, product.

@@ -19,11 +19,18 @@
 
 namespace bfq {
 
-// out element type of four consecutive outputs, chosen at run time (uniform)
+// Four values as bf16 or fp16 (uniform choice).
+__device__ __forceinline__ uint2 half4(int otype, const v4f& v) {
+    if (otype == O_FP16)
+        return make_uint2(f32_to_f16_bits(v.x) | (f32_to_f16_bits(v.y) << 16),
+                          f32_to_f16_bits(v.z) | (f32_to_f16_bits(v.w) << 16));
+    return make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+}
+
+// Four consecutive outputs, their type chosen at run time (uniform).
 __device__ __forceinline__ void store4_any(int otype, void* out, int64_t idx, const v4f& v) {
-    if (otype == O_BF16) store4<O_BF16>(out, idx, v);
-    else if (otype == O_FP16) store4<O_FP16>(out, idx, v);
-    else store4<O_FP32>(out, idx, v);
+    if (otype == O_FP32) *reinterpret_cast<v4f*>(static_cast<float*>(out) + idx) = v;
+    else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + idx) = half4(otype, v);
 }
 
 // One scale of group g of token m; packed: its byte of the word, and by the last group the zero
@@ -59,25 +66,36 @@ __device__ __forceinline__ void gated_partials(const GatedArgs& p, const v4f (&a
     }
 }
 
-// Pre-activations to p.pre and act(g) * u into acc[sm][0..SG).
+// act(g) * u into acc[sm][0..SG).
+template <int SM, int SG>
+__device__ __forceinline__ void gated_product(const GatedArgs& p, v4f (&acc)[SM][2 * SG]) {
+#pragma unroll
+    for (int sm = 0; sm < SM; ++sm)
+#pragma unroll
+        for (int sn = 0; sn < SG; ++sn)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[sm][sn][i] = act_f32(acc[sm][sn][i], p.c1, p.c3) * acc[sm][sn + SG][i];
+}
+
+// Pre-activations to p.pre, then the product.
 template <int SM, int SG, typename RowFn>
 __device__ __forceinline__ void gated_combine(const GatedArgs& p, v4f (&acc)[SM][2 * SG], int64_t n,
                                               RowFn row) {
     const int64_t F = p.N;
+    if (p.pre) {
 #pragma unroll
-    for (int sm = 0; sm < SM; ++sm) {
-        const int64_t m = row(sm);
+        for (int sm = 0; sm < SM; ++sm) {
+            const int64_t m = row(sm);
+            if (m < 0) continue;
 #pragma unroll
-        for (int sn = 0; sn < SG; ++sn) {
-            if (p.pre && m >= 0) {
-                store4<O_BF16>(p.pre, m * 2 * F + n + sn * 16, acc[sm][sn]);
-                store4<O_BF16>(p.pre, m * 2 * F + F + n + sn * 16, acc[sm][sn + SG]);
+            for (int sn = 0; sn < SG; ++sn) {
+                store4_any(O_BF16, p.pre, m * 2 * F + n + sn * 16, acc[sm][sn]);
+                store4_any(O_BF16, p.pre, m * 2 * F + F + n + sn * 16, acc[sm][sn + SG]);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[sm][sn][i] = act_f32(acc[sm][sn][i], p.c1, p.c3) * acc[sm][sn + SG][i];
         }
     }
+    gated_product<SM, SG>(p, acc);
 }
 
 // Largest magnitudes (bits) of each token's outputs in this wave's columns, in every lane of the
@@ -105,6 +123,29 @@ __device__ __forceinline__ uint32_t codes4(const v4f& v, uint32_t mx, float s) {
 
 // ---------------------------------------------------------------- standard tiles ----
 
+// Output tiles leave through LDS: a lane's accumulators hold four neighbouring columns of 16 rows a
+// sub-tile, 32-byte pieces of a row in a store, so the tile is laid out as rows of 16-byte chunks
+// and stored as whole rows (4096 x 18432 outputs with their pre-activations, K = 7168: ). Chunk c of row r sits in slot c ^ (r & (chunks - 1)) of its row, which spreads a
+// column of rows over the banks.
+template <int ROWB>
+__device__ __forceinline__ uint32_t tile_slot(int r, int byte) {
+    constexpr int C = ROWB / 16;
+    return (uint32_t)(r * ROWB + (((byte >> 4) ^ (r & (C - 1))) << 4) + (byte & 15));
+}
+// Rows of ROWB bytes from LDS to dst + r * ld, r < rows.
+template <int BM, int ROWB, int THREADS>
+__device__ __forceinline__ void store_tile(const uint8_t* lds, void* dst, int64_t ld, int64_t rows) {
+    constexpr int C = ROWB / 16, STEP = THREADS / C;
+    const int r0 = threadIdx.x / C, c = threadIdx.x % C;
+#pragma unroll
+    for (int i = 0; i < BM / STEP; ++i) {
+        const int r = r0 + i * STEP;
+        if (r < rows)
+            *reinterpret_cast<v4u*>(static_cast<uint8_t*>(dst) + r * ld + c * 16) =
+                *reinterpret_cast<const v4u*>(lds + tile_slot<ROWB>(r, c * 16));
+    }
+}
+
 // One workgroup per (tile of BM tokens x BN / 2 output columns, K split).
 template <int BM, int BN, int WM, int WN, int SCHED, int WL>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_gated_std_kernel(GatedArgs p) {
@@ -129,45 +170,73 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_gated_std_kernel(GatedArgs 
         gated_partials<SM, SG>(p, acc, n, row);
         return;
     }
-    gated_combine<SM, SG>(p, acc, n, row);
-    if (p.otype != O_CODES) {
+    // std_tile ends on a barrier: the LDS is free. lr, lc: the lane's first row and column of the tile
+    constexpr int THREADS = 64 * WM * WN;
+    const int lr = wm * TM + frow, lc = wn * TNO + 4 * fgrp;
+    const int64_t live = M - m0 < BM ? M - m0 : BM;
+    auto put = [&](int off, int otype, int half) {      // 16-bit values of one half of acc
+#pragma unroll
+        for (int sm = 0; sm < SM; ++sm)
+#pragma unroll
+            for (int sn = 0; sn < SG; ++sn)
+                *reinterpret_cast<uint2*>(lds + off + tile_slot<2 * BNO>(lr + sm * 16, 2 * (lc + sn * 16))) =
+                    half4(otype, acc[sm][sn + half * SG]);
+    };
+    if (p.pre) {
+        put(0, O_BF16, 0);
+        put(BM * 2 * BNO, O_BF16, 1);
+        lds_barrier();
+        uint16_t* pre = static_cast<uint16_t*>(p.pre) + m0 * 2 * F + n0;
+        store_tile<BM, 2 * BNO, THREADS>(lds, pre, 4 * F, live);
+        store_tile<BM, 2 * BNO, THREADS>(lds + BM * 2 * BNO, pre + F, 4 * F, live);
+        lds_barrier();
+    }
+    gated_product<SM, SG>(p, acc);
+    if (p.otype == O_FP32) {
 #pragma unroll
         for (int sm = 0; sm < SM; ++sm) {
             const int64_t m = row(sm);
             if (m < 0) continue;
 #pragma unroll
-            for (int sn = 0; sn < SG; ++sn) store4_any(p.otype, p.out, m * F + n + sn * 16, acc[sm][sn]);
+            for (int sn = 0; sn < SG; ++sn) store4_any(O_FP32, p.out, m * F + n + sn * 16, acc[sm][sn]);
         }
         return;
     }
+    if (p.otype != O_CODES) {
+        put(0, p.otype, 0);
+        lds_barrier();
+        store_tile<BM, 2 * BNO, THREADS>(lds, static_cast<uint16_t*>(p.out) + m0 * F + n0, 2 * F, live);
+        return;
+    }
     if constexpr (BNO == 128) {
-        // the tile's 128 columns are one group: largest magnitudes over its WN waves through LDS
-        // (std_tile ends on a barrier), [wn][tile row]
+        // the tile's 128 columns are one group: largest magnitudes over its WN waves through LDS,
+        // [wn][tile row], behind the codes
         uint32_t mx[SM];
         gated_amax<SM, SG>(acc, mx);
-        uint32_t* red = reinterpret_cast<uint32_t*>(lds);
+        uint32_t* red = reinterpret_cast<uint32_t*>(lds + BM * BNO);
         if (fgrp == 0)
 #pragma unroll
-            for (int sm = 0; sm < SM; ++sm) red[wn * BM + wm * TM + sm * 16 + frow] = mx[sm];
-        __syncthreads();
+            for (int sm = 0; sm < SM; ++sm) red[wn * BM + lr + sm * 16] = mx[sm];
+        lds_barrier();
         const int64_t g = n0 / 128, G = F / 128;
 #pragma unroll
         for (int sm = 0; sm < SM; ++sm) {
             uint32_t m = 0;
 #pragma unroll
-            for (int w = 0; w < WN; ++w) m = max(m, red[w * BM + wm * TM + sm * 16 + frow]);
+            for (int w = 0; w < WN; ++w) m = max(m, red[w * BM + lr + sm * 16]);
             const float s = group_scale<Q_FP8>(m, p.os_eps, p.os_ue8m0);
             const int64_t r = mw + sm * 16;
             // packed words have rows up to a multiple of four tokens, zero past the last
             if (wn == 0 && fgrp == 0 && r < (p.os_packed ? (M + 3) / 4 * 4 : M))
                 store_scale(p.out_scales, p.os_stride_m, p.os_stride_g, p.os_packed, r, g, G,
                             r < M ? s : 0.f);
-            if (r >= M) continue;
 #pragma unroll
             for (int sn = 0; sn < SG; ++sn)
-                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + r * F + n + sn * 16) =
+                *reinterpret_cast<uint32_t*>(lds + tile_slot<BNO>(lr + sm * 16, lc + sn * 16)) =
                     codes4(acc[sm][sn], m, s);
         }
+        lds_barrier();
+        store_tile<BM, BNO, THREADS>(lds, static_cast<uint8_t*>(p.out) + m0 * F + n0, F, live);
     }
 }
 
@@ -326,36 +395,50 @@ hipError_t launch_gated_swapab(const GatedArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-#define BFQ_GATED_STD(BM, BN, WM, WN, SC, WL)                                                   \
+// The last four arguments are what the tile rule knows of a kernel: the workgroups a CU holds, and
+// its times in microseconds (GatedKernel).
+#define BFQ_GATED_STD(BM, BN, WM, WN, SC, WL, OCC, LAT, THR, FIX)                               \
     GatedKernel{bfq_tile{0, BM, (BN) / 2, 128, 1, WM, WN, 2, 8, SC, 0, 0}, WL,                  \
-                (SC) == 3 ? S_UE8M0 : S_FP32, &launch_gated_std<BM, BN, WM, WN, SC, WL>}
-#define BFQ_GATED_SAB(MT, NWR, NW, KW, D, WL, CH, L)                                            \
+                (SC) == 3 ? S_UE8M0 : S_FP32, &launch_gated_std<BM, BN, WM, WN, SC, WL>, OCC, LAT, THR, FIX}
+#define BFQ_GATED_SAB1(MT, NWR, NW, KW, D, WL, CH, L, OCC, LAT, THR, FIX)                       \
     GatedKernel{bfq_tile{1, MT, (NWR) / 2 * (NW), 128, 1, KW, NW, D, 1, L, 0, 0}, WL,           \
-                (CH) == 2 ? S_PACKED : S_FP32, &launch_gated_swapab<MT, NWR, NW, KW, D, WL, CH, L>}
-#define BFQ_GATED_STD2(...) BFQ_GATED_STD(__VA_ARGS__, W_ROW), BFQ_GATED_STD(__VA_ARGS__, W_PACKED16)
-#define BFQ_GATED_SAB4(MT, NWR, NW, KW, D, L)                                                   \
-    BFQ_GATED_SAB(MT, NWR, NW, KW, D, W_ROW, 0, L), BFQ_GATED_SAB(MT, NWR, NW, KW, D, W_PACKED16, 0, L), \
-        BFQ_GATED_SAB(MT, NWR, NW, KW, D, W_ROW, 2, L), BFQ_GATED_SAB(MT, NWR, NW, KW, D, W_PACKED16, 2, L)
+                (CH) == 2 ? S_PACKED : S_FP32,                                                 \
+                &launch_gated_swapab<MT, NWR, NW, KW, D, WL, CH, L>, OCC, LAT, THR, FIX}
+#define BFQ_GATED_SAB(MT, NWR, NW, KW, D, WL, L, OCC, LAT, THR, FIX)                            \
+    BFQ_GATED_SAB1(MT, NWR, NW, KW, D, WL, 0, L, OCC, LAT, THR, FIX),                           \
+        BFQ_GATED_SAB1(MT, NWR, NW, KW, D, WL, 2, L, OCC, LAT, THR, FIX)
 
 static const GatedKernel kGatedKernels[] = {
-    BFQ_GATED_STD2(256, 256, 4, 2, 0),
-    BFQ_GATED_STD2(256, 256, 4, 2, 1),
-    BFQ_GATED_STD2(256, 256, 4, 2, 3),
-    BFQ_GATED_STD2(128, 256, 2, 2, 0),
-    BFQ_GATED_STD2(128, 256, 2, 2, 3),
-    BFQ_GATED_STD2(128, 128, 2, 2, 0),
-    BFQ_GATED_STD2(128, 128, 2, 2, 3),
-    BFQ_GATED_STD2(64, 128, 1, 2, 0),
-    BFQ_GATED_SAB4(16, 32, 1, 8, 4, 0),
-    BFQ_GATED_SAB4(16, 32, 1, 4, 4, 0),
-    BFQ_GATED_SAB4(16, 32, 8, 1, 4, 0),
-    BFQ_GATED_SAB4(16, 32, 8, 1, 4, 1),
-    BFQ_GATED_SAB4(32, 32, 8, 1, 4, 1),
-    BFQ_GATED_SAB4(32, 32, 4, 2, 4, 1),
-    BFQ_GATED_SAB4(64, 32, 8, 1, 4, 1),
-    BFQ_GATED_SAB4(64, 32, 4, 2, 4, 1),
-    BFQ_GATED_SAB4(128, 32, 8, 1, 4, 1),
-    BFQ_GATED_SAB4(128, 32, 4, 1, 4, 1),
+    BFQ_GATED_STD(64, 128, 1, 2, 0, W_ROW, 3, 0.988f, 0.397f, 3.429f),
+    BFQ_GATED_STD(64, 128, 1, 2, 0, W_PACKED16, 3, 0.943f, 0.385f, 3.607f),
+    BFQ_GATED_STD(128, 128, 2, 2, 0, W_ROW, 2, 1.152f, 0.469f, 3.644f),
+    BFQ_GATED_STD(128, 128, 2, 2, 0, W_PACKED16, 2, 1.183f, 0.002f, 3.830f),
+    BFQ_GATED_STD(128, 128, 2, 2, 3, W_ROW, 2, 0.704f, 0.426f, 3.026f),
+    BFQ_GATED_STD(128, 128, 2, 2, 3, W_PACKED16, 2, 0.663f, 0.409f, 3.445f),
+    BFQ_GATED_STD(128, 256, 2, 2, 3, W_ROW, 1, 1.092f, 0.527f, 4.171f),
+    BFQ_GATED_STD(128, 256, 2, 2, 3, W_PACKED16, 1, 1.140f, 0.093f, 4.577f),
+    BFQ_GATED_STD(256, 256, 4, 2, 0, W_ROW, 1, 1.846f, 0.571f, 3.386f),
+    BFQ_GATED_STD(256, 256, 4, 2, 0, W_PACKED16, 1, 1.751f, 0.001f, 3.582f),
+    BFQ_GATED_STD(256, 256, 4, 2, 1, W_ROW, 1, 1.798f, 1.120f, 3.769f),
+    BFQ_GATED_STD(256, 256, 4, 2, 1, W_PACKED16, 1, 1.714f, 1.314f, 4.216f),
+    BFQ_GATED_STD(256, 256, 4, 2, 3, W_ROW, 1, 1.694f, 0.506f, 2.496f),
+    BFQ_GATED_STD(256, 256, 4, 2, 3, W_PACKED16, 1, 1.584f, 1.043f, 3.180f),
+    BFQ_GATED_SAB(16, 32, 1, 4, 4, W_ROW, 0, 4, 0.002f, 0.218f, 2.090f),
+    BFQ_GATED_SAB(16, 32, 1, 4, 4, W_PACKED16, 0, 4, 0.001f, 0.129f, 1.719f),
+    BFQ_GATED_SAB(16, 32, 1, 4, 8, W_ROW, 0, 2, 0.001f, 0.166f, 4.299f),
+    BFQ_GATED_SAB(16, 32, 1, 4, 8, W_PACKED16, 0, 2, 0.000f, 0.105f, 2.726f),
+    BFQ_GATED_SAB(16, 32, 1, 8, 4, W_ROW, 0, 2, 0.001f, 0.206f, 3.114f),
+    BFQ_GATED_SAB(16, 32, 1, 8, 4, W_PACKED16, 0, 2, 0.000f, 0.121f, 2.425f),
+    BFQ_GATED_SAB(32, 32, 2, 4, 4, W_ROW, 1, 2, 0.002f, 0.416f, 3.772f),
+    BFQ_GATED_SAB(32, 32, 2, 4, 4, W_PACKED16, 1, 2, 0.000f, 0.271f, 3.656f),
+    BFQ_GATED_SAB(32, 32, 8, 1, 4, W_ROW, 1, 2, 0.000f, 1.392f, 4.279f),
+    BFQ_GATED_SAB(32, 32, 8, 1, 4, W_PACKED16, 1, 2, 0.000f, 0.759f, 4.292f),
+    BFQ_GATED_SAB(64, 32, 2, 4, 4, W_ROW, 1, 1, 0.699f, 0.448f, 5.080f),
+    BFQ_GATED_SAB(64, 32, 2, 4, 4, W_PACKED16, 1, 1, 0.903f, 0.294f, 5.115f),
+    BFQ_GATED_SAB(64, 32, 8, 1, 4, W_ROW, 1, 1, 1.345f, 0.002f, 4.972f),
+    BFQ_GATED_SAB(64, 32, 8, 1, 4, W_PACKED16, 1, 1, 0.732f, 0.577f, 4.874f),
+    BFQ_GATED_SAB(128, 32, 8, 1, 4, W_ROW, 1, 1, 1.481f, 0.994f, 6.356f),
+    BFQ_GATED_SAB(128, 32, 8, 1, 4, W_PACKED16, 1, 1, 1.090f, 0.000f, 6.339f),
 };
 
 const GatedKernel* gated_kernels(int* count) {

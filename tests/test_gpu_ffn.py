@@ -116,8 +116,6 @@ def _twin(bfq, t, wl):
          "sched": 3 if t.sched == 3 and t.variant == 0 else 0, "split_k": t.split_k}
     if t.variant == 1 and t.waves_m >= 4:
         d.update(variant=1, bm=16, bn=16, waves_m=t.waves_m, waves_n=1, stages=4, sched=0, group_m=1)
-    elif t.variant == 1 and t.waves_m == 2:
-        d.update(variant=1, bm=32, bn=64, waves_m=2, waves_n=4, stages=4, sched=1, group_m=1)
     elif t.variant == 1 and wl == bfq.BFQ_W_ROW_MAJOR:
         d.update(variant=1, bm=32, bn=128, waves_m=1, waves_n=8, stages=4, sched=1, group_m=1)
     return bfq.bfq_tile.from_dict(d)
@@ -213,6 +211,10 @@ def test_gated_selected_tile_and_layouts(bfq, M, F, K, a_lay, o_lay, sfmt):
             sa_in = bfq.quant_tokens(synth.activations(M, K, seed=M + F).to(DEV), scale_fmt=sfmt, layout=2)[1]
         out, _, _ = _run_gated(bfq, qa, sa_in, qw, sw, torch.bfloat16, 0, None, wl, sfmt, False, a_lay)
         _within(out, h, tol + H[torch.bfloat16] * h.abs(), f"{t.as_dict()}")
+        # the rule may pick another tile when codes are wanted
+        t = bfq.bfq_gated_select_tile(M, F, K, bfq.BFQ_E4M3FN, wl, sfmt)
+        gu = _gu(bfq, qa, sa, qw, sw, t, wl, sfmt)
+        h, tol = _h_ref(gu, 0)
         q, s, pre = _run_gated(bfq, qa, sa_in, qw, sw, torch.uint8, 0, None, wl, sfmt, True, a_lay, o_lay)
         _check_codes(q, _unpack_scales(bfq, s, o_lay, M, F // 128), h, tol, sfmt == 1, f"{t.as_dict()}")
         assert torch.equal(pre, gu.bfloat16())
@@ -253,6 +255,8 @@ def test_gated_special_values(bfq):
             out = bfq.gated_gemm(qa, sa, qw, sw, act=act, out_dtype=torch.float32, w_layout=wl)
             _within(out, h, tol + U * h.abs(), f"wl {wl} act {act}")
             assert bool((out[0] == 0).all()) and bool(out[2].isnan().all())
+            tc = bfq.bfq_gated_select_tile(40, F, K, bfq.BFQ_E4M3FN, wl)
+            h, tol = _h_ref(_gu(bfq, qa, sa, qw, sw, tc, wl, 0), act)
             q, s = bfq.gated_gemm(qa, sa, qw, sw, act=act, codes=True, w_layout=wl)
             assert not bool(q[0].view(torch.float8_e4m3fn).float().any())
             assert torch.equal(s[0], torch.full_like(s[0], np.float32(1e-10) / np.float32(448)))
