@@ -226,14 +226,16 @@ U8_CODES = ("uint8", "float8_e4m3fn")
 
 
 _torch = None          # torch, once a tensor has been seen (importing the binding does not need it)
+_Tensor = None         # torch.Tensor, likewise
 _DTYPE_NAMES: dict = {}
+_DTYPE_SETS: dict = {}  # tuples of dtype names -> the torch dtypes they name
 
 
 def _torch_module():
-    global _torch
+    global _torch, _Tensor
     if _torch is None:
         import torch
-        _torch = torch
+        _torch, _Tensor = torch, torch.Tensor
     return _torch
 
 
@@ -242,6 +244,17 @@ def _dt(t) -> str:
     if name is None:
         name = _DTYPE_NAMES[t.dtype] = str(t.dtype).replace("torch.", "")
     return name
+
+
+def _is(t, dtypes) -> bool:
+    """A plain tensor of one of these types (what a call is usually given); anything else goes
+    through the checks that say what is wrong."""
+    if t.__class__ is not _Tensor:
+        return False
+    known = _DTYPE_SETS.get(dtypes)
+    if known is None:
+        known = _DTYPE_SETS[dtypes] = frozenset(getattr(_torch, n) for n in dtypes)
+    return t.dtype in known
 
 
 def _tensor(t, name, dtypes):
@@ -259,16 +272,19 @@ def _devices(**tensors):
     cur = None
     for name, t in tensors.items():
         if t is not None and not isinstance(t, int):
-            if t.get_device() < 0:
+            dev = t.get_device()
+            if dev < 0:
                 raise BfqArgumentError(f"{name} is on device {t.device}; the kernels need a GPU tensor")
-            if cur is None:
-                cur = (_torch or _torch_module()).cuda.current_device()
-            if t.get_device() != cur:
+            if cur is None:                    # a GPU tensor exists, so the runtime is initialised
+                cur = (_torch or _torch_module())._C._cuda_getDevice()
+            if dev != cur:
                 raise BfqArgumentError(f"{name} is on {t.device}, not the current device cuda:{cur}")
 
 
 def _rows(t, name, dtypes, rows, cols):
     """A [rows, cols] matrix whose rows are packed at stride cols (what the kernels index)."""
+    if _is(t, dtypes) and t.is_contiguous() and t.shape == (rows, cols):
+        return
     if not _tensor(t, name, dtypes):
         return
     shape = t.shape
@@ -282,6 +298,8 @@ def _rows(t, name, dtypes, rows, cols):
 
 def _flat(t, name, dtypes, numel, exact=True):
     """A contiguous buffer of exactly (or at least) numel elements, any shape."""
+    if _is(t, dtypes) and t.numel() == numel and t.is_contiguous():
+        return
     if not _tensor(t, name, dtypes):
         return
     if (t.numel() != numel) if exact else (t.numel() < numel):
@@ -331,6 +349,10 @@ OUT_DTYPES = ("bfloat16", "float16", "float32")
 
 
 def _shape2(t, name):
+    if t.__class__ is _Tensor:
+        shape = t.shape
+        if len(shape) == 2:
+            return shape
     shape = getattr(t, "shape", ())
     if not hasattr(t, "dim") or len(shape) != 2:
         raise BfqArgumentError(f"{name} must be a 2-D tensor")
@@ -347,9 +369,11 @@ def _same_codes(a, w):
 
 def _stream(stream):
     if stream is None:
-        cuda = (_torch or _torch_module()).cuda
-        raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)   # the handle without a Stream object
-        return raw(cuda.current_device()) if raw else cuda.current_stream().cuda_stream
+        torch = _torch or _torch_module()
+        if not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        # the handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
