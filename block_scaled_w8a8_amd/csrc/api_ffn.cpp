@@ -140,7 +140,7 @@ bfq_tile select_gated(int64_t M, int64_t F, int64_t K, bool codes, int wlayout, 
 bool needs_partials(const bfq_tile& t, bool codes) { return t.split_k > 1 || (codes && t.bn != 128); }
 
 bool gated_too_large(int64_t M, int64_t F, int64_t K) {
-    return M >= kMaxRows || F >= (int64_t(1) << 27) || K > (1 << 23) || too_many_outputs(M, 2 * F) ||
+    return M >= kMaxRows || F >= (int64_t(1) << 26) || K > (1 << 23) || too_many_outputs(M, 2 * F) ||
            too_many_outputs(F, K);
 }
 
@@ -221,7 +221,7 @@ bfq_status bfq_gated_gemm(const void* a_q, const float* a_scales, bfq_scale_layo
     if (M < 0 || F <= 0 || K <= 0 || F % 128 != 0 || K % 128 != 0)
         return fail(BFQ_ERR_SHAPE, "need M >= 0 and F, K positive multiples of 128");
     if (gated_too_large(M, F, K))
-        return fail(BFQ_ERR_SHAPE, "need M < 2^24 - 4, F < 2^27, K <= 2^23, M * 2F < 2^40 and F * K < 2^40");
+        return fail(BFQ_ERR_SHAPE, "need M < 2^24 - 4, F < 2^26, K <= 2^23, M * 2F < 2^40 and F * K < 2^40");
     if (a_scale_ld > (1 << 23)) return fail(BFQ_ERR_SHAPE, "a_scale_ld must be at most 2^23");
     if (!aligned(a_q, 16) || !aligned(w_q, 16) || !aligned(out, 16) || !aligned(preact, 16) ||
         !aligned(a_scales, 4) || !aligned(w_scales, 4) || !aligned(workspace, 16) ||
@@ -316,8 +316,8 @@ bfq_status bfq_gated_backward(const void* preact, const void* dh, bfq_activation
         return fail(BFQ_ERR_DTYPE, "q_dtype must be BFQ_E4M3FN or BFQ_INT8");
     if (M < 0 || F <= 0 || F % 8 != 0 || (q && F % 128 != 0))
         return fail(BFQ_ERR_SHAPE, "need M >= 0 and F a positive multiple of 8 (of 128 with codes)");
-    if (M >= kMaxRows || F >= (int64_t(1) << 27))
-        return fail(BFQ_ERR_SHAPE, "need M < 2^24 - 4 and F < 2^27");
+    if (M >= kMaxRows || F >= (int64_t(1) << 26))
+        return fail(BFQ_ERR_SHAPE, "need M < 2^24 - 4 and F < 2^26");
     if (!aligned(preact, 16) || !aligned(dh, 16) || !aligned(dpre, 16) || !aligned(q, 16) ||
         !aligned(h, 16) || !aligned(scales, 4))
         return fail(BFQ_ERR_ALIGN, "row tensors must be 16-byte aligned, scales 4-byte");

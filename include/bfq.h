@@ -23,6 +23,7 @@
  *  - Shapes are int64; K and N must be multiples of 128 (GEMM: M, N < 2^31, M * N < 2^40,
  *    K <= 2^23, scale ld <= 2^23, and the activation scales of 256 tokens over all K blocks
  *    span less than 4 GiB), and x/q/w/out 16-byte aligned.
+ *  - Buffers of one call do not overlap unless its description says that they may.
  *  - Two calls on one stream are ordered; calls on different streams that share an output
  *    or workspace race.
  */
@@ -365,8 +366,8 @@ bfq_status bfq_moe_get_tile_candidate(bfq_weight_layout w_layout, bfq_scale_form
  *   floor out_eps: the token quantizer's formats, formed from the fp32 products (out_scales,
  *   out_layout, out_scale_ld and out_eps are not read otherwise).
  *   preact: bf16 [M][2F] = (g, u), what bfq_gated_backward reads, or NULL.
- * M >= 0, F and K positive multiples of 128; the limits of bfq_block_gemm with N = 2F, and
- * F * K < 2^40. tile NULL -> bfq_gated_select_tile. The workspace holds
+ * M in [0, 2^24 - 4), F and K positive multiples of 128, F < 2^26, K <= 2^23, M * 2F < 2^40,
+ * F * K < 2^40; activation scales as bfq_block_gemm. tile NULL -> bfq_gated_select_tile. The workspace holds
  * bfq_gated_gemm_workspace_bytes bytes (NULL when that is 0). */
 bfq_status bfq_gated_gemm(const void* a_q, const float* a_scales, bfq_scale_layout a_layout,
                           int64_t a_scale_ld, const void* w_q, const float* w_scales,
@@ -401,7 +402,8 @@ bfq_status bfq_gated_get_tile_candidate(bfq_weight_layout w_layout, bfq_scale_fo
  *   dpre bf16 [M][2F] = (dg, du); q [M][2F] codes with scales, one per 128 columns (the gradient
  *   as the next bfq_block_gemm reads it; layout, scale_ld, q_eps, scale_fmt as in
  *   bfq_quant_tokens with K = 2F, quantized from the fp32 values); h bf16 [M][F], the product
- *   again. F a positive multiple of 8, of 128 with q. q_dtype is read only with q. */
+ *   again. dpre may be preact itself, h may be dh. M < 2^24 - 4; F < 2^26 a positive multiple of
+ *   8, of 128 with q. q_dtype is read only with q. */
 bfq_status bfq_gated_backward(const void* preact, const void* dh, bfq_activation act, void* dpre,
                               void* q, bfq_dtype q_dtype, float* scales, bfq_scale_layout layout,
                               int64_t scale_ld, float q_eps, bfq_scale_format scale_fmt, void* h,
@@ -409,7 +411,7 @@ bfq_status bfq_gated_backward(const void* preact, const void* dh, bfq_activation
 
 /* Row-major weight codes [N][K] and their block scales [N/128][K/128] transposed: wt_q [K][N],
  * wt_scales [K/128][N/128]. An offline step like bfq_pack_weights (which may follow it); separate
- * buffers. N, K multiples of 128. */
+ * buffers. N, K multiples of 128, N < 2^22, K <= 2^23. */
 bfq_status bfq_transpose_weights(const void* w_q, const float* w_scales, int64_t N, int64_t K,
                                  bfq_dtype q_dtype, void* wt_q, float* wt_scales, void* stream);
 
@@ -425,8 +427,8 @@ bfq_status bfq_transpose_weights(const void* w_q, const float* w_scales, int64_t
  *   With w_pre, n is stored as normed bf16 [M][K], as codes q [M][K] with scales (the formats of
  *   bfq_quant_tokens: group_size 128 or K, q_dtype E4M3FN | INT8), or both; both are formed from
  *   the fp32 n, and n from the fp32 r'. Without w_pre, normed and q must be NULL.
- * K a positive multiple of 8 (of 128 with q), at most 16384; norm_eps positive and finite. Row
- * sums of squares are fp32: values past about 1e17 overflow them. */
+ * K a positive multiple of 8 (of 128 with q), at most 16384; M < 2^24 - 4; norm_eps positive and
+ * finite. Row sums of squares are fp32: values past about 1e17 overflow them. */
 bfq_status bfq_norm_residual(const void* y, const void* residual, bfq_dtype res_dtype,
                              const void* w_post, const void* gate, bfq_gate_kind gate_kind,
                              float res_scale, const void* w_pre, float norm_eps, void* res_out,

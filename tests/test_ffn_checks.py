@@ -33,7 +33,7 @@ def test_gated_gemm_refusals(bfq):
     for dt in (E.BFQ_INT8, E.BFQ_INT32, 77):
         assert _gated(bfq, out_dtype=dt) == E.BFQ_ERR_DTYPE
     for kw in (dict(M=-1), dict(F=0), dict(F=64), dict(K=64), dict(K=0), dict(bs=_bs(1, 256)),
-               dict(M=1 << 24), dict(F=1 << 27), dict(K=1 << 24, a_ld=1 << 17), dict(a_ld=1),
+               dict(M=1 << 24), dict(F=1 << 26), dict(K=1 << 24, a_ld=1 << 17), dict(a_ld=1),
                dict(a_layout=1, a_ld=3), dict(a_ld=1 << 24), dict(M=1 << 22, F=1 << 18),
                dict(codes, out_ld=1), dict(codes, out_layout=1, out_ld=3),
                dict(codes, out_ld=1 << 41)):
@@ -126,7 +126,7 @@ def test_gated_backward_and_transpose_refusals(bfq):
     q = dict(q=P, scales=P)
     for kw in (dict(pre=None), dict(dh=None), dict(dpre=None), dict(q=P), dict(scales=P)):
         assert bwd(**kw) == E.BFQ_ERR_NULL, kw
-    for kw in (dict(M=-1), dict(F=0), dict(F=12), dict(q, F=264), dict(M=1 << 24), dict(F=1 << 27),
+    for kw in (dict(M=-1), dict(F=0), dict(F=12), dict(q, F=264), dict(M=1 << 24), dict(F=1 << 26),
                dict(q, ld=3), dict(q, lay=1, ld=3)):
         assert bwd(**kw) == E.BFQ_ERR_SHAPE, kw
     for kw in (dict(act=3), dict(q, eps=0.0), dict(q, fmt=2), dict(q, lay=5), dict(q, lay=2)):

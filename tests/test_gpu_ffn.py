@@ -266,19 +266,21 @@ def test_gated_special_values(bfq):
 
 
 @pytest.mark.parametrize("wl", [0, 1])
-def test_gated_batch_invariant(bfq, wl):
+@pytest.mark.parametrize("sfmt", [0, 1])
+def test_gated_batch_invariant(bfq, wl, sfmt):
     """With the batch-invariant switch set, a token's outputs do not depend on the batch."""
     F, K = 512, 1536
+    kw = dict(w_layout=wl, scale_fmt=sfmt)
     was = bfq.bfq_get_batch_invariant()
     bfq.bfq_set_batch_invariant(True)
     try:
-        qa, sa, qw, sw, _ = _pair(bfq, 600, F, K, 5, 0, wl)
-        full = bfq.gated_gemm(qa, sa, qw, sw, out_dtype=torch.float32, w_layout=wl)
-        qf, sf = bfq.gated_gemm(qa, sa, qw, sw, codes=True, w_layout=wl)
+        qa, sa, qw, sw, _ = _pair(bfq, 600, F, K, 5, sfmt, wl)
+        full = bfq.gated_gemm(qa, sa, qw, sw, out_dtype=torch.float32, **kw)
+        qf, sf = bfq.gated_gemm(qa, sa, qw, sw, codes=True, **kw)
         for M in (1, 16, 30, 64, 100, 129, 513):
-            part = bfq.gated_gemm(qa[:M], sa[:M].contiguous(), qw, sw, out_dtype=torch.float32, w_layout=wl)
+            part = bfq.gated_gemm(qa[:M], sa[:M].contiguous(), qw, sw, out_dtype=torch.float32, **kw)
             assert torch.equal(part, full[:M]), M
-            q, s = bfq.gated_gemm(qa[:M], sa[:M].contiguous(), qw, sw, codes=True, w_layout=wl)
+            q, s = bfq.gated_gemm(qa[:M], sa[:M].contiguous(), qw, sw, codes=True, **kw)
             assert torch.equal(q, qf[:M]) and torch.equal(s, sf[:M]), M
     finally:
         bfq.bfq_set_batch_invariant(was)
@@ -316,6 +318,8 @@ def test_gated_backward_bf16(bfq, M, F, act):
     only = torch.full((M, F), 3.0, dtype=torch.bfloat16, device=DEV)
     bfq.bfq_gated_backward(pre, dh, act=act, h=only)
     assert torch.equal(only, h)
+    bfq.bfq_gated_backward(pre, dh, act=act, dpre=pre, h=dh)            # both in place
+    assert torch.equal(pre, dpre) and torch.equal(dh, h)
 
 
 @pytest.mark.parametrize("lay,sfmt,int8", [(0, 0, False), (1, 0, True), (1, 1, False), (2, 1, False),
@@ -691,6 +695,33 @@ def test_streams_and_graphs(bfq):
         torch.cuda.synchronize()
         torch.ones(1 << 20, device=DEV).sum()
         check()
+
+
+def test_two_streams_at_once(bfq):
+    """Calls in flight on two streams, each with its own workspace and outputs."""
+    M, K, F = 40, 2048, 1024
+    qw, sw = bfq.quant_weight_blocks(_randn(60, 2 * F, K) * 0.02)
+    tile = bfq.bfq_gated_select_tile(M, F, K)
+    tile.split_k = 4
+    n = bfq.bfq_gated_gemm_workspace_bytes(M, F, K, tile=tile)
+    jobs = []
+    for i in range(2):
+        qa, sa = bfq.quant_tokens(synth.activations(M, K, seed=61 + i).to(DEV))
+        c = _norm_case(300, 1544, True, 1, torch.bfloat16, 70 + i)
+        jobs.append((qa, sa, torch.empty(n, dtype=torch.uint8, device=DEV),
+                     torch.empty((M, F), dtype=torch.bfloat16, device=DEV), c, torch.cuda.Stream()))
+    want = [bfq.gated_gemm(qa, sa, qw, sw, tile=tile) for qa, sa, *_ in jobs]
+    rn = [bfq.norm_residual(**c) for *_, c, _ in jobs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for qa, sa, ws, out, c, st in jobs:
+            with torch.cuda.stream(st):
+                bfq.bfq_gated_gemm(qa, sa, qw, sw, out, tile=tile, workspace=ws)
+                got.append(bfq.norm_residual(**c))
+        torch.cuda.synchronize()
+        for w, r, g, (*_, out, _, _) in zip(want, rn, got, jobs):
+            assert torch.equal(out, w) and all(torch.equal(a, b) for a, b in zip(g, r))
 
 
 def test_empty_batches(bfq):
