@@ -76,13 +76,17 @@ bfq_tile gated_tile(int variant, int bm, int bn, int sched, int wlayout) {
     return bfq_tile{};
 }
 
+// Strips of row-major weights that copy whole lines through LDS.
+bool row_strip(const GatedKernel& k) { return k.wlayout == W_ROW && k.tile.variant == 1; }
+
 // Microseconds that a gated product is expected to take with kernel k and its K range in `split`
 // parts. The grid runs in rounds of 256 CUs times the workgroups a CU holds; a round's K block
 // takes the longer of a workgroup's own latency and the CU's throughput over the workgroups it
-// holds (joined smoothly), the whole no less than the weight stream; partials cost a second
-// launch and their bytes twice. The constants, here and beside the kernels, are a fit to 768
-// measured (M, F, K, layout, format, output) points of 9 to 60 configurations each, M 1 to 2048
-// on six (F, K); over them the pick is on average 3.3 % slower than the fastest configuration.
+// holds (joined smoothly), the whole no less than the weight stream (row strips take half of it
+// again for each further bm tokens); partials cost a second launch and their bytes twice. The
+// constants, here and beside the kernels, are a fit to 744 measured (M, F, K, layout, format,
+// output) points of 9 to 60 configurations each, M 1 to 2048 on six (F, K); over them the pick is
+// on average 3.3 % (packed weights) and 2.5 % (row-major) slower than the fastest configuration.
 float gated_us(const GatedKernel& k, int64_t M, int64_t F, int64_t K, bool codes, int split) {
     const bfq_tile& t = k.tile;
     const int64_t groups = ceil_div(M, t.bm) * ceil_div(F, t.bn) * split;
@@ -94,7 +98,8 @@ float gated_us(const GatedKernel& k, int64_t M, int64_t F, int64_t K, bool codes
         return std::sqrt(std::sqrt(a * a * a * a + b * b * b * b)) + k.fix;
     };
     float us = (float)full * round(k.occupancy) + (rest ? round(ceil_div(rest, kNumCUs)) : 0.f);
-    const float stream = 2.f * (float)F * (float)K / (k.wlayout == W_PACKED16 ? 6.11e6f : 4.62e6f);
+    float stream = 2.f * (float)F * (float)K / (k.wlayout == W_PACKED16 ? 6.11e6f : 4.45e6f);
+    if (row_strip(k)) stream *= 0.5f + 0.5f * (float)ceil_div(M, t.bm);
     const float x = us > stream ? stream / us : us / stream, x2 = x * x, x4 = x2 * x2;
     us = (us > stream ? us : stream) * std::sqrt(std::sqrt(std::sqrt(1.f + x4 * x4)));
     if (split > 1 || (codes && t.bn != 128)) us += 2.74f + (float)split * (float)M * (float)F * 16.f / 5.54e6f;
@@ -124,7 +129,10 @@ bfq_tile select_gated(int64_t M, int64_t F, int64_t K, bool codes, int wlayout, 
         const int64_t groups = ceil_div(M, t.bm) * ceil_div(F, t.bn);
         for (int split : {1, 2, 3, 4, 6, 8, 12}) {
             // at least two K blocks a part, and no parts beyond those that fill the CUs
-            if (split > 1 && (split * 2 > KB || groups * (split - 1) >= kNumCUs * k[i].occupancy)) break;
+            // (row strips: none gained from more than three)
+            if (split > 1 && (split * 2 > KB || groups * (split - 1) >= kNumCUs * k[i].occupancy ||
+                              (row_strip(k[i]) && split > 3)))
+                break;
             const float us = gated_us(k[i], M, F, K, codes, split);
             if (us < best_us) {
                 best_us = us;

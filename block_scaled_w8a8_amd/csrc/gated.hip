@@ -298,14 +298,153 @@ __device__ __forceinline__ void gated_finish(const Args& p, v4f (&acc)[SM][2 * S
     }
 }
 
-template <int MT, int NWR, int NWAVES, int KW, int D, int WL, int CH>
+template <int MT, int NWR, int NWAVES, int KW, int D, int CH>
 __global__ __launch_bounds__(64 * NWAVES * KW) void gemm_gated_swapab_kernel(GatedArgs p) {
-    swapab_body<MT, NWR, NWAVES, KW, D, Q_FP8, O_FP32, WL, CH, 0, 1>(p);
+    swapab_body<MT, NWR, NWAVES, KW, D, Q_FP8, O_FP32, W_PACKED16, CH, 0, 1>(p);
 }
 
-template <int MT, int NWR, int NWAVES, int KW, int D, int WL, int CH>
+template <int MT, int NWR, int NWAVES, int KW, int D, int CH>
 __global__ __launch_bounds__(64 * NWAVES * KW) void gemm_gated_swapab_lds_kernel(GatedArgs p) {
-    swapab_lds_body<MT, NWR, NWAVES, KW, D, Q_FP8, O_FP32, WL, CH, 0, 1>(p);
+    swapab_lds_body<MT, NWR, NWAVES, KW, D, Q_FP8, O_FP32, W_PACKED16, CH, 0, 1>(p);
+}
+
+// Row-major weights for a few tokens; the weight stream bounds it. A workgroup takes 16 output
+// columns (16 gate rows, 16 up rows) and its waves every KW-th K block, so that together they walk
+// KW * 128 neighbouring bytes of a row. A fragment load straight from row-major rows takes half a
+// line of each of 16 rows a request, and that stream stays near 4.3 TB/s; here a wave copies
+// whole 128-byte lines of 8 rows a load (1 KB) into a ring of its own, D K blocks of 4 KB, and
+// reads its fragments back. The ring is private to the wave, so the K loop has no barrier: the
+// wave waits until the loads of its oldest block have landed. Chunk c of row r sits in slot
+// c ^ swz(r), as in the standard tiles. Measured, F 18432 x K 7168: 50 us for 1 token
+// (5.3 TB/s of weights) and 52.5 us for 16, against 61 and 62 for direct fragment loads; F 2304:
+// 10.3 us for 16 tokens against 16.
+template <int MT, int KW, int D, int CH>
+__global__ __launch_bounds__(64 * KW) void gemm_gated_rows_kernel(GatedArgs p) {
+    constexpr int SM = MT / 16, BLOCK = 4096;
+    constexpr bool PK = CH == 2;
+    constexpr int kOps = 6 + 3 * SM;                    // vector loads of one K block
+    static_assert((D - 1) * kOps <= 63, "the wait counts loads in six bits");
+    static_assert((KW - 1) * SM * 2048 <= KW * D * BLOCK, "the slices' sums fit the rings");
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const int lane = threadIdx.x & 63;
+    const int wk = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int frow = lane & 15, fgrp = lane >> 4;
+    const int64_t M = p.M, F = p.N, K = p.K, KB = K / 128;
+    const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * MT;
+    const int split = p.split, z = blockIdx.z;
+    const int64_t ks0 = (int64_t)z * KB / split, ks1 = (int64_t)(z + 1) * KB / split;
+    const int64_t L = (ks1 - ks0 - wk + KW - 1) / KW;   // K blocks ks0 + wk, + KW, ..
+    constexpr uint32_t kNoLoad = 0x80000000u;           // past every resource here
+
+    const uint8_t* w = static_cast<const uint8_t*>(p.w);
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(w + n0 * K, (uint32_t)(16 * K));
+    const __amdgpu_buffer_rsrc_t ru = make_rsrc(w + (F + n0) * K, (uint32_t)(16 * K));
+    const int64_t rows_a = M - m0 < MT ? M - m0 : MT;
+    const int64_t ssm = p.sa_stride_m, ssk = p.sa_stride_k, sa_krows = PK ? (KB - 1) / 4 : KB - 1;
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(static_cast<const uint8_t*>(p.a) + m0 * K, (uint32_t)(rows_a * K));
+    const __amdgpu_buffer_rsrc_t rsa =
+        make_rsrc(p.sa + m0 * ssm, (uint32_t)(((rows_a - 1) * ssm + sa_krows * ssk + 1) * 4));
+    uint32_t a_voff[SM], sa_voff[SM];
+#pragma unroll
+    for (int sm = 0; sm < SM; ++sm) {
+        a_voff[sm] = (uint32_t)((sm * 16 + frow) * K + fgrp * 16);
+        sa_voff[sm] = (uint32_t)((sm * 16 + frow) * ssm * 4);
+    }
+    const __amdgpu_buffer_rsrc_t rsg = make_rsrc(p.sw + (n0 / 128) * KB, (uint32_t)(KB * 4));
+    const __amdgpu_buffer_rsrc_t rsu = make_rsrc(p.sw + (F / 128 + n0 / 128) * KB, (uint32_t)(KB * 4));
+    // copy: lane l takes row l / 8 (+ 8), slot l % 8; swz of the second eight rows differs by 1
+    const uint32_t c0 = (uint32_t)((lane >> 3) * K + (((lane & 7) ^ (lane >> 3)) << 4));
+    const uint32_t c1 = (uint32_t)(((lane >> 3) + 8) * K + (((lane & 7) ^ (lane >> 3) ^ 1) << 4));
+    const uint32_t ring = (uint32_t)(wk * D * BLOCK);
+    const uint32_t f0 = (uint32_t)(frow * 128 + ((fgrp ^ swz(frow)) << 4));
+    const uint32_t f1 = (uint32_t)(frow * 128 + (((fgrp + 4) ^ swz(frow)) << 4));
+
+    v4i abuf[D][SM][2];
+    float sab[D][SM], swb[D], swu[D];
+    int kbs[D];
+    auto fetch = [&](int slot, int64_t i) {
+        const bool live = i < L;
+        const int64_t kb = ks0 + wk + i * KW;
+        const uint32_t s = live ? (uint32_t)kb * 128u : kNoLoad;
+        const uint32_t ss = live ? (uint32_t)((PK ? kb >> 2 : kb) * ssk * 4) : kNoLoad;
+        const uint32_t sws = live ? (uint32_t)kb * 4u : kNoLoad;
+        const uint32_t at = ring + (uint32_t)(slot * BLOCK);
+        swb[slot] = buf_f32(rsg, 0, sws);
+        swu[slot] = buf_f32(rsu, 0, sws);
+        kbs[slot] = (int)(kb & 3);
+        dma16(rw, lds, at, c0, s);
+        dma16(rw, lds, at + 1024, c1, s);
+        dma16(ru, lds, at + 2048, c0, s);
+        dma16(ru, lds, at + 3072, c1, s);
+#pragma unroll
+        for (int sm = 0; sm < SM; ++sm) {
+            abuf[slot][sm][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, a_voff[sm], s, 0);
+            abuf[slot][sm][1] = __builtin_amdgcn_raw_buffer_load_b128(ra, a_voff[sm], s + 64u, 0);
+            sab[slot][sm] = buf_f32(rsa, sa_voff[sm], ss);
+        }
+    };
+    v4f acc[SM][2];
+#pragma unroll
+    for (int sm = 0; sm < SM; ++sm) acc[sm][0] = acc[sm][1] = v4f{0.f, 0.f, 0.f, 0.f};
+    auto consume = [&](int slot) {
+        const uint8_t* at = lds + ring + slot * BLOCK;
+        v8i wf[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const v4i lo = *reinterpret_cast<const v4i*>(at + h * 2048 + f0);
+            const v4i hi = *reinterpret_cast<const v4i*>(at + h * 2048 + f1);
+            wf[h] = v8i{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        }
+#pragma unroll
+        for (int sm = 0; sm < SM; ++sm) {
+            const float sav = PK ? e8m0_value(e8m0_byte(__float_as_uint(sab[slot][sm]), kbs[slot])) : sab[slot][sm];
+            const v4i a0 = abuf[slot][sm][0], a1 = abuf[slot][sm][1];
+            const v8i af = v8i{a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const v4f q = mfma_fp8_16x16x128(wf[h], af);
+                const float c = sav * (h ? swu[slot] : swb[slot]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[sm][h][j] = __builtin_fmaf(q[j], c, acc[sm][h][j]);
+            }
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+        fetch(i, i);
+        __builtin_amdgcn_sched_barrier(0);                 // slots in order: the waits count
+    }
+    for (int64_t i0 = 0; i0 < L; i0 += D) {
+#pragma unroll
+        for (int r = 0; r < D; ++r) {
+            // slot r's loads are the oldest in flight; steps past the slice only wait and refill
+            __builtin_amdgcn_sched_barrier(0);
+            wait_vmem_keep((D - 1) * kOps);
+            if (i0 + r < L) consume(r);                    // uniform over the wave
+            __builtin_amdgcn_sched_barrier(0);
+            fetch(r, i0 + r + D);
+        }
+    }
+    wait_vmem_all();       // no copy into LDS may still be in flight when the wave ends
+    // the sums of waves 1 .. KW - 1 through LDS, added in order by wave 0
+    __syncthreads();
+    v4f* red = reinterpret_cast<v4f*>(lds);
+    if (wk > 0) {
+#pragma unroll
+        for (int sm = 0; sm < SM; ++sm)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) red[(((wk - 1) * SM + sm) * 2 + h) * 64 + lane] = acc[sm][h];
+    }
+    __syncthreads();
+    if (wk == 0) {
+#pragma unroll
+        for (int w2 = 0; w2 < KW - 1; ++w2)
+#pragma unroll
+            for (int sm = 0; sm < SM; ++sm)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) acc[sm][h] += red[((w2 * SM + sm) * 2 + h) * 64 + lane];
+    }
+    gated_finish<MT, 16, 1, SM, 1>(p, acc, m0, n0, rows_a, 0, wk, lane);
 }
 
 // ---------------------------------------------------------------- reduce ----
@@ -367,39 +506,55 @@ void gated_activation(int act, float* c1, float* c3) {
 
 // ---------------------------------------------------------------- registry ----
 
-template <int BM, int BN, int WM, int WN, int SCHED, int WL>
-hipError_t launch_gated_std(const GatedArgs& a, hipStream_t stream) {
-    constexpr int LDS_BYTES = StdShape<BM, BN, WM, WN, SCHED>::lds_bytes(2);
-    const int64_t tiles = ((a.M + BM - 1) / BM) * ((a.N + BN / 2 - 1) / (BN / 2));
-    static std::atomic<uint64_t> opted{0};   // devices that opted in to more than 64 KB of LDS
+// A kernel's opt-in to more than 64 KB of LDS, once a device (`opted`: a bit for each).
+static hipError_t opt_in_lds(std::atomic<uint64_t>& opted, const void* kernel, int bytes) {
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
     const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (!(opted.load(std::memory_order_relaxed) & bit)) {
-        e = hipFuncSetAttribute(
-            reinterpret_cast<const void*>(&gemm_gated_std_kernel<BM, BN, WM, WN, SCHED, WL>),
-            hipFuncAttributeMaxDynamicSharedMemorySize, LDS_BYTES);
-        if (e != hipSuccess) return e;
-        opted.fetch_or(bit, std::memory_order_relaxed);
-    }
+    if (opted.load(std::memory_order_relaxed) & bit) return hipSuccess;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess) opted.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
+template <int BM, int BN, int WM, int WN, int SCHED, int WL>
+hipError_t launch_gated_std(const GatedArgs& a, hipStream_t stream) {
+    constexpr int LDS_BYTES = StdShape<BM, BN, WM, WN, SCHED>::lds_bytes(2);
+    const int64_t tiles = ((a.M + BM - 1) / BM) * ((a.N + BN / 2 - 1) / (BN / 2));
+    static std::atomic<uint64_t> opted{0};
+    const hipError_t e = opt_in_lds(
+        opted, reinterpret_cast<const void*>(&gemm_gated_std_kernel<BM, BN, WM, WN, SCHED, WL>), LDS_BYTES);
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL((gemm_gated_std_kernel<BM, BN, WM, WN, SCHED, WL>),
                        dim3((unsigned)tiles, 1, (unsigned)a.split), dim3(64 * WM * WN), LDS_BYTES,
                        stream, a);
     return hipGetLastError();
 }
 
-template <int MT, int NWR, int NWAVES, int KW, int D, int WL, int CH, int LDS>
+template <int MT, int NWR, int NWAVES, int KW, int D, int CH, int LDS>
 hipError_t launch_gated_swapab(const GatedArgs& a, hipStream_t stream) {
     const int64_t cols = NWR / 2 * NWAVES, strips = (a.N + cols - 1) / cols;
     const dim3 grid((unsigned)strips, (unsigned)((a.M + MT - 1) / MT), (unsigned)a.split);
     const dim3 block(64 * NWAVES * KW);
     if constexpr (LDS)
-        hipLaunchKernelGGL((gemm_gated_swapab_lds_kernel<MT, NWR, NWAVES, KW, D, WL, CH>), grid,
+        hipLaunchKernelGGL((gemm_gated_swapab_lds_kernel<MT, NWR, NWAVES, KW, D, CH>), grid,
                            block, 0, stream, a);
     else
-        hipLaunchKernelGGL((gemm_gated_swapab_kernel<MT, NWR, NWAVES, KW, D, WL, CH>), grid, block,
+        hipLaunchKernelGGL((gemm_gated_swapab_kernel<MT, NWR, NWAVES, KW, D, CH>), grid, block,
                            0, stream, a);
+    return hipGetLastError();
+}
+
+template <int MT, int KW, int D, int CH>
+hipError_t launch_gated_rows(const GatedArgs& a, hipStream_t stream) {
+    constexpr int LDS_BYTES = KW * D * 4096;
+    static std::atomic<uint64_t> opted{0};
+    const hipError_t e =
+        opt_in_lds(opted, reinterpret_cast<const void*>(&gemm_gated_rows_kernel<MT, KW, D, CH>), LDS_BYTES);
+    if (e != hipSuccess) return e;
+    const dim3 grid((unsigned)(a.N / 16), (unsigned)((a.M + MT - 1) / MT), (unsigned)a.split);
+    hipLaunchKernelGGL((gemm_gated_rows_kernel<MT, KW, D, CH>), grid, dim3(64 * KW), LDS_BYTES, stream, a);
     return hipGetLastError();
 }
 
@@ -408,45 +563,46 @@ hipError_t launch_gated_swapab(const GatedArgs& a, hipStream_t stream) {
 #define BFQ_GATED_STD(BM, BN, WM, WN, SC, WL, OCC, LAT, THR, FIX)                               \
     GatedKernel{bfq_tile{0, BM, (BN) / 2, 128, 1, WM, WN, 2, 8, SC, 0, 0}, WL,                  \
                 (SC) == 3 ? S_UE8M0 : S_FP32, &launch_gated_std<BM, BN, WM, WN, SC, WL>, OCC, LAT, THR, FIX}
-#define BFQ_GATED_SAB1(MT, NWR, NW, KW, D, WL, CH, L, OCC, LAT, THR, FIX)                       \
-    GatedKernel{bfq_tile{1, MT, (NWR) / 2 * (NW), 128, 1, KW, NW, D, 1, L, 0, 0}, WL,           \
+#define BFQ_GATED_SAB1(MT, NWR, NW, KW, D, CH, L, OCC, LAT, THR, FIX)                           \
+    GatedKernel{bfq_tile{1, MT, (NWR) / 2 * (NW), 128, 1, KW, NW, D, 1, L, 0, 0}, W_PACKED16,   \
                 (CH) == 2 ? S_PACKED : S_FP32,                                                 \
-                &launch_gated_swapab<MT, NWR, NW, KW, D, WL, CH, L>, OCC, LAT, THR, FIX}
-#define BFQ_GATED_SAB(MT, NWR, NW, KW, D, WL, L, OCC, LAT, THR, FIX)                            \
-    BFQ_GATED_SAB1(MT, NWR, NW, KW, D, WL, 0, L, OCC, LAT, THR, FIX),                           \
-        BFQ_GATED_SAB1(MT, NWR, NW, KW, D, WL, 2, L, OCC, LAT, THR, FIX)
+                &launch_gated_swapab<MT, NWR, NW, KW, D, CH, L>, OCC, LAT, THR, FIX}
+#define BFQ_GATED_SAB(MT, NWR, NW, KW, D, L, OCC, LAT, THR, FIX)                                \
+    BFQ_GATED_SAB1(MT, NWR, NW, KW, D, 0, L, OCC, LAT, THR, FIX),                           \
+        BFQ_GATED_SAB1(MT, NWR, NW, KW, D, 2, L, OCC, LAT, THR, FIX)
+
+#define BFQ_GATED_ROWS1(MT, KW, D, CH, OCC, LAT, THR, FIX)                                      \
+    GatedKernel{bfq_tile{1, MT, 16, 128, 1, KW, 1, D, 1, 2, 0, 0}, W_ROW,                       \
+                (CH) == 2 ? S_PACKED : S_FP32, &launch_gated_rows<MT, KW, D, CH>, OCC, LAT, THR, FIX}
+#define BFQ_GATED_ROWS(MT, KW, D, OCC, LAT, THR, FIX)                                           \
+    BFQ_GATED_ROWS1(MT, KW, D, 0, OCC, LAT, THR, FIX), BFQ_GATED_ROWS1(MT, KW, D, 2, OCC, LAT, THR, FIX)
 
 static const GatedKernel kGatedKernels[] = {
-    BFQ_GATED_STD(64, 128, 1, 2, 0, W_ROW, 3, 0.988f, 0.397f, 3.429f),
+    BFQ_GATED_STD(64, 128, 1, 2, 0, W_ROW, 3, 1.006f, 0.373f, 6.348f),
     BFQ_GATED_STD(64, 128, 1, 2, 0, W_PACKED16, 3, 0.943f, 0.385f, 3.607f),
-    BFQ_GATED_STD(128, 128, 2, 2, 0, W_ROW, 2, 1.152f, 0.469f, 3.644f),
+    BFQ_GATED_STD(128, 128, 2, 2, 0, W_ROW, 2, 1.185f, 0.494f, 5.811f),
     BFQ_GATED_STD(128, 128, 2, 2, 0, W_PACKED16, 2, 1.183f, 0.002f, 3.830f),
-    BFQ_GATED_STD(128, 128, 2, 2, 3, W_ROW, 2, 0.704f, 0.426f, 3.026f),
+    BFQ_GATED_STD(128, 128, 2, 2, 3, W_ROW, 2, 0.757f, 0.397f, 6.009f),
     BFQ_GATED_STD(128, 128, 2, 2, 3, W_PACKED16, 2, 0.663f, 0.409f, 3.445f),
-    BFQ_GATED_STD(128, 256, 2, 2, 3, W_ROW, 1, 1.092f, 0.527f, 4.171f),
+    BFQ_GATED_STD(128, 256, 2, 2, 3, W_ROW, 1, 1.113f, 0.000f, 6.514f),
     BFQ_GATED_STD(128, 256, 2, 2, 3, W_PACKED16, 1, 1.140f, 0.093f, 4.577f),
-    BFQ_GATED_STD(256, 256, 4, 2, 0, W_ROW, 1, 1.846f, 0.571f, 3.386f),
+    BFQ_GATED_STD(256, 256, 4, 2, 0, W_ROW, 1, 1.878f, 0.000f, 5.823f),
     BFQ_GATED_STD(256, 256, 4, 2, 0, W_PACKED16, 1, 1.751f, 0.001f, 3.582f),
-    BFQ_GATED_STD(256, 256, 4, 2, 1, W_ROW, 1, 1.798f, 1.120f, 3.769f),
-    BFQ_GATED_STD(256, 256, 4, 2, 1, W_PACKED16, 1, 1.714f, 1.314f, 4.216f),
-    BFQ_GATED_STD(256, 256, 4, 2, 3, W_ROW, 1, 1.694f, 0.506f, 2.496f),
+    BFQ_GATED_STD(256, 256, 4, 2, 1, W_ROW, 1, 1.855f, 0.772f, 6.652f),
+    BFQ_GATED_STD(256, 256, 4, 2, 3, W_ROW, 1, 1.601f, 1.200f, 4.902f),
     BFQ_GATED_STD(256, 256, 4, 2, 3, W_PACKED16, 1, 1.584f, 1.043f, 3.180f),
-    BFQ_GATED_SAB(16, 32, 1, 4, 4, W_ROW, 0, 4, 0.002f, 0.218f, 2.090f),
-    BFQ_GATED_SAB(16, 32, 1, 4, 4, W_PACKED16, 0, 4, 0.001f, 0.129f, 1.719f),
-    BFQ_GATED_SAB(16, 32, 1, 4, 8, W_ROW, 0, 2, 0.001f, 0.166f, 4.299f),
-    BFQ_GATED_SAB(16, 32, 1, 4, 8, W_PACKED16, 0, 2, 0.000f, 0.105f, 2.726f),
-    BFQ_GATED_SAB(16, 32, 1, 8, 4, W_ROW, 0, 2, 0.001f, 0.206f, 3.114f),
-    BFQ_GATED_SAB(16, 32, 1, 8, 4, W_PACKED16, 0, 2, 0.000f, 0.121f, 2.425f),
-    BFQ_GATED_SAB(32, 32, 2, 4, 4, W_ROW, 1, 2, 0.002f, 0.416f, 3.772f),
-    BFQ_GATED_SAB(32, 32, 2, 4, 4, W_PACKED16, 1, 2, 0.000f, 0.271f, 3.656f),
-    BFQ_GATED_SAB(32, 32, 8, 1, 4, W_ROW, 1, 2, 0.000f, 1.392f, 4.279f),
-    BFQ_GATED_SAB(32, 32, 8, 1, 4, W_PACKED16, 1, 2, 0.000f, 0.759f, 4.292f),
-    BFQ_GATED_SAB(64, 32, 2, 4, 4, W_ROW, 1, 1, 0.699f, 0.448f, 5.080f),
-    BFQ_GATED_SAB(64, 32, 2, 4, 4, W_PACKED16, 1, 1, 0.903f, 0.294f, 5.115f),
-    BFQ_GATED_SAB(64, 32, 8, 1, 4, W_ROW, 1, 1, 1.345f, 0.002f, 4.972f),
-    BFQ_GATED_SAB(64, 32, 8, 1, 4, W_PACKED16, 1, 1, 0.732f, 0.577f, 4.874f),
-    BFQ_GATED_SAB(128, 32, 8, 1, 4, W_ROW, 1, 1, 1.481f, 0.994f, 6.356f),
-    BFQ_GATED_SAB(128, 32, 8, 1, 4, W_PACKED16, 1, 1, 1.090f, 0.000f, 6.339f),
+    BFQ_GATED_ROWS(16, 1, 4, 10, 0.167f, 0.092f, 4.436f),
+    BFQ_GATED_ROWS(16, 2, 4, 5, 0.000f, 0.114f, 4.298f),
+    BFQ_GATED_ROWS(16, 4, 3, 3, 0.000f, 0.108f, 4.429f),
+    BFQ_GATED_ROWS(32, 2, 4, 5, 0.000f, 0.169f, 4.305f),
+    BFQ_GATED_ROWS(64, 2, 3, 4, 0.002f, 0.261f, 4.933f),
+    BFQ_GATED_SAB(16, 32, 1, 4, 4, 0, 4, 0.001f, 0.129f, 1.719f),
+    BFQ_GATED_SAB(16, 32, 1, 4, 8, 0, 2, 0.000f, 0.105f, 2.726f),
+    BFQ_GATED_SAB(32, 32, 2, 4, 4, 1, 2, 0.000f, 0.271f, 3.656f),
+    BFQ_GATED_SAB(32, 32, 8, 1, 4, 1, 2, 0.000f, 0.759f, 4.292f),
+    BFQ_GATED_SAB(64, 32, 2, 4, 4, 1, 1, 0.903f, 0.294f, 5.115f),
+    BFQ_GATED_SAB(64, 32, 8, 1, 4, 1, 1, 0.732f, 0.577f, 4.874f),
+    BFQ_GATED_SAB(128, 32, 8, 1, 4, 1, 1, 1.090f, 0.000f, 6.339f),
 };
 
 const GatedKernel* gated_kernels(int* count) {

@@ -114,15 +114,34 @@ def _twin(bfq, t, wl):
     """The block-GEMM tile that forms the same sums in the same order as gated tile t."""
     d = {"variant": 0, "bm": 128, "bn": 128, "waves_m": 2, "waves_n": 2, "stages": 2, "group_m": 8,
          "sched": 3 if t.sched == 3 and t.variant == 0 else 0, "split_k": t.split_k}
-    if t.variant == 1 and t.waves_m >= 4:
+    if t.variant == 1 and t.waves_m >= 4 and t.sched != 2:
         d.update(variant=1, bm=16, bn=16, waves_m=t.waves_m, waves_n=1, stages=4, sched=0, group_m=1)
-    elif t.variant == 1 and wl == bfq.BFQ_W_ROW_MAJOR:
-        d.update(variant=1, bm=32, bn=128, waves_m=1, waves_n=8, stages=4, sched=1, group_m=1)
     return bfq.bfq_tile.from_dict(d)
+
+
+def _gu_interleaved(bfq, qa, sa, qw, sw, t, sfmt):
+    """The row strips' sums: the waves of a workgroup take every waves_m-th K block of a part, each
+    in ascending order; their sums are added in the waves' order and the parts' in the parts'."""
+    KB, one = qa.shape[1] // 128, bfq.bfq_tile.from_dict({**_twin(bfq, t, 0).as_dict(), "split_k": 1})
+    total = None
+    for z in range(t.split_k):
+        part = None
+        for w in range(t.waves_m):
+            blocks = torch.arange(z * KB // t.split_k + w, (z + 1) * KB // t.split_k, t.waves_m, device=DEV)
+            if len(blocks):
+                cols = (blocks[:, None] * 128 + torch.arange(128, device=DEV)).flatten()
+                x = bfq.block_gemm(qa[:, cols].contiguous(), sa[:, blocks].contiguous(),
+                                   qw[:, cols].contiguous(), sw[:, blocks].contiguous(),
+                                   out_dtype=torch.float32, tile=one, w_layout=0, scale_fmt=sfmt)
+                part = x if part is None else part + x
+        total = part if total is None else total + part
+    return total.double()
 
 
 def _gu(bfq, qa, sa, qw, sw, t, wl, sfmt):
     """(g, u) of gated tile t: the fp32 output of its twin on the 2F rows."""
+    if t.variant == 1 and t.sched == 2:
+        return _gu_interleaved(bfq, qa, sa, qw, sw, t, sfmt)
     gu = bfq.block_gemm(qa, sa, qw, sw, out_dtype=torch.float32, tile=_twin(bfq, t, wl),
                         w_layout=wl, scale_fmt=sfmt)
     return gu.double()
