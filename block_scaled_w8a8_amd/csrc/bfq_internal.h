@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/bfq.h"
 
 namespace bfq {
@@ -201,5 +203,17 @@ int mfma_peak_mfmas_per_wave_iter();
 // int8 per-K-block int32 partials [K/128][M][N] (test support).
 hipError_t launch_block_partials_i32(const void* a, const void* w, int32_t* out, int64_t M,
                                      int64_t N, int64_t K, hipStream_t stream);
+
+// A kernel's opt-in to more than 64 KB of LDS, once a device (`opted`: a bit for each).
+inline hipError_t opt_in_lds(std::atomic<uint64_t>& opted, const void* kernel, int bytes) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (opted.load(std::memory_order_relaxed) & bit) return hipSuccess;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess) opted.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 }  // namespace bfq

@@ -12,8 +12,6 @@
 //
 // What bounds the forward kernels is what bounds the block GEMM's: the weight stream at decode
 // sizes, the operand bytes through a CU's L1 and the scale step at large M.
-#include <atomic>
-
 #include "activation.h"
 #include "gemm_std_tile.h"
 #include "gemm_swapab_body.h"
@@ -505,18 +503,6 @@ void gated_activation(int act, float* c1, float* c3) {
 }
 
 // ---------------------------------------------------------------- registry ----
-
-// A kernel's opt-in to more than 64 KB of LDS, once a device (`opted`: a bit for each).
-static hipError_t opt_in_lds(std::atomic<uint64_t>& opted, const void* kernel, int bytes) {
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return e;
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (opted.load(std::memory_order_relaxed) & bit) return hipSuccess;
-    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == hipSuccess) opted.fetch_or(bit, std::memory_order_relaxed);
-    return e;
-}
 
 template <int BM, int BN, int WM, int WN, int SCHED, int WL>
 hipError_t launch_gated_std(const GatedArgs& a, hipStream_t stream) {

@@ -6,7 +6,8 @@
 // GEMMs read (the token quantizer's formats), or both. All of it in fp32; n is taken from the
 // unrounded r' and quantized unrounded, so storing r' or n as bf16 costs the codes nothing.
 //
-// What bounds it: bytes. A row is read once (y, r) and written once (r', codes), everything
+// What bounds it: bytes. 4096 rows of 7168 with post norm, codes out: 46 us, 206 MB at 4.4 TB/s
+// (a large copy reaches 4.8). A row is read once (y, r) and written once (r', codes), everything
 // between stays in registers: P chunks of 8 elements a thread, chunk c of the row held by thread
 // c % T in slot c / T, so 16 neighbouring lanes own one 128-element group as in the token
 // quantizer. Each norm costs one reduction over the workgroup (DPP within a wave, LDS across).
@@ -225,11 +226,18 @@ __global__ __launch_bounds__(kNormThreads<P>) void norm_residual_kernel(NormArgs
 //   rows (CHANNEL) or the row (TOKEN).
 // Two reductions a row: {sum r'^2, sum y^2, sum w_pre*dn*r'} together (the means are these times
 // powers of rms), then {sum dz*z, sum dgate}. A workgroup walks rows blockIdx.x, + gridDim.x, ...
-// with the next row's loads in flight (P = 1; a second chunk a thread leaves no registers for
-// them), and keeps its share of the column sums in registers, 16 a chunk: dn * r^, and
-// alpha*dr*y^ (CHANNEL: times w_post it is the gate's gradient, times the gate w_post's) or dz*y^
-// (else). Each workgroup writes its shares once; norm_columns_kernel adds them in workgroup order,
-// so equal inputs give equal sums. The channel vectors wait in LDS.
+// with the next row's loads in flight and keeps its share of the column sums, 16 a chunk: dn * r^,
+// and alpha*dr*y^ (CHANNEL: times w_post it is the gate's gradient, times the gate w_post's) or
+// dz*y^ (else). Each workgroup writes its shares once; norm_columns_kernel adds them in workgroup
+// order, so equal inputs give equal sums.
+// One chunk a thread (P = 1): the sums stay in registers, the channel vectors wait in LDS. Two
+// (K > 8192): registers hold a row only, so the sums live in LDS (each thread its own slots), the
+// vectors come from L2, and the next row's loads start once their registers are free, all but y's
+// before the second reduction.
+// Bytes bound it. Measured: 4096 rows of 7168 bf16 with a channel gate 86 us with the column sums
+// (352 MB, 4.1 TB/s; two chunks a thread there 96), 4096 of 8192 fp32 127 us (4.8 TB/s; 140),
+// 1024 of 16384 fp32 85 us (3.6 TB/s: four rows a CU, the first and last uncovered; with the sums
+// of two chunks in registers, which spill, 138).
 template <int P, int RF32>
 __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
     const int t = threadIdx.x, T = blockDim.x;
@@ -237,7 +245,9 @@ __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
     const uint32_t row16 = (uint32_t)(2 * K), row_res = RF32 ? 2 * row16 : row16;
     const float fK = (float)K;
     __shared__ __attribute__((aligned(16))) float red[2][5 * 16];
-    extern __shared__ v4u vec[];                         // [3][T * P]: w_pre, w_post, channel gate
+    // P = 1: [3][T] vectors (w_pre, w_post, channel gate); P = 2: [2 sums][2 halves][2T] floats
+    extern __shared__ v4u vec[];
+    v4f* const sums = reinterpret_cast<v4f*>(vec);
     const bool channel = p.gate_kind == BFQ_GATE_CHANNEL, elements = p.gate_kind == BFQ_GATE_FULL;
     const bool post = p.w_post != nullptr;
     struct Row {
@@ -246,9 +256,12 @@ __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
     };
     // element gates of row m
     auto gate_rsrc = [&](int64_t m) { return row_rsrc(elements && m < p.M ? p.gate : nullptr, m, row16); };
-    float apre[P][8], apost[P][8];
+    float apre[1][8], apost[1][8];                       // P = 1
     block_sum_init(red[0], 160);
-    auto load = [&](Row (&x)[P], int64_t m) {
+    const __amdgpu_buffer_rsrc_t v_pre = row_rsrc(p.w_pre, 0, row16), v_post = row_rsrc(p.w_post, 0, row16),
+                                 v_gate = row_rsrc(channel ? p.gate : nullptr, 0, row16);
+    // row m's operands, y and / or the others (constants); the stream's gradient is needed last
+    auto load = [&](Row (&x)[P], int64_t m, bool y, bool others) {
         const bool in = m < p.M;
         const __amdgpu_buffer_rsrc_t rr = row_rsrc(in && p.w_pre ? p.residual : nullptr, m, row_res),
                                      rd = row_rsrc(in ? p.d_res_out : nullptr, m, row_res),
@@ -257,31 +270,57 @@ __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
 #pragma unroll
         for (int u = 0; u < P; ++u) {
             const uint32_t voff = (uint32_t)(u * T + t) * 16;
-            x[u].r.load(rr, voff);
-            x[u].n = load16(rn, voff);
-            x[u].y = load16(ry, voff);
-            x[u].d.load(rd, voff);
+            if (others) {
+                x[u].r.load(rr, voff);
+                x[u].n = load16(rn, voff);
+            }
+            if (y) x[u].y = load16(ry, voff);
+            if (others) x[u].d.load(rd, voff);
         }
     };
     Row cur[P];
-    load(cur, blockIdx.x);
-    {
-        const __amdgpu_buffer_rsrc_t r0 = row_rsrc(p.w_pre, 0, row16), r1 = row_rsrc(p.w_post, 0, row16),
-                                     r2 = row_rsrc(channel ? p.gate : nullptr, 0, row16);
+    load(cur, blockIdx.x, true, true);
+    auto w_pre_at = [&](int i) { return P == 1 ? vec[i] : load16(v_pre, (uint32_t)i * 16); };
+    auto w_post_at = [&](int i) {
+        return P == 1 ? vec[T + i] : ones_unless(load16(v_post, (uint32_t)i * 16), post);
+    };
+    auto gate_at = [&](int i) { return P == 1 ? vec[2 * T + i] : load16(v_gate, (uint32_t)i * 16); };
 #pragma unroll
-        for (int u = 0; u < P; ++u) {
-            const int i = u * T + t;
-            vec[i] = load16(r0, (uint32_t)i * 16);
-            vec[T * P + i] = ones_unless(load16(r1, (uint32_t)i * 16), post);
-            vec[2 * T * P + i] = load16(r2, (uint32_t)i * 16);
+    for (int u = 0; u < P; ++u) {
+        const int i = u * T + t;
+        if constexpr (P == 1) {
+            vec[i] = load16(v_pre, (uint32_t)i * 16);
+            vec[T + i] = ones_unless(load16(v_post, (uint32_t)i * 16), post);
+            vec[2 * T + i] = load16(v_gate, (uint32_t)i * 16);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) apre[u][j] = apost[u][j] = 0.f;
+            for (int j = 0; j < 8; ++j) apre[0][j] = apost[0][j] = 0.f;
+        } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) sums[h * T * P + i] = v4f{0.f, 0.f, 0.f, 0.f};
         }
     }
+    // sum k (0: pre, 1: post) of chunk u += x * y
+    auto add = [&](int k, int u, const float* x, const float* y) {
+        if constexpr (P == 1) {
+            float* a = k ? apost[0] : apre[0];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = __builtin_fmaf(x[i], y[i], a[i]);
+        } else {
+            v4f* a = sums + (2 * k * P * T + u * T + t);
+            v4f lo = a[0], hi = a[T * P];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lo[i] = __builtin_fmaf(x[i], y[i], lo[i]);
+                hi[i] = __builtin_fmaf(x[i + 4], y[i + 4], hi[i]);
+            }
+            a[0] = lo;
+            a[T * P] = hi;
+        }
+    };
     int par = 0;
     for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x, par ^= 1) {
         Row next[P];
-        if constexpr (P == 1) load(next, m + gridDim.x);
+        if constexpr (P == 1) load(next, m + gridDim.x, true, true);
         float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
         for (int u = 0; u < P; ++u) {
@@ -289,7 +328,7 @@ __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
             cur[u].r.get(r);
             unpack(cur[u].y, y);
             unpack(cur[u].n, dn);
-            unpack(vec[u * T + t], w);
+            unpack(w_pre_at(u * T + t), w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 s[0] = __builtin_fmaf(r[i], r[i], s[0]);
@@ -311,16 +350,17 @@ __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
             cur[u].r.get(r);
             cur[u].d.get(dr);
             unpack(cur[u].n, dn);
-            unpack(vec[u * T + t], w);
+            unpack(w_pre_at(u * T + t), w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dr[i] = __builtin_fmaf(ir, __builtin_fmaf(-r[i], cr, w[i] * dn[i]), dr[i]);
-                apre[u][i] = __builtin_fmaf(dn[i], r[i] * ir, apre[u][i]);
+                r[i] *= ir;
             }
+            add(0, u, dn, r);
             Chunk<RF32>::store(o_r, voff, dr);
             unpack(cur[u].y, y);
-            unpack(ones_unless(channel ? vec[2 * T * P + u * T + t] : load16(rg, voff), channel || elements), g);
-            unpack(vec[T * P + u * T + t], w);
+            unpack(ones_unless(channel ? gate_at(u * T + t) : load16(rg, voff), channel || elements), g);
+            unpack(w_post_at(u * T + t), w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float yn = y[i] * iy, z = yn * w[i], ad = alpha * dr[i];
@@ -328,10 +368,13 @@ __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
                 dg[i] = ad * z;
                 q[0] = __builtin_fmaf(dz[u][i], z, q[0]);
                 q[1] += dg[i];
-                apost[u][i] = __builtin_fmaf(channel ? ad : dz[u][i], yn, apost[u][i]);
+                y[i] = yn;
+                dr[i] = channel ? ad : dz[u][i];
             }
+            add(1, u, dr, y);
             store16(o_g, voff, pack(dg));
         }
+        if constexpr (P > 1) load(cur, m + gridDim.x, false, true);
         block_sum<2>(q, red[par] + 3 * 16);
         if (p.gate_kind == BFQ_GATE_TOKEN && p.d_gate && t == 0) static_cast<float*>(p.d_gate)[m] = q[1];
         const float cy = post ? iy * q[0] / fK : 0.f;
@@ -339,13 +382,13 @@ __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
         for (int u = 0; u < P; ++u) {
             float y[8], w[8];
             unpack(cur[u].y, y);
-            unpack(vec[T * P + u * T + t], w);
+            unpack(w_post_at(u * T + t), w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dz[u][i] = iy * __builtin_fmaf(-y[i], cy, w[i] * dz[u][i]);
             store16(o_y, (uint32_t)(u * T + t) * 16, pack(dz[u]));
         }
         if constexpr (P == 1) cur[0] = next[0];
-        else load(cur, m + gridDim.x);
+        else load(cur, m + gridDim.x, true, false);
     }
     if (!p.columns) return;
     const uint32_t row32 = (uint32_t)(4 * K);
@@ -353,8 +396,17 @@ __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
                                  s1 = row_rsrc(p.partials, 2 * (int64_t)blockIdx.x + 1, row32);
 #pragma unroll
     for (int u = 0; u < P; ++u) {
-        Chunk<1>::store(s0, (uint32_t)(u * T + t) * 16, apre[u]);
-        Chunk<1>::store(s1, (uint32_t)(u * T + t) * 16, apost[u]);
+        const uint32_t voff = (uint32_t)(u * T + t) * 16;
+        if constexpr (P == 1) {
+            Chunk<1>::store(s0, voff, apre[0]);
+            Chunk<1>::store(s1, voff, apost[0]);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                buf_store_v4f(s0, sums[h * T * P + u * T + t], 2 * voff, 16 * h);
+                buf_store_v4f(s1, sums[(2 + h) * T * P + u * T + t], 2 * voff, 16 * h);
+            }
+        }
     }
 }
 
@@ -426,23 +478,31 @@ hipError_t launch_norm_residual(const NormArgs& a, int res_f32, hipStream_t stre
 }
 
 // Workgroups of the backward kernel: one for each row up to what the CUs hold at once (16 waves
-// each at its register count).
+// each at its register count; past K = 8192 one, by its LDS).
 int64_t norm_bwd_groups(int64_t M, int64_t K) {
     const int64_t most = 256 * (1024 / threads_for(K, K <= 8192 ? 1 : 2));
     return M < most ? M : most;
 }
 
+template <int P, int RF32>
+static hipError_t launch_bwd(const NormArgs& a, int64_t groups, hipStream_t stream) {
+    const unsigned threads = threads_for(a.K, P), lds = threads * (P == 1 ? 48 : 128);
+    if constexpr (P > 1) {
+        static std::atomic<uint64_t> opted{0};
+        const hipError_t e = opt_in_lds(
+            opted, reinterpret_cast<const void*>(&norm_residual_bwd_kernel<P, RF32>), 1024 * 128);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((norm_residual_bwd_kernel<P, RF32>), dim3((unsigned)groups), dim3(threads), lds, stream, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_norm_residual_bwd(const NormArgs& a, int res_f32, hipStream_t stream) {
     const int64_t groups = norm_bwd_groups(a.M, a.K);
     if (groups > 0) {
-        const int P = a.K <= 8192 ? 1 : 2;
-        const dim3 grid((unsigned)groups), block(threads_for(a.K, P));
-        const unsigned lds = block.x * P * 3 * sizeof(v4u);
-        if (P == 1 && res_f32) hipLaunchKernelGGL((norm_residual_bwd_kernel<1, 1>), grid, block, lds, stream, a);
-        else if (P == 1) hipLaunchKernelGGL((norm_residual_bwd_kernel<1, 0>), grid, block, lds, stream, a);
-        else if (res_f32) hipLaunchKernelGGL((norm_residual_bwd_kernel<2, 1>), grid, block, lds, stream, a);
-        else hipLaunchKernelGGL((norm_residual_bwd_kernel<2, 0>), grid, block, lds, stream, a);
-        const hipError_t e = hipGetLastError();
+        const hipError_t e = a.K <= 8192
+                                 ? (res_f32 ? launch_bwd<1, 1>(a, groups, stream) : launch_bwd<1, 0>(a, groups, stream))
+                                 : (res_f32 ? launch_bwd<2, 1>(a, groups, stream) : launch_bwd<2, 0>(a, groups, stream));
         if (e != hipSuccess) return e;
     }
     if (a.columns) {

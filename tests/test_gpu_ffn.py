@@ -586,6 +586,23 @@ def test_norm_backward_parts(bfq):
     assert all(not bool(empty[k].any()) for k in ("d_w_pre", "d_w_post", "d_gate"))
 
 
+@pytest.mark.parametrize("K", [8192, 8200, 12288])
+def test_norm_backward_in_place_long_rows(bfq, K):
+    """In place on both sides of the widest row that a workgroup holds in one chunk a thread, with
+    more rows than workgroups (each then walks several)."""
+    M = 700
+    c = _norm_case(M, K, True, 1, torch.float32, K)
+    r = c.pop("residual")
+    dn, dro = _randn(K + 1, M, K).bfloat16(), _randn(K + 2, M, K)
+    full = bfq.norm_residual_backward(r, **c, d_normed=dn, d_res_out=dro)
+    ref, tols = _bwd_ref(c, r, dn, dro)
+    for k in ref:
+        _within(full[k], ref[k], tols[k] + H[full[k].dtype] * ref[k].abs() + 1e-30, k)
+    same, dy = dro.clone(), torch.empty_like(c["y"])
+    bfq.bfq_norm_residual_backward(r, same, **c, d_normed=dn, d_res_out=same, d_y=dy)
+    assert torch.equal(same, full["d_res"]) and torch.equal(dy, full["d_y"])
+
+
 @pytest.mark.parametrize("kind", range(4))
 def test_norm_backward_against_differences(bfq, kind):
     """Every gradient along a random direction against central differences in 64 bits."""
