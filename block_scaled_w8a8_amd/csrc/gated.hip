@@ -11,7 +11,15 @@
 // fp32 partials of the 2F-wide product instead and gated_reduce_kernel finishes them.
 //
 // What bounds the forward kernels is what bounds the block GEMM's: the weight stream at decode
-// sizes, the operand bytes through a CU's L1 and the scale step at large M.
+// sizes, the operand bytes through a CU's L1 and the scale step at large M. Measured, F 18432 x
+// K 7168, packed weights, SILU, bf16 out: 1 token 42 us (6.3 TB/s of weights), 64 tokens 56 us,
+// 512 tokens 222 us, 4096 tokens 1002 us with fp32 scales (2.16 PFLOP/s) and 895 us with powers of
+// two, 73 us more where the pre-activations are kept (302 MB).
+// The two sums carry the e4m3 MFMA's own error, as the block GEMM's do: 3.5e-5 to 4.6e-5 of the
+// result (relative, Frobenius) on outlier-bearing tokens, whichever schedule or tile. Where codes
+// are wanted it decides the values that lie that near to a rounding boundary: 333 x 2048 codes
+// over K 7168 differ from those of the exact product in 0.4 % of places, by one step, and are no
+// farther from the unrounded product (2.640 % both).
 #include "activation.h"
 #include "gemm_std_tile.h"
 #include "gemm_swapab_body.h"
@@ -449,6 +457,7 @@ __global__ __launch_bounds__(64 * KW) void gemm_gated_rows_kernel(GatedArgs p) {
 
 // Eight columns a thread: g and u summed over the K ranges in order, then as the epilogues above.
 // Groups of 128 columns are 16 lanes; the grid's rows past M (packed words only) write zeros.
+// Bytes bound it, its launch at decode sizes (2.7 us): 5.2 us for 333 x 2048 in two parts.
 __global__ __launch_bounds__(256) void gated_reduce_kernel(GatedArgs p) {
     const int lane = threadIdx.x & 63;
     const int64_t m = blockIdx.x, F = p.N, c = (int64_t)blockIdx.y * 256 + threadIdx.x;
@@ -599,8 +608,10 @@ const GatedKernel* gated_kernels(int* count) {
 // ---------------------------------------------------------------- backward ----
 
 // With a = act(g): dg = dh * u * act'(g), du = dh * a, and the product h = a * u again. Eight
-// columns a thread, read once and written once (bytes bound it). Codes: 128-column groups of the
-// 2F-wide row, one scale each, 16 lanes a group; rows past M (packed words only) write zeros.
+// columns a thread, read once and written once; bytes bound it: 4096 x 18432 takes 179 us for the
+// pair's gradient and h as bf16 (906 MB, 5.1 TB/s) and 123 us for its codes (604 MB, 4.9 TB/s; a
+// large copy reaches 4.8). Codes: 128-column groups of the 2F-wide row, one scale each, 16 lanes a
+// group; rows past M (packed words only) write zeros.
 template <int Q>
 __global__ __launch_bounds__(256) void gated_bwd_kernel(GatedBwdArgs p) {
     const int lane = threadIdx.x & 63;
@@ -659,7 +670,8 @@ hipError_t launch_gated_bwd(const GatedBwdArgs& a, hipStream_t stream) {
 }
 
 // Codes [N][K] and their 128x128 block scales to [K][N]: one 64 x 64 tile a workgroup through LDS,
-// 16-byte rows in and out; the first workgroup of a block moves its scale. An offline step.
+// 16-byte rows in and out; the first workgroup of a block moves its scale. An offline step: 129 us
+// for 36864 x 7168 (4.1 TB/s).
 __global__ __launch_bounds__(256) void transpose_weights_kernel(const uint8_t* __restrict__ w,
                                                                 const float* __restrict__ s,
                                                                 uint8_t* __restrict__ wt,
