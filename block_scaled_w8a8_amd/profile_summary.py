@@ -22,7 +22,8 @@ import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 KERNEL_SOURCES = ("csrc/gemm_std.hip", "csrc/gemm_swapab.hip", "csrc/quant.hip",
-                  "csrc/moe.hip", "csrc/device_common.h")
+                  "csrc/moe.hip", "csrc/device_common.h", "csrc/gemm_std_tile.h",
+                  "csrc/gemm_swapab_body.h", "csrc/quant_device.h")
 
 
 def source_hash() -> str:

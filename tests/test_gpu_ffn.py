@@ -804,3 +804,17 @@ def test_offsets_past_32_bits(bfq):
     t = bfq.bfq_gated_select_tile(M2, F2, K)
     part = bfq.gated_gemm(qa[tail].contiguous(), sa[tail].contiguous(), qw, sw, tile=t)
     assert torch.equal(out[tail], part)
+
+
+def test_readme_example():
+    """The feed-forward example of the README runs as it stands, after its first one."""
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(__file__), "..", "README.md")).read()
+    code = re.findall(r"```python\n(.*?)```", text, re.S)
+    env = {}
+    for block in code:
+        exec(block.replace('device="cuda"', 'device="cuda:0"'), env)
+    torch.cuda.synchronize()
+    assert env["out"].shape == (64, 7168) and env["dx"].shape == (64, 7168)
+    assert all(bool(env[n].float().isfinite().all()) for n in ("y", "res", "out", "dx"))
