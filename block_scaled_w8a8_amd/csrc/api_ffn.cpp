@@ -76,30 +76,35 @@ bfq_tile gated_tile(int variant, int bm, int bn, int sched, int wlayout) {
     return bfq_tile{};
 }
 
-// Strips of row-major weights that copy whole lines through LDS.
-bool row_strip(const GatedKernel& k) { return k.wlayout == W_ROW && k.tile.variant == 1; }
+// Strips that copy the weights through a ring in LDS.
+bool ring_strip(const GatedKernel& k) { return k.tile.variant == 1 && k.tile.sched == 2; }
 
 // Microseconds that a gated product is expected to take with kernel k and its K range in `split`
 // parts. The grid runs in rounds of 256 CUs times the workgroups a CU holds; a round's K block
 // takes the longer of a workgroup's own latency and the CU's throughput over the workgroups it
-// holds (joined smoothly), the whole no less than the weight stream (row strips take half of it
+// holds (joined smoothly), the whole no less than the weight stream (ring strips take half of it
 // again for each further bm tokens); partials cost a second launch and their bytes twice. The
-// constants, here and beside the kernels, are a fit to 744 measured (M, F, K, layout, format,
-// output) points of 9 to 60 configurations each, M 1 to 2048 on six (F, K); over them the pick is
-// on average 3.3 % (packed weights) and 2.5 % (row-major) slower than the fastest configuration.
+// constants, here and beside the kernels, are a fit to 840 measured (M, F, K, layout, format,
+// output) points of 9 to 100 configurations each, M 1 to 2048 on seven (F, K), weights read from
+// HBM as between the layers of a model; over them the pick is on average 1.7 % slower than the
+// fastest configuration.
 float gated_us(const GatedKernel& k, int64_t M, int64_t F, int64_t K, bool codes, int split) {
     const bfq_tile& t = k.tile;
     const int64_t groups = ceil_div(M, t.bm) * ceil_div(F, t.bn) * split;
     const int64_t slots = kNumCUs * k.occupancy, full = groups / slots, rest = groups % slots;
     const int kw = t.variant == 1 ? t.waves_m : 1;         // waves that share a strip's K range
     const float blocks = (float)ceil_div(ceil_div(K / 128, split), kw);
+    // strips whose waves fetch their own tokens: up to 0.6 of the throughput's time more for them
+    const float thr = k.thr * (t.variant == 1 && t.sched == 0
+                                   ? 1.f + 0.6f * (float)(M < t.bm ? M : t.bm) / (float)t.bm : 1.f);
     auto round = [&](int64_t held) {
-        const float a = k.lat * blocks, b = (float)held * k.thr * blocks * kw;
+        const float a = k.lat * blocks, b = (float)held * thr * blocks * kw;
         return std::sqrt(std::sqrt(a * a * a * a + b * b * b * b)) + k.fix;
     };
     float us = (float)full * round(k.occupancy) + (rest ? round(ceil_div(rest, kNumCUs)) : 0.f);
-    float stream = 2.f * (float)F * (float)K / (k.wlayout == W_PACKED16 ? 6.11e6f : 4.45e6f);
-    if (row_strip(k)) stream *= 0.5f + 0.5f * (float)ceil_div(M, t.bm);
+    const float rate = ring_strip(k) ? 5.03e6f : k.wlayout == W_PACKED16 ? 5.71e6f : 4.27e6f;
+    float stream = 2.f * (float)F * (float)K / rate;
+    if (ring_strip(k)) stream *= 0.5f + 0.5f * (float)ceil_div(M, t.bm);
     const float x = us > stream ? stream / us : us / stream, x2 = x * x, x4 = x2 * x2;
     us = (us > stream ? us : stream) * std::sqrt(std::sqrt(std::sqrt(1.f + x4 * x4)));
     if (split > 1 || (codes && t.bn != 128)) us += 2.74f + (float)split * (float)M * (float)F * 16.f / 5.54e6f;
@@ -107,7 +112,7 @@ float gated_us(const GatedKernel& k, int64_t M, int64_t F, int64_t K, bool codes
 }
 
 // The rule: the kernel and K split with the least expected time. Strips read the weights again
-// for every bm tokens, so they are left out where that is many times.
+// for every bm tokens, so they are left out where that is more often than was measured.
 bfq_tile select_gated(int64_t M, int64_t F, int64_t K, bool codes, int wlayout, int sfmt) {
     const int64_t KB = K / 128;
     if (batch_invariant()) {
@@ -125,13 +130,13 @@ bfq_tile select_gated(int64_t M, int64_t F, int64_t K, bool codes, int wlayout, 
         const bfq_tile& t = k[i].tile;
         if (k[i].wlayout != wlayout || k[i].sfmt == S_PACKED || (k[i].sfmt == S_UE8M0 && sfmt != S_UE8M0))
             continue;
-        if (t.variant == 1 ? M > 512 || M > 4 * t.bm : M < 24 || M < t.bm / 4) continue;
+        if (t.variant == 1 ? M > (ring_strip(k[i]) ? 4 : 2) * t.bm : M < 24 || M < t.bm / 4) continue;
         const int64_t groups = ceil_div(M, t.bm) * ceil_div(F, t.bn);
         for (int split : {1, 2, 3, 4, 6, 8, 12}) {
-            // at least two K blocks a part, and no parts beyond those that fill the CUs
-            // (row strips: none gained from more than three)
+            // at least two K blocks a part, and no parts beyond those that fill the CUs (ring
+            // strips: none gained from a split that partials alone pay for, nor from over three)
             if (split > 1 && (split * 2 > KB || groups * (split - 1) >= kNumCUs * k[i].occupancy ||
-                              (row_strip(k[i]) && split > 3)))
+                              (ring_strip(k[i]) && (!codes || split > 3))))
                 break;
             const float us = gated_us(k[i], M, F, K, codes, split);
             if (us < best_us) {

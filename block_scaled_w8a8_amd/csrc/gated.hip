@@ -314,18 +314,21 @@ __global__ __launch_bounds__(64 * NWAVES * KW) void gemm_gated_swapab_lds_kernel
     swapab_lds_body<MT, NWR, NWAVES, KW, D, Q_FP8, O_FP32, W_PACKED16, CH, 0, 1>(p);
 }
 
-// Row-major weights for a few tokens; the weight stream bounds it. A workgroup takes 16 output
-// columns (16 gate rows, 16 up rows) and its waves every KW-th K block, so that together they walk
-// KW * 128 neighbouring bytes of a row. A fragment load straight from row-major rows takes half a
-// line of each of 16 rows a request, and that stream stays near 4.3 TB/s; here a wave copies
-// whole 128-byte lines of 8 rows a load (1 KB) into a ring of its own, D K blocks of 4 KB, and
-// reads its fragments back. The ring is private to the wave, so the K loop has no barrier: the
-// wave waits until the loads of its oldest block have landed. Chunk c of row r sits in slot
-// c ^ swz(r), as in the standard tiles. Measured, F 18432 x K 7168: 50 us for 1 token
-// (5.3 TB/s of weights) and 52.5 us for 16, against 61 and 62 for direct fragment loads; F 2304:
-// 10.3 us for 16 tokens against 16.
-template <int MT, int KW, int D, int CH>
-__global__ __launch_bounds__(64 * KW) void gemm_gated_rows_kernel(GatedArgs p) {
+// Strips for a few tokens, the weights through LDS; the weight stream bounds them. A workgroup
+// takes 16 output columns (16 gate rows, 16 up rows) and its waves every KW-th K block, so that
+// together they walk neighbouring bytes of the weights. Each wave copies 1 KB a load (row-major:
+// whole 128-byte lines of 8 rows; packed: a fragment half) into a ring of its own, D K blocks of
+// 4 KB, and reads its fragments back: no barrier in the K loop, the wave waits until the loads of
+// its oldest block have landed, and what is in flight takes no registers, so a CU holds up to 10
+// waves of 16 KB in flight each. Row-major chunk c of row r sits in slot c ^ swz(r), as in the
+// standard tiles.
+// Row-major, F 18432 x K 7168: 50 us for 1 token (5.3 TB/s of weights), 52.5 for 16; fragment loads
+// straight from the rows take half a line of each of 16 rows a request: 61 and 62 us, 4.3 TB/s.
+// Packed: ahead of the strips above where the products are short (F 5632 x K 2048, 16 tokens: 7.9 us
+// against 10.8; F 4096 x K 4096: 9.5 against 11.5) and behind on long streams (F 18432 x K 7168, 1
+// token: 48 against 43).
+template <int MT, int KW, int D, int WL, int CH>
+__global__ __launch_bounds__(64 * KW) void gemm_gated_ring_kernel(GatedArgs p) {
     constexpr int SM = MT / 16, BLOCK = 4096;
     constexpr bool PK = CH == 2;
     constexpr int kOps = 6 + 3 * SM;                    // vector loads of one K block
@@ -358,12 +361,16 @@ __global__ __launch_bounds__(64 * KW) void gemm_gated_rows_kernel(GatedArgs p) {
     }
     const __amdgpu_buffer_rsrc_t rsg = make_rsrc(p.sw + (n0 / 128) * KB, (uint32_t)(KB * 4));
     const __amdgpu_buffer_rsrc_t rsu = make_rsrc(p.sw + (F / 128 + n0 / 128) * KB, (uint32_t)(KB * 4));
-    // copy: lane l takes row l / 8 (+ 8), slot l % 8; swz of the second eight rows differs by 1
-    const uint32_t c0 = (uint32_t)((lane >> 3) * K + (((lane & 7) ^ (lane >> 3)) << 4));
-    const uint32_t c1 = (uint32_t)(((lane >> 3) + 8) * K + (((lane & 7) ^ (lane >> 3) ^ 1) << 4));
+    // copy of rows: lane l takes row l / 8 (+ 8), slot l % 8; swz of the second eight differs by 1
+    constexpr bool rows = WL == W_ROW;
+    const uint32_t c0 = rows ? (uint32_t)((lane >> 3) * K + (((lane & 7) ^ (lane >> 3)) << 4))
+                             : (uint32_t)(lane * 16);
+    const uint32_t c1 = rows ? (uint32_t)(((lane >> 3) + 8) * K + (((lane & 7) ^ (lane >> 3) ^ 1) << 4))
+                             : (uint32_t)(1024 + lane * 16);
     const uint32_t ring = (uint32_t)(wk * D * BLOCK);
-    const uint32_t f0 = (uint32_t)(frow * 128 + ((fgrp ^ swz(frow)) << 4));
-    const uint32_t f1 = (uint32_t)(frow * 128 + (((fgrp + 4) ^ swz(frow)) << 4));
+    const uint32_t f0 = rows ? (uint32_t)(frow * 128 + ((fgrp ^ swz(frow)) << 4)) : (uint32_t)(lane * 16);
+    const uint32_t f1 = rows ? (uint32_t)(frow * 128 + (((fgrp + 4) ^ swz(frow)) << 4))
+                             : (uint32_t)(1024 + lane * 16);
 
     v4i abuf[D][SM][2];
     float sab[D][SM], swb[D], swu[D];
@@ -373,15 +380,16 @@ __global__ __launch_bounds__(64 * KW) void gemm_gated_rows_kernel(GatedArgs p) {
         const int64_t kb = ks0 + wk + i * KW;
         const uint32_t s = live ? (uint32_t)kb * 128u : kNoLoad;
         const uint32_t ss = live ? (uint32_t)((PK ? kb >> 2 : kb) * ssk * 4) : kNoLoad;
+        const uint32_t ws = rows ? s : live ? (uint32_t)kb * 2048u : kNoLoad;
         const uint32_t sws = live ? (uint32_t)kb * 4u : kNoLoad;
         const uint32_t at = ring + (uint32_t)(slot * BLOCK);
         swb[slot] = buf_f32(rsg, 0, sws);
         swu[slot] = buf_f32(rsu, 0, sws);
         kbs[slot] = (int)(kb & 3);
-        dma16(rw, lds, at, c0, s);
-        dma16(rw, lds, at + 1024, c1, s);
-        dma16(ru, lds, at + 2048, c0, s);
-        dma16(ru, lds, at + 3072, c1, s);
+        dma16(rw, lds, at, c0, ws);
+        dma16(rw, lds, at + 1024, c1, ws);
+        dma16(ru, lds, at + 2048, c0, ws);
+        dma16(ru, lds, at + 3072, c1, ws);
 #pragma unroll
         for (int sm = 0; sm < SM; ++sm) {
             abuf[slot][sm][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, a_voff[sm], s, 0);
@@ -541,15 +549,15 @@ hipError_t launch_gated_swapab(const GatedArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int MT, int KW, int D, int CH>
-hipError_t launch_gated_rows(const GatedArgs& a, hipStream_t stream) {
+template <int MT, int KW, int D, int WL, int CH>
+hipError_t launch_gated_ring(const GatedArgs& a, hipStream_t stream) {
     constexpr int LDS_BYTES = KW * D * 4096;
     static std::atomic<uint64_t> opted{0};
     const hipError_t e =
-        opt_in_lds(opted, reinterpret_cast<const void*>(&gemm_gated_rows_kernel<MT, KW, D, CH>), LDS_BYTES);
+        opt_in_lds(opted, reinterpret_cast<const void*>(&gemm_gated_ring_kernel<MT, KW, D, WL, CH>), LDS_BYTES);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)(a.N / 16), (unsigned)((a.M + MT - 1) / MT), (unsigned)a.split);
-    hipLaunchKernelGGL((gemm_gated_rows_kernel<MT, KW, D, CH>), grid, dim3(64 * KW), LDS_BYTES, stream, a);
+    hipLaunchKernelGGL((gemm_gated_ring_kernel<MT, KW, D, WL, CH>), grid, dim3(64 * KW), LDS_BYTES, stream, a);
     return hipGetLastError();
 }
 
@@ -566,38 +574,42 @@ hipError_t launch_gated_rows(const GatedArgs& a, hipStream_t stream) {
     BFQ_GATED_SAB1(MT, NWR, NW, KW, D, 0, L, OCC, LAT, THR, FIX),                           \
         BFQ_GATED_SAB1(MT, NWR, NW, KW, D, 2, L, OCC, LAT, THR, FIX)
 
-#define BFQ_GATED_ROWS1(MT, KW, D, CH, OCC, LAT, THR, FIX)                                      \
-    GatedKernel{bfq_tile{1, MT, 16, 128, 1, KW, 1, D, 1, 2, 0, 0}, W_ROW,                       \
-                (CH) == 2 ? S_PACKED : S_FP32, &launch_gated_rows<MT, KW, D, CH>, OCC, LAT, THR, FIX}
-#define BFQ_GATED_ROWS(MT, KW, D, OCC, LAT, THR, FIX)                                           \
-    BFQ_GATED_ROWS1(MT, KW, D, 0, OCC, LAT, THR, FIX), BFQ_GATED_ROWS1(MT, KW, D, 2, OCC, LAT, THR, FIX)
+#define BFQ_GATED_RING1(MT, KW, D, WL, CH, OCC, LAT, THR, FIX)                                  \
+    GatedKernel{bfq_tile{1, MT, 16, 128, 1, KW, 1, D, 1, 2, 0, 0}, WL,                          \
+                (CH) == 2 ? S_PACKED : S_FP32, &launch_gated_ring<MT, KW, D, WL, CH>, OCC, LAT, THR, FIX}
+#define BFQ_GATED_RING(MT, KW, D, WL, OCC, LAT, THR, FIX)                                       \
+    BFQ_GATED_RING1(MT, KW, D, WL, 0, OCC, LAT, THR, FIX),                                      \
+        BFQ_GATED_RING1(MT, KW, D, WL, 2, OCC, LAT, THR, FIX)
 
 static const GatedKernel kGatedKernels[] = {
-    BFQ_GATED_STD(64, 128, 1, 2, 0, W_ROW, 3, 1.006f, 0.373f, 6.348f),
-    BFQ_GATED_STD(64, 128, 1, 2, 0, W_PACKED16, 3, 0.943f, 0.385f, 3.607f),
-    BFQ_GATED_STD(128, 128, 2, 2, 0, W_ROW, 2, 1.185f, 0.494f, 5.811f),
-    BFQ_GATED_STD(128, 128, 2, 2, 0, W_PACKED16, 2, 1.183f, 0.002f, 3.830f),
-    BFQ_GATED_STD(128, 128, 2, 2, 3, W_ROW, 2, 0.757f, 0.397f, 6.009f),
-    BFQ_GATED_STD(128, 128, 2, 2, 3, W_PACKED16, 2, 0.663f, 0.409f, 3.445f),
-    BFQ_GATED_STD(128, 256, 2, 2, 3, W_ROW, 1, 1.113f, 0.000f, 6.514f),
-    BFQ_GATED_STD(128, 256, 2, 2, 3, W_PACKED16, 1, 1.140f, 0.093f, 4.577f),
-    BFQ_GATED_STD(256, 256, 4, 2, 0, W_ROW, 1, 1.878f, 0.000f, 5.823f),
-    BFQ_GATED_STD(256, 256, 4, 2, 0, W_PACKED16, 1, 1.751f, 0.001f, 3.582f),
-    BFQ_GATED_STD(256, 256, 4, 2, 1, W_ROW, 1, 1.855f, 0.772f, 6.652f),
-    BFQ_GATED_STD(256, 256, 4, 2, 3, W_ROW, 1, 1.601f, 1.200f, 4.902f),
-    BFQ_GATED_STD(256, 256, 4, 2, 3, W_PACKED16, 1, 1.584f, 1.043f, 3.180f),
-    BFQ_GATED_ROWS(16, 1, 4, 10, 0.167f, 0.092f, 4.436f),
-    BFQ_GATED_ROWS(16, 2, 4, 5, 0.000f, 0.114f, 4.298f),
-    BFQ_GATED_ROWS(16, 4, 3, 3, 0.000f, 0.108f, 4.429f),
-    BFQ_GATED_ROWS(32, 2, 4, 5, 0.000f, 0.169f, 4.305f),
-    BFQ_GATED_ROWS(64, 2, 3, 4, 0.002f, 0.261f, 4.933f),
-    BFQ_GATED_SAB(16, 32, 1, 4, 4, 0, 4, 0.001f, 0.129f, 1.719f),
-    BFQ_GATED_SAB(16, 32, 1, 4, 8, 0, 2, 0.000f, 0.105f, 2.726f),
-    BFQ_GATED_SAB(32, 32, 2, 4, 4, 1, 2, 0.000f, 0.271f, 3.656f),
-    BFQ_GATED_SAB(32, 32, 8, 1, 4, 1, 2, 0.000f, 0.759f, 4.292f),
-    BFQ_GATED_SAB(64, 32, 2, 4, 4, 1, 1, 0.903f, 0.294f, 5.115f),
-    BFQ_GATED_SAB(64, 32, 8, 1, 4, 1, 1, 0.732f, 0.577f, 4.874f),
-    BFQ_GATED_SAB(128, 32, 8, 1, 4, 1, 1, 1.090f, 0.000f, 6.339f),
+    BFQ_GATED_STD(64, 128, 1, 2, 0, W_ROW, 3, 1.196f, 0.330f, 6.205f),
+    BFQ_GATED_STD(64, 128, 1, 2, 0, W_PACKED16, 3, 1.003f, 0.342f, 6.349f),
+    BFQ_GATED_STD(128, 128, 2, 2, 0, W_ROW, 2, 1.357f, 0.287f, 5.575f),
+    BFQ_GATED_STD(128, 128, 2, 2, 0, W_PACKED16, 2, 1.217f, 0.275f, 5.742f),
+    BFQ_GATED_STD(128, 128, 2, 2, 3, W_ROW, 2, 1.014f, 0.458f, 5.405f),
+    BFQ_GATED_STD(128, 128, 2, 2, 3, W_PACKED16, 2, 0.890f, 0.427f, 5.830f),
+    BFQ_GATED_STD(128, 256, 2, 2, 3, W_ROW, 1, 1.301f, 0.824f, 6.088f),
+    BFQ_GATED_STD(128, 256, 2, 2, 3, W_PACKED16, 1, 1.180f, 0.338f, 7.080f),
+    BFQ_GATED_STD(256, 256, 4, 2, 0, W_ROW, 1, 2.001f, 0.510f, 4.738f),
+    BFQ_GATED_STD(256, 256, 4, 2, 0, W_PACKED16, 1, 1.861f, 0.290f, 4.960f),
+    BFQ_GATED_STD(256, 256, 4, 2, 1, W_ROW, 1, 1.904f, 0.665f, 4.860f),
+    BFQ_GATED_STD(256, 256, 4, 2, 3, W_ROW, 1, 1.827f, 0.652f, 4.592f),
+    BFQ_GATED_STD(256, 256, 4, 2, 3, W_PACKED16, 1, 1.766f, 0.243f, 4.914f),
+    BFQ_GATED_RING(16, 1, 4, W_ROW, 10, 0.162f, 0.094f, 4.667f),
+    BFQ_GATED_RING(16, 1, 4, W_PACKED16, 10, 0.164f, 0.090f, 4.762f),
+    BFQ_GATED_RING(16, 2, 4, W_ROW, 5, 0.000f, 0.126f, 4.340f),
+    BFQ_GATED_RING(16, 2, 4, W_PACKED16, 5, 0.000f, 0.120f, 4.408f),
+    BFQ_GATED_RING(32, 2, 4, W_ROW, 5, 0.000f, 0.179f, 4.192f),
+    BFQ_GATED_RING(32, 2, 4, W_PACKED16, 5, 0.000f, 0.174f, 4.207f),
+    BFQ_GATED_RING(64, 2, 3, W_ROW, 4, 0.000f, 0.271f, 4.821f),
+    BFQ_GATED_RING(64, 2, 3, W_PACKED16, 4, 0.000f, 0.266f, 4.922f),
+    BFQ_GATED_SAB(16, 32, 1, 4, 4, 0, 4, 0.001f, 0.093f, 4.037f),
+    BFQ_GATED_SAB(16, 32, 1, 4, 8, 0, 2, 0.000f, 0.079f, 4.549f),
+    BFQ_GATED_SAB(32, 32, 2, 4, 4, 1, 2, 0.000f, 0.269f, 5.311f),
+    BFQ_GATED_SAB(32, 32, 8, 1, 4, 1, 2, 0.002f, 0.712f, 6.910f),
+    BFQ_GATED_SAB(64, 32, 2, 4, 4, 1, 1, 0.007f, 0.364f, 5.901f),
+    BFQ_GATED_SAB(64, 32, 8, 1, 4, 1, 1, 0.000f, 0.764f, 7.413f),
+    BFQ_GATED_SAB(128, 32, 8, 1, 4, 1, 1, 0.001f, 1.091f, 8.584f),
 };
 
 const GatedKernel* gated_kernels(int* count) {

@@ -381,8 +381,8 @@ bfq_status bfq_gated_gemm(const void* a_q, const float* a_scales, bfq_scale_layo
 
 /* The tile that bfq_gated_gemm takes: a rule on M, F, K, the layout, the scale format and whether
  * codes are wanted (bn counts output columns: 2 * bn weight rows). Variant 1 with sched 2 (gated
- * tiles of row-major weights only): the waves take every waves_m-th K block and copy the weight
- * rows through LDS. Batch-invariant mode applies as in bfq_select_tile. */
+ * tiles only): the waves take every waves_m-th K block and copy the weights through LDS, stages K
+ * blocks ahead. Batch-invariant mode applies as in bfq_select_tile. */
 bfq_status bfq_gated_select_tile(int64_t M, int64_t F, int64_t K, bfq_dtype out_dtype,
                                  bfq_weight_layout w_layout, bfq_scale_format scale_fmt,
                                  bfq_tile* tile_out);

@@ -119,20 +119,25 @@ def _twin(bfq, t, wl):
     return bfq.bfq_tile.from_dict(d)
 
 
-def _gu_interleaved(bfq, qa, sa, qw, sw, t, sfmt):
-    """The row strips' sums: the waves of a workgroup take every waves_m-th K block of a part, each
+def _gu_interleaved(bfq, qa, sa, qw, sw, t, wl, sfmt):
+    """The ring strips' sums: the waves of a workgroup take every waves_m-th K block of a part, each
     in ascending order; their sums are added in the waves' order and the parts' in the parts'."""
-    KB, one = qa.shape[1] // 128, bfq.bfq_tile.from_dict({**_twin(bfq, t, 0).as_dict(), "split_k": 1})
+    KB, one = qa.shape[1] // 128, bfq.bfq_tile.from_dict({**_twin(bfq, t, wl).as_dict(), "split_k": 1})
+
+    def w(blocks, cols):
+        if not wl:
+            return qw[:, cols].contiguous()
+        return qw.view(qw.shape[0] // 16, KB, 2048)[:, blocks].contiguous().view(qw.shape[0], -1)
     total = None
     for z in range(t.split_k):
         part = None
-        for w in range(t.waves_m):
-            blocks = torch.arange(z * KB // t.split_k + w, (z + 1) * KB // t.split_k, t.waves_m, device=DEV)
+        for v in range(t.waves_m):
+            blocks = torch.arange(z * KB // t.split_k + v, (z + 1) * KB // t.split_k, t.waves_m, device=DEV)
             if len(blocks):
                 cols = (blocks[:, None] * 128 + torch.arange(128, device=DEV)).flatten()
                 x = bfq.block_gemm(qa[:, cols].contiguous(), sa[:, blocks].contiguous(),
-                                   qw[:, cols].contiguous(), sw[:, blocks].contiguous(),
-                                   out_dtype=torch.float32, tile=one, w_layout=0, scale_fmt=sfmt)
+                                   w(blocks, cols), sw[:, blocks].contiguous(),
+                                   out_dtype=torch.float32, tile=one, w_layout=wl, scale_fmt=sfmt)
                 part = x if part is None else part + x
         total = part if total is None else total + part
     return total.double()
@@ -141,7 +146,7 @@ def _gu_interleaved(bfq, qa, sa, qw, sw, t, sfmt):
 def _gu(bfq, qa, sa, qw, sw, t, wl, sfmt):
     """(g, u) of gated tile t: the fp32 output of its twin on the 2F rows."""
     if t.variant == 1 and t.sched == 2:
-        return _gu_interleaved(bfq, qa, sa, qw, sw, t, sfmt)
+        return _gu_interleaved(bfq, qa, sa, qw, sw, t, wl, sfmt)
     gu = bfq.block_gemm(qa, sa, qw, sw, out_dtype=torch.float32, tile=_twin(bfq, t, wl),
                         w_layout=wl, scale_fmt=sfmt)
     return gu.double()
