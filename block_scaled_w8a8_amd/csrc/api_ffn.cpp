@@ -86,7 +86,7 @@ bool ring_strip(const GatedKernel& k) { return k.tile.variant == 1 && k.tile.sch
 // again for each further bm tokens); partials cost a second launch and their bytes twice. The
 // constants, here and beside the kernels, are a fit to 840 measured (M, F, K, layout, format,
 // output) points of 9 to 100 configurations each, M 1 to 2048 on seven (F, K), weights read from
-// HBM as between the layers of a model; over them the pick is on average 1.7 % slower than the
+// HBM as between the layers of a model; over them the pick is on average 1.1 % slower than the
 // fastest configuration.
 float gated_us(const GatedKernel& k, int64_t M, int64_t F, int64_t K, bool codes, int split) {
     const bfq_tile& t = k.tile;
@@ -102,7 +102,7 @@ float gated_us(const GatedKernel& k, int64_t M, int64_t F, int64_t K, bool codes
         return std::sqrt(std::sqrt(a * a * a * a + b * b * b * b)) + k.fix;
     };
     float us = (float)full * round(k.occupancy) + (rest ? round(ceil_div(rest, kNumCUs)) : 0.f);
-    const float rate = ring_strip(k) ? 5.03e6f : k.wlayout == W_PACKED16 ? 5.71e6f : 4.27e6f;
+    const float rate = t.variant == 0 ? 4.6e6f : ring_strip(k) ? 5.0e6f : 5.88e6f;
     float stream = 2.f * (float)F * (float)K / rate;
     if (ring_strip(k)) stream *= 0.5f + 0.5f * (float)ceil_div(M, t.bm);
     const float x = us > stream ? stream / us : us / stream, x2 = x * x, x4 = x2 * x2;
@@ -117,10 +117,10 @@ bfq_tile select_gated(int64_t M, int64_t F, int64_t K, bool codes, int wlayout, 
     const int64_t KB = K / 128;
     if (batch_invariant()) {
         // one MFMA per K block and fp32 scale FMAs in ascending order, whatever M
-        if (wlayout == W_PACKED16 && M <= 128)
-            return gated_tile(1, M <= 32 ? 32 : M <= 64 ? 64 : 128, 128, 1, wlayout);
+        if (wlayout == W_PACKED16 && M <= 64) return gated_tile(1, M <= 32 ? 32 : 64, 128, 1, wlayout);
         if (M <= 64) return gated_tile(0, 64, 64, 0, wlayout);
-        return M <= 512 ? gated_tile(0, 128, 64, 0, wlayout) : gated_tile(0, 256, 128, 0, wlayout);
+        if (M <= 512) return gated_tile(0, 128, 64, 0, wlayout);
+        return gated_tile(0, 256, 128, wlayout == W_PACKED16 ? 0 : 1, wlayout);
     }
     int n = 0;
     const GatedKernel* k = gated_kernels(&n);

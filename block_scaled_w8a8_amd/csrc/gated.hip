@@ -4,7 +4,8 @@
 // (block-scaled e4m3 operands, as the block GEMM), both products, the activation and the product
 // in one kernel: a workgroup takes the gate rows and the up rows of the same output columns, so a
 // lane's accumulators hold both factors of each of its outputs and the 2F-wide product is never
-// stored. The tile routines are the block GEMM's (gemm_std_tile.h, gemm_swapab_body.h).
+// stored. Large batches and packed weights at a few tokens use the block GEMM's tile routines
+// (gemm_std_tile.h, gemm_swapab_body.h); the sizes between have tiles of their own below.
 // Outputs are bf16 / fp16 / fp32, or e4m3 codes with one scale per 128 columns, which is what the
 // down projection's GEMM reads: a workgroup that covers 128 output columns holds whole groups.
 // A tile whose K range is split, or that covers less than a group when codes are wanted, writes
@@ -13,7 +14,7 @@
 // What bounds the forward kernels is what bounds the block GEMM's: the weight stream at decode
 // sizes, the operand bytes through a CU's L1 and the scale step at large M. Measured, F 18432 x
 // K 7168, packed weights, SILU, bf16 out: 1 token 42 us (6.3 TB/s of weights), 64 tokens 56 us,
-// 512 tokens 222 us, 4096 tokens 1002 us with fp32 scales (2.16 PFLOP/s) and 895 us with powers of
+// 512 tokens 204 us, 4096 tokens 1002 us with fp32 scales (2.16 PFLOP/s) and 895 us with powers of
 // two, 73 us more where the pre-activations are kept (302 MB).
 // The two sums carry the e4m3 MFMA's own error, as the block GEMM's do: 3.5e-5 to 4.6e-5 of the
 // result (relative, Frobenius) on outlier-bearing tokens, whichever schedule or tile. Where codes
@@ -156,21 +157,13 @@ __device__ __forceinline__ void store_tile(const uint8_t* lds, void* dst, int64_
     }
 }
 
-// One workgroup per (tile of BM tokens x BN / 2 output columns, K split).
-template <int BM, int BN, int WM, int WN, int SCHED, int WL>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_gated_std_kernel(GatedArgs p) {
-    using Shape = StdShape<BM, BN, WM, WN, SCHED>;
-    constexpr int TM = Shape::TM, SM = Shape::SM, SG = Shape::SN / 2, BNO = BN / 2, TNO = BNO / WN;
-    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-    const int64_t M = p.M, F = p.N, KB = p.K / 128;
-    const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (F + BNO - 1) / BNO;
-    int64_t pid_m, pid_n;
-    tile_coords(blockIdx.x, tiles_m, tiles_n, p.group_m, p.raster, pid_m, pid_n);
-    const int64_t m0 = pid_m * BM, n0 = pid_n * BNO;
-    const int split = p.split, z = blockIdx.z;
-    typename Shape::AccT acc[SM][2 * SG];
-    std_tile<BM, BN, WM, WN, Q_FP8, SCHED, 2, WL, 0, 1>(p, lds, m0, n0, (int64_t)z * KB / split,
-                                                        (int64_t)(z + 1) * KB / split, acc);
+// Finishes a tile of BM tokens x BNO output columns from (m0, n0): wave (wm, wn) holds rows wm * TM
+// and columns wn * TNO. The LDS is free (the callers end on a barrier).
+template <int BM, int BNO, int WM, int WN, int SM, int SG>
+__device__ __forceinline__ void gated_finish_tile(const GatedArgs& p, uint8_t* lds, v4f (&acc)[SM][2 * SG],
+                                                  int64_t m0, int64_t n0) {
+    constexpr int TM = BM / WM, TNO = BNO / WN;
+    const int64_t M = p.M, F = p.N;
     const int lane = threadIdx.x & 63, frow = lane & 15, fgrp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -180,7 +173,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_gated_std_kernel(GatedArgs 
         gated_partials<SM, SG>(p, acc, n, row);
         return;
     }
-    // std_tile ends on a barrier: the LDS is free. lr, lc: the lane's first row and column of the tile
+    // lr, lc: the lane's first row and column of the tile
     constexpr int THREADS = 64 * WM * WN;
     const int lr = wm * TM + frow, lc = wn * TNO + 4 * fgrp;
     const int64_t live = M - m0 < BM ? M - m0 : BM;
@@ -248,6 +241,176 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_gated_std_kernel(GatedArgs 
         lds_barrier();
         store_tile<BM, BNO, THREADS>(lds, static_cast<uint8_t*>(p.out) + m0 * F + n0, F, live);
     }
+}
+
+// One workgroup per (tile of BM tokens x BN / 2 output columns, K split).
+template <int BM, int BN, int WM, int WN, int SCHED, int WL>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_gated_std_kernel(GatedArgs p) {
+    using Shape = StdShape<BM, BN, WM, WN, SCHED>;
+    constexpr int SM = Shape::SM, SG = Shape::SN / 2, BNO = BN / 2;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const int64_t M = p.M, F = p.N, KB = p.K / 128;
+    const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (F + BNO - 1) / BNO;
+    int64_t pid_m, pid_n;
+    tile_coords(blockIdx.x, tiles_m, tiles_n, p.group_m, p.raster, pid_m, pid_n);
+    const int64_t m0 = pid_m * BM, n0 = pid_n * BNO;
+    const int split = p.split, z = blockIdx.z;
+    typename Shape::AccT acc[SM][2 * SG];
+    std_tile<BM, BN, WM, WN, Q_FP8, SCHED, 2, WL, 0, 1>(p, lds, m0, n0, (int64_t)z * KB / split,
+                                                        (int64_t)(z + 1) * KB / split, acc);
+    gated_finish_tile<BM, BNO, WM, WN, SM, SG>(p, lds, acc, m0, n0);
+}
+
+// Tiles for tens to hundreds of tokens on short products, where a K block's trip to memory costs
+// more than its arithmetic: D LDS stages of one K block (BM token rows, BNO gate rows, BNO up rows),
+// D - 1 of them in flight. A wave waits for its own loads of the oldest stage, one barrier makes the
+// stage whole and frees the one before, which is refilled at once. Token rows and row-major weight
+// rows are swizzled as in the standard tiles, packed weights are fragment halves. Scales travel in
+// registers, counted with the loads. Against tiles of two stages, which wait out the trip every K
+// block: F 4096 x K 4096, 512 tokens, 28.7 us for 38.8; F 2304 x K 7168, 128 tokens, 20.2 for 26.7;
+// F 18432 x K 7168, 512 tokens, 204 for 223. At those sizes the fixed costs lead: some 3 us to start
+// and drain, 3 us for a split's second launch.
+template <int BM, int BNO, int WM, int WN, int D, int SCHED, int WL>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_gated_pipe_kernel(GatedArgs p) {
+    constexpr int NW = WM * WN, TM = BM / WM, TNO = BNO / WN, SM = TM / 16, SG = TNO / 16;
+    constexpr int STAGE = (BM + 2 * BNO) * 128, CA = BM / 8 / NW, CW = BNO / 8 / NW;   // loads a wave
+    constexpr int kOps = CA + 2 * CW + SM + 2;
+    constexpr bool rows = WL == W_ROW;
+    static_assert(NW % 2 == 0 && BM / 8 % NW == 0 && BNO / 8 % NW == 0 && 128 % BNO == 0, "whole loads a wave");
+    static_assert((D - 2) * kOps <= 63, "the wait counts loads in six bits");
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const int lane = threadIdx.x & 63, frow = lane & 15, fgrp = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int64_t M = p.M, F = p.N, K = p.K, KB = K / 128;
+    int64_t pid_m, pid_n;
+    tile_coords(blockIdx.x, (M + BM - 1) / BM, F / BNO, p.group_m, p.raster, pid_m, pid_n);
+    const int64_t m0 = pid_m * BM, n0 = pid_n * BNO;
+    const int64_t kb0 = (int64_t)blockIdx.z * KB / p.split, L = (int64_t)(blockIdx.z + 1) * KB / p.split - kb0;
+    constexpr uint32_t kNoLoad = 0x80000000u;           // past every resource here
+
+    const uint8_t* w = static_cast<const uint8_t*>(p.w);
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(w + n0 * K, (uint32_t)(BNO * K));
+    const __amdgpu_buffer_rsrc_t ru = make_rsrc(w + (F + n0) * K, (uint32_t)(BNO * K));
+    const int64_t live = M - m0 < BM ? M - m0 : BM, ssm = p.sa_stride_m, ssk = p.sa_stride_k;
+    const int packed = p.sa_packed;
+    const uint32_t pmask = packed ? ~0u : 0u;
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(static_cast<const uint8_t*>(p.a) + m0 * K, (uint32_t)(live * K));
+    const __amdgpu_buffer_rsrc_t rsa = make_rsrc(
+        p.sa + m0 * ssm, (uint32_t)(((live - 1) * ssm + (packed ? (KB - 1) / 4 : KB - 1) * ssk + 1) * 4));
+    const __amdgpu_buffer_rsrc_t rsg = make_rsrc(p.sw + (n0 / 128) * KB, (uint32_t)(KB * 4));
+    const __amdgpu_buffer_rsrc_t rsu = make_rsrc(p.sw + (F / 128 + n0 / 128) * KB, (uint32_t)(KB * 4));
+    uint32_t sa_voff[SM];
+#pragma unroll
+    for (int sm = 0; sm < SM; ++sm) sa_voff[sm] = (uint32_t)((wm * TM + sm * 16 + frow) * ssm * 4);
+    // a load of rows: 8 of them, lane l row l / 8, slot l % 8; load i of a wave starts at row
+    // 8 * (wave + NW * i), whose swizzle phase is the wave's (NW is even)
+    const uint32_t row_voff = (uint32_t)(((lane >> 3) + wave * 8) * K + (((lane & 7) ^ (lane >> 3) ^ (wave & 1)) << 4));
+    // packed: 16-row group (wave + NW * i) / 2, half (wave + NW * i) % 2
+    const uint32_t w_voff = rows ? row_voff : (uint32_t)((wave >> 1) * KB * 2048 + (wave & 1) * 1024 + lane * 16);
+
+    float sab[D][SM], sgb[D], sub[D];
+    int kbs[D];
+    auto fetch = [&](int slot, int64_t i) {
+        const bool in = i < L;
+        const int64_t kb = kb0 + i;
+        const uint32_t sk = in ? (uint32_t)kb * 128u : kNoLoad;
+        const uint32_t wk = rows ? sk : in ? (uint32_t)kb * 2048u : kNoLoad;
+        const uint32_t ss = in ? (uint32_t)((packed ? kb >> 2 : kb) * ssk * 4) : kNoLoad;
+        const uint32_t sws = in ? (uint32_t)kb * 4u : kNoLoad;
+        const uint32_t at = (uint32_t)(slot * STAGE + wave * 1024);
+        // the scales first: they are waited for first
+        sgb[slot] = buf_f32(rsg, 0, sws);
+        sub[slot] = buf_f32(rsu, 0, sws);
+#pragma unroll
+        for (int sm = 0; sm < SM; ++sm) sab[slot][sm] = buf_f32(rsa, sa_voff[sm], ss);
+        kbs[slot] = (int)(kb & 3);
+#pragma unroll
+        for (int c = 0; c < CA; ++c)
+            dma16(ra, lds, at + c * NW * 1024, row_voff, sk + (uint32_t)(NW * c * 8 * K));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < CW; ++c)
+                dma16(h ? ru : rw, lds, at + (uint32_t)(BM * 128 + h * BNO * 128 + c * NW * 1024), w_voff,
+                      wk + (rows ? (uint32_t)(NW * c * 8 * K) : (uint32_t)(NW * c / 2 * KB * 2048)));
+    };
+    v4f acc[SM][2 * SG];
+#pragma unroll
+    for (int sm = 0; sm < SM; ++sm)
+#pragma unroll
+        for (int n = 0; n < 2 * SG; ++n) acc[sm][n] = v4f{0.f, 0.f, 0.f, 0.f};
+    const uint32_t f0 = (uint32_t)(frow * 128 + ((fgrp ^ swz(frow)) << 4));
+    const uint32_t f1 = (uint32_t)(frow * 128 + (((fgrp + 4) ^ swz(frow)) << 4));
+    auto frag = [&](const uint8_t* at, uint32_t lo, uint32_t hi) {
+        const v4i x = *reinterpret_cast<const v4i*>(at + lo), y = *reinterpret_cast<const v4i*>(at + hi);
+        return v8i{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    };
+    auto compute = [&](int slot) {
+        const uint8_t* at = lds + slot * STAGE;
+        v8i a[SM];
+        float sa[SM];
+        int ea[SM];
+#pragma unroll
+        for (int sm = 0; sm < SM; ++sm) {
+            a[sm] = frag(at + (wm * TM + sm * 16) * 128, f0, f1);
+            // packed: byte kb % 4 of the word (selects without a branch)
+            const uint32_t word = __float_as_uint(sab[slot][sm]), code = e8m0_byte(word, kbs[slot]);
+            if constexpr (SCHED == 3)
+                ea[sm] = (int)((code & pmask) | (e8m0_of(sab[slot][sm]) & ~pmask));
+            else
+                sa[sm] = __uint_as_float((__float_as_uint(e8m0_value(code)) & pmask) | (word & ~pmask));
+        }
+        // the scale step of a sub-tile column runs behind the next one's MFMAs (SCHED 0); powers of
+        // two are the MFMA's own scale operands, and it accumulates (SCHED 3)
+        v4f q[2][SM];
+        auto scale = [&](int n) {
+#pragma unroll
+            for (int sm = 0; sm < SM; ++sm) {
+                const float c = sa[sm] * (n / SG ? sub[slot] : sgb[slot]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[sm][n][j] = __builtin_fmaf(q[n & 1][sm][j], c, acc[sm][n][j]);
+            }
+        };
+#pragma unroll
+        for (int n = 0; n < 2 * SG; ++n) {
+            const uint8_t* wat = at + BM * 128 + (n / SG * BNO + wn * TNO + (n % SG) * 16) * 128;
+            const v8i wf = rows ? frag(wat, f0, f1) : frag(wat, lane * 16, 1024 + lane * 16);
+            const int ew = (int)e8m0_of(n / SG ? sub[slot] : sgb[slot]);
+#pragma unroll
+            for (int sm = 0; sm < SM; ++sm) {
+                if constexpr (SCHED == 3) acc[sm][n] = mfma_fp8_16x16x128_e8(wf, a[sm], acc[sm][n], ew, ea[sm]);
+                else q[n & 1][sm] = mfma_fp8_16x16x128(wf, a[sm]);
+            }
+            if constexpr (SCHED == 0) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (n > 0) scale(n - 1);
+            }
+        }
+        if constexpr (SCHED == 0) scale(2 * SG - 1);
+    };
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) {
+        fetch(i, i);
+        __builtin_amdgcn_sched_barrier(0);              // stages in order: the waits count
+    }
+    for (int64_t i0 = 0; i0 < L; i0 += D) {
+#pragma unroll
+        for (int r = 0; r < D; ++r) {
+            if (i0 + r >= L) break;                     // uniform over the workgroup
+            __builtin_amdgcn_sched_barrier(0);
+            wait_vmem_keep((D - 2) * kOps);
+            // a plain barrier: the fences of the others would wait for the copies in flight. This
+            // wave's reads of the last stage are done (its MFMAs took them)
+            asm volatile("s_barrier" ::: "memory");
+            fetch((r + D - 1) % D, i0 + r + D - 1);
+            __builtin_amdgcn_sched_barrier(0);
+            compute(r);
+        }
+    }
+    wait_vmem_all();       // no copy into LDS may still be in flight
+    __syncthreads();
+    gated_finish_tile<BM, BNO, WM, WN, SM, SG>(p, lds, acc, m0, n0);
 }
 
 // ---------------------------------------------------------------- swap-AB strips ----
@@ -535,6 +698,21 @@ hipError_t launch_gated_std(const GatedArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <int BM, int BNO, int WM, int WN, int D, int SCHED, int WL>
+hipError_t launch_gated_pipe(const GatedArgs& a, hipStream_t stream) {
+    constexpr int LDS_BYTES = D * (BM + 2 * BNO) * 128;
+    static_assert(LDS_BYTES <= 160 * 1024 && LDS_BYTES >= BM * 4 * BNO, "the stages fit, the epilogue's tiles too");
+    const int64_t tiles = ((a.M + BM - 1) / BM) * (a.N / BNO);
+    static std::atomic<uint64_t> opted{0};
+    const hipError_t e = opt_in_lds(
+        opted, reinterpret_cast<const void*>(&gemm_gated_pipe_kernel<BM, BNO, WM, WN, D, SCHED, WL>), LDS_BYTES);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((gemm_gated_pipe_kernel<BM, BNO, WM, WN, D, SCHED, WL>),
+                       dim3((unsigned)tiles, 1, (unsigned)a.split), dim3(64 * WM * WN), LDS_BYTES,
+                       stream, a);
+    return hipGetLastError();
+}
+
 template <int MT, int NWR, int NWAVES, int KW, int D, int CH, int LDS>
 hipError_t launch_gated_swapab(const GatedArgs& a, hipStream_t stream) {
     const int64_t cols = NWR / 2 * NWAVES, strips = (a.N + cols - 1) / cols;
@@ -581,35 +759,44 @@ hipError_t launch_gated_ring(const GatedArgs& a, hipStream_t stream) {
     BFQ_GATED_RING1(MT, KW, D, WL, 0, OCC, LAT, THR, FIX),                                      \
         BFQ_GATED_RING1(MT, KW, D, WL, 2, OCC, LAT, THR, FIX)
 
+#define BFQ_GATED_PIPE(BM, BNO, WM, WN, D, SC, WL, OCC, LAT, THR, FIX)                          \
+    GatedKernel{bfq_tile{0, BM, BNO, 128, 1, WM, WN, D, 8, SC, 0, 0}, WL,                       \
+                (SC) == 3 ? S_UE8M0 : S_FP32, &launch_gated_pipe<BM, BNO, WM, WN, D, SC, WL>, OCC, LAT, THR, FIX}
+
 static const GatedKernel kGatedKernels[] = {
-    BFQ_GATED_STD(64, 128, 1, 2, 0, W_ROW, 3, 1.196f, 0.330f, 6.205f),
-    BFQ_GATED_STD(64, 128, 1, 2, 0, W_PACKED16, 3, 1.003f, 0.342f, 6.349f),
-    BFQ_GATED_STD(128, 128, 2, 2, 0, W_ROW, 2, 1.357f, 0.287f, 5.575f),
-    BFQ_GATED_STD(128, 128, 2, 2, 0, W_PACKED16, 2, 1.217f, 0.275f, 5.742f),
-    BFQ_GATED_STD(128, 128, 2, 2, 3, W_ROW, 2, 1.014f, 0.458f, 5.405f),
-    BFQ_GATED_STD(128, 128, 2, 2, 3, W_PACKED16, 2, 0.890f, 0.427f, 5.830f),
-    BFQ_GATED_STD(128, 256, 2, 2, 3, W_ROW, 1, 1.301f, 0.824f, 6.088f),
-    BFQ_GATED_STD(128, 256, 2, 2, 3, W_PACKED16, 1, 1.180f, 0.338f, 7.080f),
-    BFQ_GATED_STD(256, 256, 4, 2, 0, W_ROW, 1, 2.001f, 0.510f, 4.738f),
-    BFQ_GATED_STD(256, 256, 4, 2, 0, W_PACKED16, 1, 1.861f, 0.290f, 4.960f),
-    BFQ_GATED_STD(256, 256, 4, 2, 1, W_ROW, 1, 1.904f, 0.665f, 4.860f),
-    BFQ_GATED_STD(256, 256, 4, 2, 3, W_ROW, 1, 1.827f, 0.652f, 4.592f),
-    BFQ_GATED_STD(256, 256, 4, 2, 3, W_PACKED16, 1, 1.766f, 0.243f, 4.914f),
-    BFQ_GATED_RING(16, 1, 4, W_ROW, 10, 0.162f, 0.094f, 4.667f),
-    BFQ_GATED_RING(16, 1, 4, W_PACKED16, 10, 0.164f, 0.090f, 4.762f),
-    BFQ_GATED_RING(16, 2, 4, W_ROW, 5, 0.000f, 0.126f, 4.340f),
-    BFQ_GATED_RING(16, 2, 4, W_PACKED16, 5, 0.000f, 0.120f, 4.408f),
-    BFQ_GATED_RING(32, 2, 4, W_ROW, 5, 0.000f, 0.179f, 4.192f),
-    BFQ_GATED_RING(32, 2, 4, W_PACKED16, 5, 0.000f, 0.174f, 4.207f),
-    BFQ_GATED_RING(64, 2, 3, W_ROW, 4, 0.000f, 0.271f, 4.821f),
-    BFQ_GATED_RING(64, 2, 3, W_PACKED16, 4, 0.000f, 0.266f, 4.922f),
-    BFQ_GATED_SAB(16, 32, 1, 4, 4, 0, 4, 0.001f, 0.093f, 4.037f),
-    BFQ_GATED_SAB(16, 32, 1, 4, 8, 0, 2, 0.000f, 0.079f, 4.549f),
-    BFQ_GATED_SAB(32, 32, 2, 4, 4, 1, 2, 0.000f, 0.269f, 5.311f),
-    BFQ_GATED_SAB(32, 32, 8, 1, 4, 1, 2, 0.002f, 0.712f, 6.910f),
-    BFQ_GATED_SAB(64, 32, 2, 4, 4, 1, 1, 0.007f, 0.364f, 5.901f),
-    BFQ_GATED_SAB(64, 32, 8, 1, 4, 1, 1, 0.000f, 0.764f, 7.413f),
-    BFQ_GATED_SAB(128, 32, 8, 1, 4, 1, 1, 0.001f, 1.091f, 8.584f),
+    BFQ_GATED_PIPE(32, 64, 1, 4, 4, 0, W_ROW, 2, 0.349f, 0.329f, 5.107f),
+    BFQ_GATED_PIPE(32, 64, 1, 4, 4, 0, W_PACKED16, 2, 0.352f, 0.316f, 5.009f),
+    BFQ_GATED_PIPE(32, 64, 1, 4, 4, 3, W_ROW, 2, 0.285f, 0.310f, 5.093f),
+    BFQ_GATED_PIPE(32, 64, 1, 4, 4, 3, W_PACKED16, 2, 0.282f, 0.301f, 4.989f),
+    BFQ_GATED_PIPE(64, 64, 2, 2, 3, 0, W_ROW, 2, 0.484f, 0.390f, 5.551f),
+    BFQ_GATED_PIPE(64, 64, 2, 2, 3, 0, W_PACKED16, 2, 0.474f, 0.366f, 5.459f),
+    BFQ_GATED_PIPE(64, 64, 2, 2, 3, 3, W_ROW, 2, 0.381f, 0.376f, 5.492f),
+    BFQ_GATED_PIPE(64, 64, 2, 2, 3, 3, W_PACKED16, 2, 0.392f, 0.360f, 5.431f),
+    BFQ_GATED_PIPE(64, 128, 2, 4, 3, 0, W_ROW, 1, 0.766f, 0.041f, 6.092f),
+    BFQ_GATED_PIPE(64, 128, 2, 4, 3, 0, W_PACKED16, 1, 0.714f, 0.000f, 6.142f),
+    BFQ_GATED_PIPE(64, 128, 2, 4, 3, 3, W_ROW, 1, 0.738f, 0.000f, 5.995f),
+    BFQ_GATED_PIPE(64, 128, 2, 4, 3, 3, W_PACKED16, 1, 0.692f, 0.041f, 6.081f),
+    BFQ_GATED_PIPE(128, 64, 4, 2, 4, 0, W_ROW, 1, 0.700f, 0.001f, 5.495f),
+    BFQ_GATED_PIPE(128, 64, 4, 2, 4, 0, W_PACKED16, 1, 0.665f, 0.012f, 5.531f),
+    BFQ_GATED_PIPE(128, 64, 4, 2, 4, 3, W_ROW, 1, 0.661f, 0.001f, 5.554f),
+    BFQ_GATED_PIPE(128, 64, 4, 2, 4, 3, W_PACKED16, 1, 0.608f, 0.183f, 5.528f),
+    BFQ_GATED_PIPE(128, 128, 2, 4, 3, 0, W_ROW, 1, 1.163f, 0.631f, 5.905f),
+    BFQ_GATED_PIPE(128, 128, 2, 4, 3, 0, W_PACKED16, 1, 1.156f, 0.054f, 5.905f),
+    BFQ_GATED_PIPE(128, 128, 2, 4, 3, 3, W_ROW, 1, 1.033f, 0.190f, 5.802f),
+    BFQ_GATED_PIPE(128, 128, 2, 4, 3, 3, W_PACKED16, 1, 1.017f, 0.238f, 5.929f),
+    BFQ_GATED_STD(256, 256, 4, 2, 0, W_PACKED16, 1, 1.895f, 0.577f, 4.221f),
+    BFQ_GATED_STD(256, 256, 4, 2, 1, W_ROW, 1, 1.965f, 0.002f, 4.049f),
+    BFQ_GATED_STD(256, 256, 4, 2, 3, W_ROW, 1, 1.881f, 0.442f, 3.857f),
+    BFQ_GATED_STD(256, 256, 4, 2, 3, W_PACKED16, 1, 1.806f, 0.172f, 4.122f),
+    BFQ_GATED_RING(16, 1, 4, W_ROW, 10, 0.163f, 0.095f, 4.624f),
+    BFQ_GATED_RING(16, 1, 4, W_PACKED16, 10, 0.165f, 0.094f, 4.703f),
+    BFQ_GATED_RING(16, 2, 4, W_ROW, 5, 0.000f, 0.127f, 4.288f),
+    BFQ_GATED_RING(16, 2, 4, W_PACKED16, 5, 0.000f, 0.126f, 4.272f),
+    BFQ_GATED_RING(32, 2, 4, W_ROW, 5, 0.000f, 0.178f, 4.223f),
+    BFQ_GATED_RING(32, 2, 4, W_PACKED16, 5, 0.000f, 0.177f, 4.147f),
+    BFQ_GATED_SAB(16, 32, 1, 4, 4, 0, 4, 0.001f, 0.094f, 4.058f),
+    BFQ_GATED_SAB(32, 32, 8, 1, 4, 1, 2, 0.001f, 0.747f, 6.555f),
+    BFQ_GATED_SAB(64, 32, 8, 1, 4, 1, 1, 0.001f, 0.786f, 6.937f),
 };
 
 const GatedKernel* gated_kernels(int* count) {
