@@ -138,22 +138,37 @@ __device__ __forceinline__ uint32_t codes4(const v4f& v, uint32_t mx, float s) {
 // 18432 outputs and their pre-activations (K = 7168) take 1087 us instead of 1126 us; of that, the
 // 302 MB of pre-activations are 73 us. Chunk c of row r sits in slot c ^ (r & (chunks - 1)) of its
 // row, which spreads a column of rows over the banks.
+//
+// Outputs of more bytes than the L2s hold (8 x 4 MB) are stored past them: the next kernel would
+// not find them there, and writing them evicts operands. F 18432 x K 7168, packed, bf16 out: 1024
+// tokens 327 -> 299 us, 4096 tokens 991 -> 973 us (with pre-activations 1040 -> 1005).
+__device__ __forceinline__ bool past_caches(int64_t bytes) { return bytes > (int64_t(32) << 20); }
 template <int ROWB>
 __device__ __forceinline__ uint32_t tile_slot(int r, int byte) {
     constexpr int C = ROWB / 16;
     return (uint32_t)(r * ROWB + (((byte >> 4) ^ (r & (C - 1))) << 4) + (byte & 15));
 }
-// Rows of ROWB bytes from LDS to dst + r * ld, r < rows.
+// Rows of ROWB bytes from LDS to dst + r * ld, r < rows. `past`: past the caches (see
+// past_caches), which the operands that other workgroups still read then keep.
 template <int BM, int ROWB, int THREADS>
-__device__ __forceinline__ void store_tile(const uint8_t* lds, void* dst, int64_t ld, int64_t rows) {
+__device__ __forceinline__ void store_tile(const uint8_t* lds, void* dst, int64_t ld, int64_t rows,
+                                           bool past) {
     constexpr int C = ROWB / 16, STEP = THREADS / C;
     const int r0 = threadIdx.x / C, c = threadIdx.x % C;
 #pragma unroll
     for (int i = 0; i < BM / STEP; ++i) {
         const int r = r0 + i * STEP;
-        if (r < rows)
-            *reinterpret_cast<v4u*>(static_cast<uint8_t*>(dst) + r * ld + c * 16) =
-                *reinterpret_cast<const v4u*>(lds + tile_slot<ROWB>(r, c * 16));
+        if (r < rows) {
+            const v4u v = *reinterpret_cast<const v4u*>(lds + tile_slot<ROWB>(r, c * 16));
+            v4u* o = reinterpret_cast<v4u*>(static_cast<uint8_t*>(dst) + r * ld + c * 16);
+            if (past) {
+                asm volatile("");      // or the compiler makes the two stores one, without the hint
+                __builtin_nontemporal_store(v, o);
+                asm volatile("");
+            } else {
+                *o = v;
+            }
+        }
     }
 }
 
@@ -190,8 +205,8 @@ __device__ __forceinline__ void gated_finish_tile(const GatedArgs& p, uint8_t* l
         put(BM * 2 * BNO, O_BF16, 1);
         lds_barrier();
         uint16_t* pre = static_cast<uint16_t*>(p.pre) + m0 * 2 * F + n0;
-        store_tile<BM, 2 * BNO, THREADS>(lds, pre, 4 * F, live);
-        store_tile<BM, 2 * BNO, THREADS>(lds + BM * 2 * BNO, pre + F, 4 * F, live);
+        store_tile<BM, 2 * BNO, THREADS>(lds, pre, 4 * F, live, past_caches(4 * M * F));
+        store_tile<BM, 2 * BNO, THREADS>(lds + BM * 2 * BNO, pre + F, 4 * F, live, past_caches(4 * M * F));
         lds_barrier();
     }
     gated_product<SM, SG>(p, acc);
@@ -208,7 +223,8 @@ __device__ __forceinline__ void gated_finish_tile(const GatedArgs& p, uint8_t* l
     if (p.otype != O_CODES) {
         put(0, p.otype, 0);
         lds_barrier();
-        store_tile<BM, 2 * BNO, THREADS>(lds, static_cast<uint16_t*>(p.out) + m0 * F + n0, 2 * F, live);
+        store_tile<BM, 2 * BNO, THREADS>(lds, static_cast<uint16_t*>(p.out) + m0 * F + n0, 2 * F, live,
+                                         past_caches(2 * M * F));
         return;
     }
     if constexpr (BNO == 128) {
@@ -239,7 +255,7 @@ __device__ __forceinline__ void gated_finish_tile(const GatedArgs& p, uint8_t* l
                     codes4(acc[sm][sn], m, s);
         }
         lds_barrier();
-        store_tile<BM, BNO, THREADS>(lds, static_cast<uint8_t*>(p.out) + m0 * F + n0, F, live);
+        store_tile<BM, BNO, THREADS>(lds, static_cast<uint8_t*>(p.out) + m0 * F + n0, F, live, past_caches(M * F));
     }
 }
 
