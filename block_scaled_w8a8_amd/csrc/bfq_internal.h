@@ -204,6 +204,10 @@ int mfma_peak_mfmas_per_wave_iter();
 hipError_t launch_block_partials_i32(const void* a, const void* w, int32_t* out, int64_t M,
                                      int64_t N, int64_t K, hipStream_t stream);
 
+// Whether an output of this many bytes is more than the L2s hold (8 x 4 MB): the next kernel would
+// not find it there, and writing it the ordinary way evicts operands still in use.
+__host__ __device__ inline bool past_caches(int64_t bytes) { return bytes > (int64_t(32) << 20); }
+
 // A kernel's opt-in to more than 64 KB of LDS, once a device (`opted`: a bit for each).
 inline hipError_t opt_in_lds(std::atomic<uint64_t>& opted, const void* kernel, int bytes) {
     int dev = 0;

@@ -138,11 +138,9 @@ __device__ __forceinline__ uint32_t codes4(const v4f& v, uint32_t mx, float s) {
 // 18432 outputs and their pre-activations (K = 7168) take 1087 us instead of 1126 us; of that, the
 // 302 MB of pre-activations are 73 us. Chunk c of row r sits in slot c ^ (r & (chunks - 1)) of its
 // row, which spreads a column of rows over the banks.
-//
-// Outputs of more bytes than the L2s hold (8 x 4 MB) are stored past them: the next kernel would
-// not find them there, and writing them evicts operands. F 18432 x K 7168, packed, bf16 out: 1024
-// tokens 327 -> 299 us, 4096 tokens 991 -> 973 us (with pre-activations 1040 -> 1005).
-__device__ __forceinline__ bool past_caches(int64_t bytes) { return bytes > (int64_t(32) << 20); }
+// Outputs of more bytes than the L2s hold are stored past them (past_caches): F 18432 x K 7168,
+// packed, bf16 out: 1024 tokens 326 -> 298 us, 4096 tokens 991 -> 965 us (with pre-activations
+// 1040 -> 990).
 template <int ROWB>
 __device__ __forceinline__ uint32_t tile_slot(int r, int byte) {
     constexpr int C = ROWB / 16;
@@ -822,12 +820,22 @@ const GatedKernel* gated_kernels(int* count) {
 
 // ---------------------------------------------------------------- backward ----
 
+// 16 bytes, with the non-temporal hint if S.
+template <int S> __device__ __forceinline__ uint4 stream_load(const uint4* p) {
+    if constexpr (S) return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p)));
+    else return *p;
+}
+template <int S> __device__ __forceinline__ void stream_store(uint4* p, const uint4& v) {
+    if constexpr (S) __builtin_nontemporal_store(__builtin_bit_cast(v4u, v), reinterpret_cast<v4u*>(p));
+    else *p = v;
+}
+
 // With a = act(g): dg = dh * u * act'(g), du = dh * a, and the product h = a * u again. Eight
-// columns a thread, read once and written once; bytes bound it: 4096 x 18432 takes 179 us for the
-// pair's gradient and h as bf16 (906 MB, 5.1 TB/s) and 123 us for its codes (604 MB, 4.9 TB/s; a
-// large copy reaches 4.8). Codes: 128-column groups of the 2F-wide row, one scale each, 16 lanes a
+// columns a thread, read once and written once; bytes bound it: 4096 x 18432 takes 170 us for the
+// pair's gradient and h as bf16 (906 MB, 5.3 TB/s; 179 without the non-temporal hints) and 116 us
+// for its codes (604 MB, 5.2 TB/s; a large copy reaches 4.8). Codes: 128-column groups of the 2F-wide row, one scale each, 16 lanes a
 // group; rows past M (packed words only) write zeros.
-template <int Q>
+template <int Q, int S>
 __global__ __launch_bounds__(256) void gated_bwd_kernel(GatedBwdArgs p) {
     const int lane = threadIdx.x & 63;
     const int64_t m = blockIdx.x, F = p.F, c = (int64_t)blockIdx.y * 256 + threadIdx.x;
@@ -837,8 +845,8 @@ __global__ __launch_bounds__(256) void gated_bwd_kernel(GatedBwdArgs p) {
     for (int i = 0; i < 8; ++i) dg[i] = du[i] = 0.f;
     if (live && real) {
         const uint4* pre = static_cast<const uint4*>(p.pre) + m * 2 * F / 8;
-        const uint4 gc = pre[c], uc = pre[F / 8 + c];
-        const uint4 dc = static_cast<const uint4*>(p.dh)[m * F / 8 + c];
+        const uint4 gc = stream_load<S>(pre + c), uc = stream_load<S>(pre + F / 8 + c);
+        const uint4 dc = stream_load<S>(static_cast<const uint4*>(p.dh) + m * F / 8 + c);
         float g[8], u[8], dh[8], h[8];
         unpack8(gc, g);
         unpack8(uc, u);
@@ -851,11 +859,11 @@ __global__ __launch_bounds__(256) void gated_bwd_kernel(GatedBwdArgs p) {
             dg[i] = dh[i] * u[i] * slope;
             du[i] = dh[i] * a;
         }
-        if (p.h) static_cast<uint4*>(p.h)[m * F / 8 + c] = pack8(h);
+        if (p.h) stream_store<S>(static_cast<uint4*>(p.h) + m * F / 8 + c, pack8(h));
         if (p.dpre) {
             uint4* d = static_cast<uint4*>(p.dpre) + m * 2 * F / 8;
-            d[c] = pack8(dg);
-            d[F / 8 + c] = pack8(du);
+            stream_store<S>(d + c, pack8(dg));
+            stream_store<S>(d + F / 8 + c, pack8(du));
         }
     }
     if constexpr (Q >= 0) {
@@ -875,12 +883,18 @@ __global__ __launch_bounds__(256) void gated_bwd_kernel(GatedBwdArgs p) {
     }
 }
 
-hipError_t launch_gated_bwd(const GatedBwdArgs& a, hipStream_t stream) {
+template <int S>
+static void launch_bwd(const GatedBwdArgs& a, hipStream_t stream) {
     const int64_t rows = a.q && a.packed ? (a.M + 3) / 4 * 4 : a.M;
     const dim3 grid((unsigned)rows, (unsigned)((a.F / 8 + 255) / 256));
-    if (!a.q) hipLaunchKernelGGL(gated_bwd_kernel<-1>, grid, dim3(256), 0, stream, a);
-    else if (a.qtype == Q_FP8) hipLaunchKernelGGL(gated_bwd_kernel<Q_FP8>, grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL(gated_bwd_kernel<Q_INT8>, grid, dim3(256), 0, stream, a);
+    if (!a.q) hipLaunchKernelGGL((gated_bwd_kernel<-1, S>), grid, dim3(256), 0, stream, a);
+    else if (a.qtype == Q_FP8) hipLaunchKernelGGL((gated_bwd_kernel<Q_FP8, S>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((gated_bwd_kernel<Q_INT8, S>), grid, dim3(256), 0, stream, a);
+}
+
+hipError_t launch_gated_bwd(const GatedBwdArgs& a, hipStream_t stream) {
+    if (past_caches(a.M * a.F * ((a.dpre ? 4 : 0) + (a.q ? 2 : 0) + (a.h ? 2 : 0)))) launch_bwd<1>(a, stream);
+    else launch_bwd<0>(a, stream);
     return hipGetLastError();
 }
 

@@ -6,8 +6,8 @@
 // GEMMs read (the token quantizer's formats), or both. All of it in fp32; n is taken from the
 // unrounded r' and quantized unrounded, so storing r' or n as bf16 costs the codes nothing.
 //
-// What bounds it: bytes. 4096 rows of 7168 with post norm, codes out: 46 us, 206 MB at 4.4 TB/s
-// (a large copy reaches 4.8). A row is read once (y, r) and written once (r', codes), everything
+// What bounds it: bytes. 4096 rows of 7168 with post norm, codes out: 44.8 us, 206 MB at 4.6 TB/s
+// (a large copy reaches 4.8; without the non-temporal hints 48.8). A row is read once (y, r) and written once (r', codes), everything
 // between stays in registers: P chunks of 8 elements a thread, chunk c of the row held by thread
 // c % T in slot c / T, so 16 neighbouring lanes own one 128-element group as in the token
 // quantizer. Each norm costs one reduction over the workgroup (DPP within a wave, LDS across).
@@ -23,11 +23,16 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void* p, int64_
     const uint8_t* base = static_cast<const uint8_t*>(p) + (p ? m * bytes : 0);
     return make_rsrc(base, p ? bytes : 0);
 }
-__device__ __forceinline__ v4u load16(__amdgpu_buffer_rsrc_t r, uint32_t voff) {
-    return __builtin_amdgcn_raw_buffer_load_b128(r, voff, 0, 0);
+// S = 1: with the non-temporal hint, for rows of a call that writes more than the L2s hold
+// (past_caches): nobody finds them there, and the channel vectors keep their place.
+constexpr int kNonTemporal = 2;                          // the cache policy operand's bit
+template <int S = 0>
+__device__ __forceinline__ v4u load16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff = 0) {
+    return __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, S ? kNonTemporal : 0);
 }
-__device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t r, uint32_t voff, const v4u& v) {
-    __builtin_amdgcn_raw_buffer_store_b128(v, r, voff, 0, 0);
+template <int S>
+__device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t r, uint32_t voff, const v4u& v, uint32_t soff = 0) {
+    __builtin_amdgcn_raw_buffer_store_b128(v, r, voff, soff, S ? kNonTemporal : 0);
 }
 __device__ __forceinline__ void unpack(const v4u& v, float* x) {
     unpack8(make_uint4(v.x, v.y, v.z, v.w), x);
@@ -37,28 +42,28 @@ __device__ __forceinline__ v4u pack(const float* x) {
 }
 
 // Eight values of the residual stream at byte offset voff of a bf16 row (twice that of fp32).
-template <int F32> struct Chunk;
-template <> struct Chunk<0> {
+template <int F32, int S> struct Chunk;
+template <int S> struct Chunk<0, S> {
     v4u v;
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t voff) { v = load16(r, voff); }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t voff) { v = load16<S>(r, voff); }
     __device__ __forceinline__ void get(float* x) const { unpack(v, x); }
     static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t voff, const float* x) {
-        store16(r, voff, pack(x));
+        store16<S>(r, voff, pack(x));
     }
 };
-template <> struct Chunk<1> {
+template <int S> struct Chunk<1, S> {
     v4f a, b;
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t voff) {
-        a = buf_load_v4f(r, 2 * voff, 0);
-        b = buf_load_v4f(r, 2 * voff, 16);
+        a = __builtin_bit_cast(v4f, load16<S>(r, 2 * voff));
+        b = __builtin_bit_cast(v4f, load16<S>(r, 2 * voff, 16));
     }
     __device__ __forceinline__ void get(float* x) const {
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
         x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     }
     static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t voff, const float* x) {
-        buf_store_v4f(r, v4f{x[0], x[1], x[2], x[3]}, 2 * voff, 0);
-        buf_store_v4f(r, v4f{x[4], x[5], x[6], x[7]}, 2 * voff, 16);
+        store16<S>(r, 2 * voff, __builtin_bit_cast(v4u, v4f{x[0], x[1], x[2], x[3]}));
+        store16<S>(r, 2 * voff, __builtin_bit_cast(v4u, v4f{x[4], x[5], x[6], x[7]}), 16);
     }
 };
 
@@ -83,7 +88,7 @@ template <int P> constexpr int kNormThreads = P == 4 ? 512 : 1024;
 
 // One row a workgroup. Q: -1 no codes, else Q_FP8 / Q_INT8. Rows M .. (packed scale words: up to a
 // multiple of 4) exist only to write zero words.
-template <int P, int RF32, int Q>
+template <int P, int RF32, int Q, int S>
 __global__ __launch_bounds__(kNormThreads<P>) void norm_residual_kernel(NormArgs p) {
     const int t = threadIdx.x, lane = t & 63, T = blockDim.x;
     const int64_t m = blockIdx.x, K = p.K;
@@ -107,12 +112,12 @@ __global__ __launch_bounds__(kNormThreads<P>) void norm_residual_kernel(NormArgs
     // P = 1 (few rows): every load up front, one trip to memory. Else the channel vectors, which
     // hit L2, come only when they are needed: fewer registers, more rows in flight on a CU.
     uint32_t voff[P];
-    Chunk<RF32> rc[P];
+    Chunk<RF32, S> rc[P];
     v4u yc[P], gc[P], wpost[P], wpre[P];
 #pragma unroll
     for (int u = 0; u < P; ++u) {
         voff[u] = (uint32_t)(u * T + t) * 16;
-        yc[u] = load16(r_y, voff[u]);
+        yc[u] = load16<S>(r_y, voff[u]);
         rc[u].load(r_res, voff[u]);
     }
     auto load_post = [&]() {
@@ -160,7 +165,7 @@ __global__ __launch_bounds__(kNormThreads<P>) void norm_residual_kernel(NormArgs
             r[u][i] = __builtin_fmaf(y[i] * c * w[i], g[i], r[u][i]);
             s[0] = __builtin_fmaf(r[u][i], r[u][i], s[0]);
         }
-        Chunk<RF32>::store(r_out, voff[u], r[u]);
+        Chunk<RF32, S>::store(r_out, voff[u], r[u]);
     }
     if (!p.w_pre) return;                                 // uniform
     if constexpr (P > 1) {
@@ -175,14 +180,14 @@ __global__ __launch_bounds__(kNormThreads<P>) void norm_residual_kernel(NormArgs
         unpack(wpre[u], w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) r[u][i] = r[u][i] * ir * w[i];
-        store16(r_n, voff[u], pack(r[u]));
+        store16<S>(r_n, voff[u], pack(r[u]));
     }
     if constexpr (Q >= 0) {
         const __amdgpu_buffer_rsrc_t r_q = row_rsrc(p.q, m, (uint32_t)K);
         auto store_codes = [&](int u, uint32_t mx, float sc) {
             const uint2 q = encode8_group<Q>(r[u], mx, sc);
             typedef unsigned int v2u __attribute__((ext_vector_type(2)));
-            __builtin_amdgcn_raw_buffer_store_b64(v2u{q.x, q.y}, r_q, voff[u] / 2, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(v2u{q.x, q.y}, r_q, voff[u] / 2, 0, S ? kNonTemporal : 0);
         };
         // lanes past the row hold zeros: they join the reductions and store nothing
         if (p.per_token) {
@@ -234,11 +239,11 @@ __global__ __launch_bounds__(kNormThreads<P>) void norm_residual_kernel(NormArgs
 // (K > 8192): registers hold a row only, so the sums live in LDS (each thread its own slots), the
 // vectors come from L2, and the next row's loads start once their registers are free, all but y's
 // before the second reduction.
-// Bytes bound it. Measured: 4096 rows of 7168 bf16 with a channel gate 86 us with the column sums
-// (352 MB, 4.1 TB/s; two chunks a thread there 96), 4096 of 8192 fp32 127 us (4.8 TB/s; 140),
+// Bytes bound it. Measured: 4096 rows of 7168 bf16 with a channel gate 81 us with the column sums
+// (352 MB, 4.3 TB/s; two chunks a thread there some 10 more), 4096 of 8192 fp32 127 us (4.8 TB/s; 140),
 // 1024 of 16384 fp32 85 us (3.6 TB/s: four rows a CU, the first and last uncovered; with the sums
 // of two chunks in registers, which spill, 138).
-template <int P, int RF32>
+template <int P, int RF32, int S>
 __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
     const int t = threadIdx.x, T = blockDim.x;
     const int64_t K = p.K;
@@ -251,7 +256,7 @@ __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
     const bool channel = p.gate_kind == BFQ_GATE_CHANNEL, elements = p.gate_kind == BFQ_GATE_FULL;
     const bool post = p.w_post != nullptr;
     struct Row {
-        Chunk<RF32> r, d;       // the stored sum, the stream's gradient
+        Chunk<RF32, S> r, d;       // the stored sum, the stream's gradient
         v4u y, n;               // the block's output, the gradient at its normed successor
     };
     // element gates of row m
@@ -272,9 +277,9 @@ __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
             const uint32_t voff = (uint32_t)(u * T + t) * 16;
             if (others) {
                 x[u].r.load(rr, voff);
-                x[u].n = load16(rn, voff);
+                x[u].n = load16<S>(rn, voff);
             }
-            if (y) x[u].y = load16(ry, voff);
+            if (y) x[u].y = load16<S>(ry, voff);
             if (others) x[u].d.load(rd, voff);
         }
     };
@@ -357,7 +362,7 @@ __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
                 r[i] *= ir;
             }
             add(0, u, dn, r);
-            Chunk<RF32>::store(o_r, voff, dr);
+            Chunk<RF32, S>::store(o_r, voff, dr);
             unpack(cur[u].y, y);
             unpack(ones_unless(channel ? gate_at(u * T + t) : load16(rg, voff), channel || elements), g);
             unpack(w_post_at(u * T + t), w);
@@ -372,7 +377,7 @@ __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
                 dr[i] = channel ? ad : dz[u][i];
             }
             add(1, u, dr, y);
-            store16(o_g, voff, pack(dg));
+            store16<S>(o_g, voff, pack(dg));
         }
         if constexpr (P > 1) load(cur, m + gridDim.x, false, true);
         block_sum<2>(q, red[par] + 3 * 16);
@@ -385,7 +390,7 @@ __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
             unpack(w_post_at(u * T + t), w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dz[u][i] = iy * __builtin_fmaf(-y[i], cy, w[i] * dz[u][i]);
-            store16(o_y, (uint32_t)(u * T + t) * 16, pack(dz[u]));
+            store16<S>(o_y, (uint32_t)(u * T + t) * 16, pack(dz[u]));
         }
         if constexpr (P == 1) cur[0] = next[0];
         else load(cur, m + gridDim.x, true, false);
@@ -398,8 +403,8 @@ __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
     for (int u = 0; u < P; ++u) {
         const uint32_t voff = (uint32_t)(u * T + t) * 16;
         if constexpr (P == 1) {
-            Chunk<1>::store(s0, voff, apre[0]);
-            Chunk<1>::store(s1, voff, apost[0]);
+            Chunk<1, 0>::store(s0, voff, apre[0]);
+            Chunk<1, 0>::store(s1, voff, apost[0]);
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -449,17 +454,23 @@ static unsigned threads_for(int64_t K, int P) {
     return (unsigned)((K / 8 + 64 * P - 1) / (64 * P) * 64);
 }
 
-template <int P, int RF32>
+template <int P, int RF32, int S>
 static hipError_t launch_norm_q(const NormArgs& a, hipStream_t stream) {
     const int64_t rows = a.packed ? (a.M + 3) / 4 * 4 : a.M;
     const dim3 grid((unsigned)rows), block(threads_for(a.K, P));
     if (!a.q)
-        hipLaunchKernelGGL((norm_residual_kernel<P, RF32, -1>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((norm_residual_kernel<P, RF32, -1, S>), grid, block, 0, stream, a);
     else if (a.qtype == Q_FP8)
-        hipLaunchKernelGGL((norm_residual_kernel<P, RF32, Q_FP8>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((norm_residual_kernel<P, RF32, Q_FP8, S>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((norm_residual_kernel<P, RF32, Q_INT8>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((norm_residual_kernel<P, RF32, Q_INT8, S>), grid, block, 0, stream, a);
     return hipGetLastError();
+}
+
+template <int P, int RF32>
+static hipError_t launch_norm_s(const NormArgs& a, hipStream_t stream) {
+    const int64_t out = (a.res_out ? (RF32 ? 4 : 2) : 0) + (a.normed ? 2 : 0) + (a.q ? 1 : 0);
+    return past_caches(a.M * a.K * out) ? launch_norm_q<P, RF32, 1>(a, stream) : launch_norm_q<P, RF32, 0>(a, stream);
 }
 
 // Chunks a thread. Few waves a row start and reduce sooner (one row of 1536: 3.4 us with one chunk
@@ -468,9 +479,9 @@ static hipError_t launch_norm_q(const NormArgs& a, hipStream_t stream) {
 // 25.8 with four).
 template <int RF32>
 static hipError_t launch_norm_p(const NormArgs& a, hipStream_t stream) {
-    if (a.K <= 2048) return launch_norm_q<1, RF32>(a, stream);
-    if (a.K <= 8192 || a.M <= 256) return launch_norm_q<2, RF32>(a, stream);
-    return launch_norm_q<4, RF32>(a, stream);
+    if (a.K <= 2048) return launch_norm_s<1, RF32>(a, stream);
+    if (a.K <= 8192 || a.M <= 256) return launch_norm_s<2, RF32>(a, stream);
+    return launch_norm_s<4, RF32>(a, stream);
 }
 
 hipError_t launch_norm_residual(const NormArgs& a, int res_f32, hipStream_t stream) {
@@ -484,17 +495,24 @@ int64_t norm_bwd_groups(int64_t M, int64_t K) {
     return M < most ? M : most;
 }
 
-template <int P, int RF32>
-static hipError_t launch_bwd(const NormArgs& a, int64_t groups, hipStream_t stream) {
+template <int P, int RF32, int S>
+static hipError_t launch_bwd_s(const NormArgs& a, int64_t groups, hipStream_t stream) {
     const unsigned threads = threads_for(a.K, P), lds = threads * (P == 1 ? 48 : 128);
     if constexpr (P > 1) {
         static std::atomic<uint64_t> opted{0};
         const hipError_t e = opt_in_lds(
-            opted, reinterpret_cast<const void*>(&norm_residual_bwd_kernel<P, RF32>), 1024 * 128);
+            opted, reinterpret_cast<const void*>(&norm_residual_bwd_kernel<P, RF32, S>), 1024 * 128);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((norm_residual_bwd_kernel<P, RF32>), dim3((unsigned)groups), dim3(threads), lds, stream, a);
+    hipLaunchKernelGGL((norm_residual_bwd_kernel<P, RF32, S>), dim3((unsigned)groups), dim3(threads), lds, stream, a);
     return hipGetLastError();
+}
+
+template <int P, int RF32>
+static hipError_t launch_bwd(const NormArgs& a, int64_t groups, hipStream_t stream) {
+    const int64_t out = (RF32 ? 4 : 2) + (a.d_y ? 2 : 0) + (a.d_gate && a.gate_kind == BFQ_GATE_FULL ? 2 : 0);
+    return past_caches(a.M * a.K * out) ? launch_bwd_s<P, RF32, 1>(a, groups, stream)
+                                        : launch_bwd_s<P, RF32, 0>(a, groups, stream);
 }
 
 hipError_t launch_norm_residual_bwd(const NormArgs& a, int res_f32, hipStream_t stream) {

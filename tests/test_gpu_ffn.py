@@ -823,3 +823,43 @@ def test_readme_example():
     torch.cuda.synchronize()
     assert env["out"].shape == (64, 7168) and env["dx"].shape == (64, 7168)
     assert all(bool(env[n].float().isfinite().all()) for n in ("y", "res", "out", "dx"))
+
+
+@pytest.mark.parametrize("rt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K", [1536, 7168, 12288])
+def test_large_outputs_equal_small_ones(bfq, K, rt):
+    """Calls that write more than the L2s hold store past them; their rows are those of a small
+    call, bit for bit (300 rows: fewer may split a long row over more threads)."""
+    M = (40 << 20) // (2 * K)
+    some = torch.linspace(0, M - 1, 300, device=DEV).long()
+    c = _norm_case(M, K, True, 3, rt, K)
+    small = {k: v[some].contiguous() if k in ("residual", "y", "gate") else v for k, v in c.items()}
+    for kw in (dict(codes=False), dict(codes=True), dict(codes=True, q_dtype=bfq.BFQ_INT8, per_token=True)):
+        for a, b in zip(bfq.norm_residual(**c, **kw), bfq.norm_residual(**small, **kw)):
+            assert torch.equal(a[some], b)
+    r, rs = c.pop("residual"), small.pop("residual")
+    dn, dro = (_randn(K + 1, M, K) * 0.1).bfloat16(), (_randn(K + 2, M, K) * 0.1).to(rt)
+    a = bfq.norm_residual_backward(r, **c, d_normed=dn, d_res_out=dro)
+    b = bfq.norm_residual_backward(rs, **small, d_normed=dn[some].contiguous(), d_res_out=dro[some].contiguous())
+    for k in ("d_res", "d_y", "d_gate"):
+        assert torch.equal(a[k][some], b[k]), k
+
+
+def test_large_gated_outputs_equal_small_ones(bfq):
+    F, K = 2048, 256
+    M = (40 << 20) // F                               # more than 32 MB even as codes
+    some = torch.tensor([0, 1, M // 2, M - 1], device=DEV)
+    for wl, sfmt in ((0, 0), (1, 0), (1, 1)):
+        qa, sa, qw, sw, _ = _pair(bfq, M, F, K, 11, sfmt, wl)
+        t = bfq.bfq_gated_select_tile(M, F, K, bfq.BFQ_E4M3FN, wl, sfmt)
+        kw = dict(keep_preact=True, tile=t, w_layout=wl, scale_fmt=sfmt)
+        qs, ss = qa[some].contiguous(), sa[some].contiguous()
+        for codes in (False, True):
+            for a, b in zip(bfq.gated_gemm(qa, sa, qw, sw, codes=codes, **kw),
+                            bfq.gated_gemm(qs, ss, qw, sw, codes=codes, **kw)):
+                assert torch.equal(a[some], b)
+    pre, dh = _randn(12, M, 2 * F).bfloat16(), _randn(13, M, F).bfloat16()
+    for codes in (False, True):
+        for a, b in zip(bfq.gated_backward(pre, dh, codes=codes, want_h=True),
+                        bfq.gated_backward(pre[some].contiguous(), dh[some].contiguous(), codes=codes, want_h=True)):
+            assert torch.equal(a[some], b)
