@@ -102,7 +102,7 @@ float gated_us(const GatedKernel& k, int64_t M, int64_t F, int64_t K, bool codes
         return std::sqrt(std::sqrt(a * a * a * a + b * b * b * b)) + k.fix;
     };
     float us = (float)full * round(k.occupancy) + (rest ? round(ceil_div(rest, kNumCUs)) : 0.f);
-    const float rate = t.variant == 0 ? 4.6e6f : ring_strip(k) ? 5.0e6f : 5.88e6f;
+    const float rate = t.variant == 0 ? 4.63e6f : ring_strip(k) ? 5.62e6f : 5.93e6f;
     float stream = 2.f * (float)F * (float)K / rate;
     if (ring_strip(k)) stream *= 0.5f + 0.5f * (float)ceil_div(M, t.bm);
     const float x = us > stream ? stream / us : us / stream, x2 = x * x, x4 = x2 * x2;

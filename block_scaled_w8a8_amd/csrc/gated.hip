@@ -14,8 +14,8 @@
 // What bounds the forward kernels is what bounds the block GEMM's: the weight stream at decode
 // sizes, the operand bytes through a CU's L1 and the scale step at large M. Measured, F 18432 x
 // K 7168, packed weights, SILU, bf16 out: 1 token 42 us (6.3 TB/s of weights), 64 tokens 56 us,
-// 512 tokens 204 us, 4096 tokens 1002 us with fp32 scales (2.16 PFLOP/s) and 895 us with powers of
-// two, 73 us more where the pre-activations are kept (302 MB).
+// 512 tokens 204 us, 4096 tokens 965 us with fp32 scales (2.24 PFLOP/s) and 890 us with powers of
+// two, 25 to 80 us more, by the box, where the pre-activations are kept (302 MB).
 // The two sums carry the e4m3 MFMA's own error, as the block GEMM's do: 3.5e-5 to 4.6e-5 of the
 // result (relative, Frobenius) on outlier-bearing tokens, whichever schedule or tile. Where codes
 // are wanted it decides the values that lie that near to a rounding boundary: 333 x 2048 codes
@@ -134,10 +134,9 @@ __device__ __forceinline__ uint32_t codes4(const v4f& v, uint32_t mx, float s) {
 
 // Output tiles leave through LDS: a lane's accumulators hold four neighbouring columns of 16 rows a
 // sub-tile, 32-byte pieces of a row in a store, so the tile is laid out as rows of 16-byte chunks
-// and stored as whole rows. With the hardware's bf16 conversion in place of the integer one, 4096 x
-// 18432 outputs and their pre-activations (K = 7168) take 1087 us instead of 1126 us; of that, the
-// 302 MB of pre-activations are 73 us. Chunk c of row r sits in slot c ^ (r & (chunks - 1)) of its
-// row, which spreads a column of rows over the banks.
+// and stored as whole rows: with the hardware's bf16 conversion in place of the integer one, 39 us
+// less for 4096 x 18432 outputs and their pre-activations (K = 7168). Chunk c of row r sits in slot
+// c ^ (r & (chunks - 1)) of its row, which spreads a column of rows over the banks.
 // Outputs of more bytes than the L2s hold are stored past them (past_caches): F 18432 x K 7168,
 // packed, bf16 out: 1024 tokens 326 -> 298 us, 4096 tokens 991 -> 965 us (with pre-activations
 // 1040 -> 990).
@@ -491,6 +490,14 @@ __global__ __launch_bounds__(64 * NWAVES * KW) void gemm_gated_swapab_lds_kernel
     swapab_lds_body<MT, NWR, NWAVES, KW, D, Q_FP8, O_FP32, W_PACKED16, CH, 0, 1>(p);
 }
 
+// 16 bytes per lane from global memory into LDS (dma16), with the non-temporal hint if ONCE.
+template <int ONCE>
+__device__ __forceinline__ void dma16_weights(__amdgpu_buffer_rsrc_t r, uint8_t* lds_base,
+                                              uint32_t lds_off, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        r, (__attribute__((address_space(3))) void*)(lds_base + lds_off), 16, voff, soff, 0, ONCE ? 2 : 0);
+}
+
 // Strips for a few tokens, the weights through LDS; the weight stream bounds them. A workgroup
 // takes 16 output columns (16 gate rows, 16 up rows) and its waves every KW-th K block, so that
 // together they walk neighbouring bytes of the weights. Each wave copies 1 KB a load (row-major:
@@ -499,12 +506,14 @@ __global__ __launch_bounds__(64 * NWAVES * KW) void gemm_gated_swapab_lds_kernel
 // its oldest block have landed, and what is in flight takes no registers, so a CU holds up to 10
 // waves of 16 KB in flight each. Row-major chunk c of row r sits in slot c ^ swz(r), as in the
 // standard tiles.
-// Row-major, F 18432 x K 7168: 50 us for 1 token (5.3 TB/s of weights), 52.5 for 16; fragment loads
-// straight from the rows take half a line of each of 16 rows a request: 61 and 62 us, 4.3 TB/s.
-// Packed: ahead of the strips above where the products are short (F 5632 x K 2048, 16 tokens: 7.9 us
-// against 10.8; F 4096 x K 4096: 9.5 against 11.5) and behind on long streams (F 18432 x K 7168, 1
-// token: 48 against 43).
-template <int MT, int KW, int D, int WL, int CH>
+// ONCE (M <= MT): no other workgroup reads these weights, and they are loaded with the non-temporal
+// hint: 10 % off the time at F 18432 and 5 to 13 % on short products. With more tokens it would cost
+// up to 6 %: the tiles above find the weights in L2.
+// Row-major, F 18432 x K 7168: 45.4 us for 1 token (5.8 TB/s of weights), 49.5 for 16; fragment
+// loads straight from the rows take half a line of each of 16 rows a request: 61 and 62 us. Packed:
+// ahead of the strips above where the products are short (F 4096 x K 4096, 16 tokens: 8.8 us against
+// 11.5) and behind on long streams (F 18432 x K 7168, 1 token: 49 against 43).
+template <int MT, int KW, int D, int WL, int CH, int ONCE>
 __global__ __launch_bounds__(64 * KW) void gemm_gated_ring_kernel(GatedArgs p) {
     constexpr int SM = MT / 16, BLOCK = 4096;
     constexpr bool PK = CH == 2;
@@ -563,10 +572,10 @@ __global__ __launch_bounds__(64 * KW) void gemm_gated_ring_kernel(GatedArgs p) {
         swb[slot] = buf_f32(rsg, 0, sws);
         swu[slot] = buf_f32(rsu, 0, sws);
         kbs[slot] = (int)(kb & 3);
-        dma16(rw, lds, at, c0, ws);
-        dma16(rw, lds, at + 1024, c1, ws);
-        dma16(ru, lds, at + 2048, c0, ws);
-        dma16(ru, lds, at + 3072, c1, ws);
+        dma16_weights<ONCE>(rw, lds, at, c0, ws);
+        dma16_weights<ONCE>(rw, lds, at + 1024, c1, ws);
+        dma16_weights<ONCE>(ru, lds, at + 2048, c0, ws);
+        dma16_weights<ONCE>(ru, lds, at + 3072, c1, ws);
 #pragma unroll
         for (int sm = 0; sm < SM; ++sm) {
             abuf[slot][sm][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, a_voff[sm], s, 0);
@@ -741,16 +750,22 @@ hipError_t launch_gated_swapab(const GatedArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int MT, int KW, int D, int WL, int CH>
-hipError_t launch_gated_ring(const GatedArgs& a, hipStream_t stream) {
+template <int MT, int KW, int D, int WL, int CH, int ONCE>
+hipError_t launch_gated_ring_once(const GatedArgs& a, hipStream_t stream) {
     constexpr int LDS_BYTES = KW * D * 4096;
     static std::atomic<uint64_t> opted{0};
     const hipError_t e =
-        opt_in_lds(opted, reinterpret_cast<const void*>(&gemm_gated_ring_kernel<MT, KW, D, WL, CH>), LDS_BYTES);
+        opt_in_lds(opted, reinterpret_cast<const void*>(&gemm_gated_ring_kernel<MT, KW, D, WL, CH, ONCE>), LDS_BYTES);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)(a.N / 16), (unsigned)((a.M + MT - 1) / MT), (unsigned)a.split);
-    hipLaunchKernelGGL((gemm_gated_ring_kernel<MT, KW, D, WL, CH>), grid, dim3(64 * KW), LDS_BYTES, stream, a);
+    hipLaunchKernelGGL((gemm_gated_ring_kernel<MT, KW, D, WL, CH, ONCE>), grid, dim3(64 * KW), LDS_BYTES, stream, a);
     return hipGetLastError();
+}
+
+template <int MT, int KW, int D, int WL, int CH>
+hipError_t launch_gated_ring(const GatedArgs& a, hipStream_t stream) {
+    return a.M <= MT ? launch_gated_ring_once<MT, KW, D, WL, CH, 1>(a, stream)
+                     : launch_gated_ring_once<MT, KW, D, WL, CH, 0>(a, stream);
 }
 
 // The last four arguments are what the tile rule knows of a kernel: the workgroups a CU holds, and
@@ -778,39 +793,39 @@ hipError_t launch_gated_ring(const GatedArgs& a, hipStream_t stream) {
                 (SC) == 3 ? S_UE8M0 : S_FP32, &launch_gated_pipe<BM, BNO, WM, WN, D, SC, WL>, OCC, LAT, THR, FIX}
 
 static const GatedKernel kGatedKernels[] = {
-    BFQ_GATED_PIPE(32, 64, 1, 4, 4, 0, W_ROW, 2, 0.349f, 0.329f, 5.107f),
-    BFQ_GATED_PIPE(32, 64, 1, 4, 4, 0, W_PACKED16, 2, 0.352f, 0.316f, 5.009f),
-    BFQ_GATED_PIPE(32, 64, 1, 4, 4, 3, W_ROW, 2, 0.285f, 0.310f, 5.093f),
-    BFQ_GATED_PIPE(32, 64, 1, 4, 4, 3, W_PACKED16, 2, 0.282f, 0.301f, 4.989f),
-    BFQ_GATED_PIPE(64, 64, 2, 2, 3, 0, W_ROW, 2, 0.484f, 0.390f, 5.551f),
-    BFQ_GATED_PIPE(64, 64, 2, 2, 3, 0, W_PACKED16, 2, 0.474f, 0.366f, 5.459f),
-    BFQ_GATED_PIPE(64, 64, 2, 2, 3, 3, W_ROW, 2, 0.381f, 0.376f, 5.492f),
-    BFQ_GATED_PIPE(64, 64, 2, 2, 3, 3, W_PACKED16, 2, 0.392f, 0.360f, 5.431f),
-    BFQ_GATED_PIPE(64, 128, 2, 4, 3, 0, W_ROW, 1, 0.766f, 0.041f, 6.092f),
-    BFQ_GATED_PIPE(64, 128, 2, 4, 3, 0, W_PACKED16, 1, 0.714f, 0.000f, 6.142f),
-    BFQ_GATED_PIPE(64, 128, 2, 4, 3, 3, W_ROW, 1, 0.738f, 0.000f, 5.995f),
-    BFQ_GATED_PIPE(64, 128, 2, 4, 3, 3, W_PACKED16, 1, 0.692f, 0.041f, 6.081f),
-    BFQ_GATED_PIPE(128, 64, 4, 2, 4, 0, W_ROW, 1, 0.700f, 0.001f, 5.495f),
-    BFQ_GATED_PIPE(128, 64, 4, 2, 4, 0, W_PACKED16, 1, 0.665f, 0.012f, 5.531f),
-    BFQ_GATED_PIPE(128, 64, 4, 2, 4, 3, W_ROW, 1, 0.661f, 0.001f, 5.554f),
-    BFQ_GATED_PIPE(128, 64, 4, 2, 4, 3, W_PACKED16, 1, 0.608f, 0.183f, 5.528f),
-    BFQ_GATED_PIPE(128, 128, 2, 4, 3, 0, W_ROW, 1, 1.163f, 0.631f, 5.905f),
-    BFQ_GATED_PIPE(128, 128, 2, 4, 3, 0, W_PACKED16, 1, 1.156f, 0.054f, 5.905f),
-    BFQ_GATED_PIPE(128, 128, 2, 4, 3, 3, W_ROW, 1, 1.033f, 0.190f, 5.802f),
-    BFQ_GATED_PIPE(128, 128, 2, 4, 3, 3, W_PACKED16, 1, 1.017f, 0.238f, 5.929f),
-    BFQ_GATED_STD(256, 256, 4, 2, 0, W_PACKED16, 1, 1.895f, 0.577f, 4.221f),
-    BFQ_GATED_STD(256, 256, 4, 2, 1, W_ROW, 1, 1.965f, 0.002f, 4.049f),
-    BFQ_GATED_STD(256, 256, 4, 2, 3, W_ROW, 1, 1.881f, 0.442f, 3.857f),
-    BFQ_GATED_STD(256, 256, 4, 2, 3, W_PACKED16, 1, 1.806f, 0.172f, 4.122f),
-    BFQ_GATED_RING(16, 1, 4, W_ROW, 10, 0.163f, 0.095f, 4.624f),
-    BFQ_GATED_RING(16, 1, 4, W_PACKED16, 10, 0.165f, 0.094f, 4.703f),
-    BFQ_GATED_RING(16, 2, 4, W_ROW, 5, 0.000f, 0.127f, 4.288f),
-    BFQ_GATED_RING(16, 2, 4, W_PACKED16, 5, 0.000f, 0.126f, 4.272f),
-    BFQ_GATED_RING(32, 2, 4, W_ROW, 5, 0.000f, 0.178f, 4.223f),
-    BFQ_GATED_RING(32, 2, 4, W_PACKED16, 5, 0.000f, 0.177f, 4.147f),
-    BFQ_GATED_SAB(16, 32, 1, 4, 4, 0, 4, 0.001f, 0.094f, 4.058f),
-    BFQ_GATED_SAB(32, 32, 8, 1, 4, 1, 2, 0.001f, 0.747f, 6.555f),
-    BFQ_GATED_SAB(64, 32, 8, 1, 4, 1, 1, 0.001f, 0.786f, 6.937f),
+    BFQ_GATED_PIPE(32, 64, 1, 4, 4, 0, W_ROW, 2, 0.351f, 0.332f, 5.060f),
+    BFQ_GATED_PIPE(32, 64, 1, 4, 4, 0, W_PACKED16, 2, 0.356f, 0.317f, 4.915f),
+    BFQ_GATED_PIPE(32, 64, 1, 4, 4, 3, W_ROW, 2, 0.283f, 0.313f, 5.061f),
+    BFQ_GATED_PIPE(32, 64, 1, 4, 4, 3, W_PACKED16, 2, 0.283f, 0.301f, 4.891f),
+    BFQ_GATED_PIPE(64, 64, 2, 2, 3, 0, W_ROW, 2, 0.485f, 0.393f, 5.538f),
+    BFQ_GATED_PIPE(64, 64, 2, 2, 3, 0, W_PACKED16, 2, 0.477f, 0.365f, 5.461f),
+    BFQ_GATED_PIPE(64, 64, 2, 2, 3, 3, W_ROW, 2, 0.379f, 0.379f, 5.470f),
+    BFQ_GATED_PIPE(64, 64, 2, 2, 3, 3, W_PACKED16, 2, 0.396f, 0.358f, 5.394f),
+    BFQ_GATED_PIPE(64, 128, 2, 4, 3, 0, W_ROW, 1, 0.774f, 0.053f, 6.016f),
+    BFQ_GATED_PIPE(64, 128, 2, 4, 3, 0, W_PACKED16, 1, 0.714f, 0.040f, 6.121f),
+    BFQ_GATED_PIPE(64, 128, 2, 4, 3, 3, W_ROW, 1, 0.744f, 0.000f, 5.962f),
+    BFQ_GATED_PIPE(64, 128, 2, 4, 3, 3, W_PACKED16, 1, 0.691f, 0.040f, 6.057f),
+    BFQ_GATED_PIPE(128, 64, 4, 2, 4, 0, W_ROW, 1, 0.690f, 0.323f, 5.539f),
+    BFQ_GATED_PIPE(128, 64, 4, 2, 4, 0, W_PACKED16, 1, 0.666f, 0.083f, 5.533f),
+    BFQ_GATED_PIPE(128, 64, 4, 2, 4, 3, W_ROW, 1, 0.659f, 0.000f, 5.606f),
+    BFQ_GATED_PIPE(128, 64, 4, 2, 4, 3, W_PACKED16, 1, 0.609f, 0.184f, 5.534f),
+    BFQ_GATED_PIPE(128, 128, 2, 4, 3, 0, W_ROW, 1, 1.179f, 0.548f, 5.883f),
+    BFQ_GATED_PIPE(128, 128, 2, 4, 3, 0, W_PACKED16, 1, 1.136f, 0.611f, 5.883f),
+    BFQ_GATED_PIPE(128, 128, 2, 4, 3, 3, W_ROW, 1, 1.032f, 0.155f, 5.811f),
+    BFQ_GATED_PIPE(128, 128, 2, 4, 3, 3, W_PACKED16, 1, 1.023f, 0.000f, 5.928f),
+    BFQ_GATED_STD(256, 256, 4, 2, 0, W_PACKED16, 1, 1.894f, 0.509f, 4.267f),
+    BFQ_GATED_STD(256, 256, 4, 2, 1, W_ROW, 1, 1.951f, 0.000f, 4.198f),
+    BFQ_GATED_STD(256, 256, 4, 2, 3, W_ROW, 1, 1.862f, 0.531f, 3.938f),
+    BFQ_GATED_STD(256, 256, 4, 2, 3, W_PACKED16, 1, 1.793f, 0.524f, 4.234f),
+    BFQ_GATED_RING(16, 1, 4, W_ROW, 10, 0.164f, 0.103f, 3.870f),
+    BFQ_GATED_RING(16, 1, 4, W_PACKED16, 10, 0.164f, 0.102f, 3.902f),
+    BFQ_GATED_RING(16, 2, 4, W_ROW, 5, 0.000f, 0.129f, 3.611f),
+    BFQ_GATED_RING(16, 2, 4, W_PACKED16, 5, 0.000f, 0.126f, 3.507f),
+    BFQ_GATED_RING(32, 2, 4, W_ROW, 5, 0.000f, 0.175f, 3.802f),
+    BFQ_GATED_RING(32, 2, 4, W_PACKED16, 5, 0.000f, 0.169f, 3.685f),
+    BFQ_GATED_SAB(16, 32, 1, 4, 4, 0, 4, 0.002f, 0.093f, 3.957f),
+    BFQ_GATED_SAB(32, 32, 8, 1, 4, 1, 2, 0.000f, 0.750f, 6.568f),
+    BFQ_GATED_SAB(64, 32, 8, 1, 4, 1, 1, 0.283f, 0.780f, 7.093f),
 };
 
 const GatedKernel* gated_kernels(int* count) {
