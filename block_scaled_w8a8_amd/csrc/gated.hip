@@ -574,8 +574,8 @@ __global__ __launch_bounds__(64 * KW) void gemm_gated_ring_kernel(GatedArgs p) {
         kbs[slot] = (int)(kb & 3);
         dma16_weights<ONCE>(rw, lds, at, c0, ws);
         dma16_weights<ONCE>(rw, lds, at + 1024, c1, ws);
-        dma16_weights<ONCE>(ru, lds, at + 2048, c0, ws);
-        dma16_weights<ONCE>(ru, lds, at + 3072, c1, ws);
+        dma16_weights<ONCE>(ru, lds, at + 2 * 1024, c0, ws);
+        dma16_weights<ONCE>(ru, lds, at + 3 * 1024, c1, ws);
 #pragma unroll
         for (int sm = 0; sm < SM; ++sm) {
             abuf[slot][sm][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, a_voff[sm], s, 0);

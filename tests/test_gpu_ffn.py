@@ -863,3 +863,24 @@ def test_large_gated_outputs_equal_small_ones(bfq):
         for a, b in zip(bfq.gated_backward(pre, dh, codes=codes, want_h=True),
                         bfq.gated_backward(pre[some].contiguous(), dh[some].contiguous(), codes=codes, want_h=True)):
             assert torch.equal(a[some], b)
+
+
+@pytest.mark.parametrize("wl", [0, 1])
+def test_gated_longest_k(bfq, wl):
+    """K = 2^23, the longest: offsets inside a tile's operands stay below 2^32."""
+    F, K = 128, 1 << 23
+    g = _gen(5)
+    qw = torch.randint(0, 120, (2 * F, K), dtype=torch.uint8, device=DEV, generator=g)
+    sw = torch.rand(2, K // 128, device=DEV, generator=g) * 1e-4
+    qw = bfq.pack_weights(qw) if wl else qw
+    for M in (3, 40, 130):
+        qa = torch.randint(0, 250, (M, K), dtype=torch.uint8, device=DEV, generator=g)
+        qa[(qa & 0x7F) == 0x7F] = 0
+        sa = torch.rand(M, K // 128, device=DEV, generator=g) * 1e-3
+        t = bfq.bfq_gated_select_tile(M, F, K, w_layout=wl)
+        print("longest K", wl, M, t.as_dict(), flush=True)
+        gu = _gu(bfq, qa, sa, qw, sw, t, wl, 0)
+        h, tol = _h_ref(gu, 0)
+        out, _, pre = _run_gated(bfq, qa, sa, qw, sw, torch.float32, 0, t, wl, 0, True)
+        _within(out, h, tol + U * h.abs() + TINY[torch.float32], f"{t.as_dict()}")
+        assert torch.equal(pre, gu.bfloat16())
