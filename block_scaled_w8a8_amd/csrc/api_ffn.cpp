@@ -50,8 +50,9 @@ bool serves(const GatedKernel& k, int sfmt) {
     return k.sfmt == S_FP32 || sfmt == S_UE8M0;
 }
 
-const GatedKernel* find_gated(const bfq_tile& t, int wlayout, int sfmt) {
+const GatedKernel* find_gated(bfq_tile t, int wlayout, int sfmt) {
     if (t.bk != 0 && t.bk != 128) return nullptr;
+    if (t.variant == 2) t.variant = 0;                     // the same kernels, the last tiles split
     int n = 0;
     const GatedKernel* k = gated_kernels(&n);
     for (int i = 0; i < n; ++i) {
@@ -83,12 +84,14 @@ bool ring_strip(const GatedKernel& k) { return k.tile.variant == 1 && k.tile.sch
 // parts. The grid runs in rounds of 256 CUs times the workgroups a CU holds; a round's K block
 // takes the longer of a workgroup's own latency and the CU's throughput over the workgroups it
 // holds (joined smoothly), the whole no less than the weight stream (ring strips take half of it
-// again for each further bm tokens); partials cost a second launch and their bytes twice. The
+// again for each further bm tokens); partials cost a second launch and their bytes twice (those of
+// a split last round, written by all CUs at the end of it, at a lower rate). The
 // constants, here and beside the kernels, are a fit to 840 measured (M, F, K, layout, format,
 // output) points of 9 to 100 configurations each, M 1 to 2048 on seven (F, K), weights read from
 // HBM as between the layers of a model; over them the pick is on average 1.1 % slower than the
 // fastest configuration.
-float gated_us(const GatedKernel& k, int64_t M, int64_t F, int64_t K, bool codes, int split) {
+// tail: the parts of the last round's tiles (variant 2), 1 otherwise.
+float gated_us(const GatedKernel& k, int64_t M, int64_t F, int64_t K, bool codes, int split, int tail) {
     const bfq_tile& t = k.tile;
     const int64_t groups = ceil_div(M, t.bm) * ceil_div(F, t.bn) * split;
     const int64_t slots = kNumCUs * k.occupancy, full = groups / slots, rest = groups % slots;
@@ -97,18 +100,36 @@ float gated_us(const GatedKernel& k, int64_t M, int64_t F, int64_t K, bool codes
     // strips whose waves fetch their own tokens: up to 0.6 of the throughput's time more for them
     const float thr = k.thr * (t.variant == 1 && t.sched == 0
                                    ? 1.f + 0.6f * (float)(M < t.bm ? M : t.bm) / (float)t.bm : 1.f);
-    auto round = [&](int64_t held) {
-        const float a = k.lat * blocks, b = (float)held * thr * blocks * kw;
+    auto round = [&](int64_t held, float n) {
+        const float a = k.lat * n, b = (float)held * thr * n * kw;
         return std::sqrt(std::sqrt(a * a * a * a + b * b * b * b)) + k.fix;
     };
-    float us = (float)full * round(k.occupancy) + (rest ? round(ceil_div(rest, kNumCUs)) : 0.f);
+    float us = (float)full * round(k.occupancy, blocks) +
+               (rest ? round(ceil_div(rest, kNumCUs), std::ceil(blocks / (float)tail)) : 0.f);
     const float rate = t.variant == 0 ? 4.63e6f : ring_strip(k) ? 5.62e6f : 5.93e6f;
     float stream = 2.f * (float)F * (float)K / rate;
     if (ring_strip(k)) stream *= 0.5f + 0.5f * (float)ceil_div(M, t.bm);
     const float x = us > stream ? stream / us : us / stream, x2 = x * x, x4 = x2 * x2;
     us = (us > stream ? us : stream) * std::sqrt(std::sqrt(std::sqrt(1.f + x4 * x4)));
+    if (tail > 1) us += 2.74f + (float)(rest * tail) * (float)(t.bm * t.bn) * 16.f / 4.2e6f;
     if (split > 1 || (codes && t.bn != 128)) us += 2.74f + (float)split * (float)M * (float)F * 16.f / 5.54e6f;
     return us;
+}
+
+// Variant 2: whole tiles in rounds of one workgroup a CU, the K range of the tiles that are left over
+// in as many parts as fill one more round, two K blocks or more each. parts = 1: nothing to split.
+struct TailPlan {
+    int64_t tiles, first;
+    int parts;
+};
+TailPlan tail_plan(const bfq_tile& t, int64_t M, int64_t F, int64_t K) {
+    const int64_t tiles = ceil_div(M, t.bm) * ceil_div(F, t.bn), first = tiles / kNumCUs * kNumCUs;
+    if (t.variant != 2 || first == 0 || first == tiles) return {tiles, tiles, 1};
+    const int64_t fill = kNumCUs / (tiles - first), parts = fill < K / 256 ? fill : K / 256;
+    return parts > 1 ? TailPlan{tiles, first, (int)(parts < 16 ? parts : 16)} : TailPlan{tiles, tiles, 1};
+}
+size_t tail_bytes(const TailPlan& p, const bfq_tile& t) {
+    return p.parts > 1 ? (size_t)(p.tiles - p.first) * (size_t)p.parts * (size_t)t.bm * 2 * (size_t)t.bn * sizeof(float) : 0;
 }
 
 // The rule: the kernel and K split with the least expected time. Strips read the weights again
@@ -138,12 +159,21 @@ bfq_tile select_gated(int64_t M, int64_t F, int64_t K, bool codes, int wlayout, 
             if (split > 1 && (split * 2 > KB || groups * (split - 1) >= kNumCUs * k[i].occupancy ||
                               (ring_strip(k[i]) && (!codes || split > 3))))
                 break;
-            const float us = gated_us(k[i], M, F, K, codes, split);
+            const float us = gated_us(k[i], M, F, K, codes, split, 1);
             if (us < best_us) {
                 best_us = us;
                 best = t;
                 best.split_k = split;
             }
+        }
+        bfq_tile u = t;
+        u.variant = 2;
+        if (t.variant != 0 || k[i].occupancy != 1 || (codes && t.bn != 128)) continue;
+        const int parts = tail_plan(u, M, F, K).parts;
+        const float us = parts > 1 ? gated_us(k[i], M, F, K, codes, 1, parts) : best_us;
+        if (us < best_us) {
+            best_us = us;
+            best = u;
         }
     }
     return best;
@@ -184,6 +214,7 @@ size_t bfq_gated_gemm_workspace_bytes(int64_t M, int64_t F, int64_t K, bfq_dtype
     if (!tile && (!wlayout_ok(w_layout) || F % 128 != 0 || K % 128 != 0)) return 0;
     const bool codes = out_dtype == BFQ_E4M3FN;
     const bfq_tile t = tile ? *tile : select_gated(M, F, K, codes, (int)w_layout, (int)scale_fmt);
+    if (t.variant == 2) return t.bm > 0 && t.bn > 0 ? tail_bytes(tail_plan(t, M, F, K), t) : 0;
     if (!needs_partials(t, codes) || t.split_k < 1) return 0;
     return (size_t)t.split_k * (size_t)M * 2 * (size_t)F * sizeof(float);
 }
@@ -275,15 +306,18 @@ bfq_status bfq_gated_gemm(const void* a_q, const float* a_scales, bfq_scale_layo
                                   "and scale format");
     if (t.split_k < 1 || t.split_k > 256 || t.split_k > KB)
         return fail(BFQ_ERR_TILE, "split_k must be in [1, min(256, K/128)]");
-    if (t.variant == 0 && (t.group_m < 1 || t.raster < 0 || t.raster > 1))
+    if (t.variant != 1 && (t.group_m < 1 || t.raster < 0 || t.raster > 1))
         return fail(BFQ_ERR_TILE, "group_m must be >= 1 and raster 0 or 1");
+    if (t.variant == 2 && (gk->tile.variant != 0 || t.split_k != 1 || (codes && t.bn != 128)))
+        return fail(BFQ_ERR_TILE, "variant 2 takes the tiles of variant 0 with split_k 1 and, for codes, bn 128");
+    const TailPlan tail = tail_plan(t, M, F, K);
     const bool parts = needs_partials(t, codes);
-    const size_t need = parts ? (size_t)t.split_k * (size_t)M * 2 * (size_t)F * sizeof(float) : 0;
+    const size_t need = parts ? (size_t)t.split_k * (size_t)M * 2 * (size_t)F * sizeof(float) : tail_bytes(tail, t);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(BFQ_ERR_WORKSPACE, "workspace of " + std::to_string(need) + " bytes required");
     // a grid dimension holds fewer than 2^32 threads
     const int64_t threads = 64 * t.waves_m * t.waves_n;
-    if (t.variant == 0 ? ceil_div(M, t.bm) * ceil_div(F, t.bn) * threads >= (int64_t(1) << 32)
+    if (t.variant != 1 ? (tail.tiles + kNumCUs) * threads >= (int64_t(1) << 32)
                        : ceil_div(M, t.bm) > 65535 || ceil_div(F, t.bn) * threads >= (int64_t(1) << 32))
         return fail(BFQ_ERR_SHAPE, "too many output tiles for one launch");
     if (M == 0) return BFQ_OK;
@@ -309,9 +343,15 @@ bfq_status bfq_gated_gemm(const void* a_q, const float* a_scales, bfq_scale_layo
     ga.out_scales = out_scales;
     ga.os_ue8m0 = scale_fmt == BFQ_SCALE_UE8M0;
     ga.os_eps = out_eps;
+    ga.tail_first = tail.first;
+    ga.tail_parts = tail.parts;
+    ga.tail_bm = t.bm;
+    ga.tail_bn = t.bn;
+    ga.tail = tail.parts > 1 ? static_cast<float*>(workspace) : nullptr;
     hipStream_t s = (hipStream_t)stream;
     hipError_t e = gk->launch(ga, s);
     if (e == hipSuccess && parts) e = launch_gated_reduce(ga, s);
+    if (e == hipSuccess && tail.parts > 1) e = launch_gated_tail(ga, tail.tiles, s);
     if (e != hipSuccess) return fail(BFQ_ERR_HIP, hipGetErrorString(e));
     return BFQ_OK;
 }

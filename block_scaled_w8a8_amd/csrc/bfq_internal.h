@@ -145,6 +145,11 @@ struct GatedArgs : GemmArgs {
     int64_t os_stride_m, os_stride_g;
     int os_ue8m0, os_packed;
     float os_eps;
+    // tiles from tail_first on have their K range in tail_parts (> 1) parts, whose fp32 sums go to
+    // tail[tile - tail_first][part][tail_bm][2 * tail_bn] (gate columns, then up)
+    int64_t tail_first;
+    int tail_parts, tail_bm, tail_bn;
+    float* tail;
 };
 typedef hipError_t (*GatedLaunchFn)(const GatedArgs& args, hipStream_t stream);
 // bfq_tile of a gated kernel: bn = output columns of a workgroup (2 * bn weight rows). For the
@@ -160,6 +165,8 @@ struct GatedKernel {
 const GatedKernel* gated_kernels(int* count);
 // out (and pre) from the partials of `split` K ranges: sums in range order, activation, product.
 hipError_t launch_gated_reduce(const GatedArgs& a, hipStream_t stream);
+// The same for the split tiles of a launch with tail_parts > 1.
+hipError_t launch_gated_tail(const GatedArgs& a, int64_t tiles, hipStream_t stream);
 // The activation's constants.
 void gated_activation(int act, float* c1, float* c3);
 

@@ -14,7 +14,7 @@
 // What bounds the forward kernels is what bounds the block GEMM's: the weight stream at decode
 // sizes, the operand bytes through a CU's L1 and the scale step at large M. Measured, F 18432 x
 // K 7168, packed weights, SILU, bf16 out: 1 token 42 us (6.3 TB/s of weights), 64 tokens 56 us,
-// 512 tokens 204 us, 4096 tokens 965 us with fp32 scales (2.24 PFLOP/s) and 890 us with powers of
+// 512 tokens 152 us, 4096 tokens 965 us with fp32 scales (2.24 PFLOP/s) and 890 us with powers of
 // two, 25 to 80 us more, by the box, where the pre-activations are kept (302 MB).
 // The two sums carry the e4m3 MFMA's own error, as the block GEMM's do: 3.5e-5 to 4.6e-5 of the
 // result (relative, Frobenius) on outlier-bearing tokens, whichever schedule or tile. Where codes
@@ -171,9 +171,10 @@ __device__ __forceinline__ void store_tile(const uint8_t* lds, void* dst, int64_
 
 // Finishes a tile of BM tokens x BNO output columns from (m0, n0): wave (wm, wn) holds rows wm * TM
 // and columns wn * TNO. The LDS is free (the callers end on a barrier).
+// slot >= 0: a part of a split tile, whose sums go to that slot of p.tail.
 template <int BM, int BNO, int WM, int WN, int SM, int SG>
 __device__ __forceinline__ void gated_finish_tile(const GatedArgs& p, uint8_t* lds, v4f (&acc)[SM][2 * SG],
-                                                  int64_t m0, int64_t n0) {
+                                                  int64_t m0, int64_t n0, int64_t slot) {
     constexpr int TM = BM / WM, TNO = BNO / WN;
     const int64_t M = p.M, F = p.N;
     const int lane = threadIdx.x & 63, frow = lane & 15, fgrp = lane >> 4;
@@ -181,6 +182,15 @@ __device__ __forceinline__ void gated_finish_tile(const GatedArgs& p, uint8_t* l
     const int wm = wave / WN, wn = wave % WN;
     const int64_t mw = m0 + wm * TM + frow, n = n0 + wn * TNO + 4 * fgrp;
     auto row = [&](int sm) { return mw + sm * 16 < M ? mw + sm * 16 : (int64_t)-1; };
+    if (slot >= 0) {
+        float* o = p.tail + (slot * BM + wm * TM + frow) * (2 * BNO) + wn * TNO + 4 * fgrp;
+#pragma unroll
+        for (int sm = 0; sm < SM; ++sm)
+#pragma unroll
+            for (int n2 = 0; n2 < 2 * SG; ++n2)
+                *reinterpret_cast<v4f*>(o + sm * 16 * 2 * BNO + n2 / SG * BNO + n2 % SG * 16) = acc[sm][n2];
+        return;
+    }
     if (p.partials) {
         gated_partials<SM, SG>(p, acc, n, row);
         return;
@@ -256,22 +266,37 @@ __device__ __forceinline__ void gated_finish_tile(const GatedArgs& p, uint8_t* l
     }
 }
 
+// The tile of this workgroup and its part of the K range: whole tiles (or all of them split alike,
+// blockIdx.z), then the parts of the last ones, part by part so that a tile's parts stay on one XCD.
+// A grid that fills its last round to an eighth or a quarter leaves the chip idle for most of it:
+// F 18432 x K 7168, packed, 256 x 128 tiles: 512 tokens (1.1 rounds) 223 -> 152 us, 1024 (2.25) 321 ->
+// 266, 2048 (4.5) 534 -> 517; with 128 tiles left over the parts' bytes cost what they gain.
+struct GatedWork {
+    int64_t tile, kb0, kb1, slot;
+};
+__device__ __forceinline__ GatedWork gated_work(const GatedArgs& p, int64_t tiles) {
+    const int64_t KB = p.K / 128, t = (int64_t)blockIdx.x - p.tail_first;
+    if (p.tail_parts <= 1 || t < 0)
+        return {(int64_t)blockIdx.x, (int64_t)blockIdx.z * KB / p.split, (int64_t)(blockIdx.z + 1) * KB / p.split, -1};
+    const int64_t tail = tiles - p.tail_first, part = t / tail, j = t % tail;
+    return {p.tail_first + j, part * KB / p.tail_parts, (part + 1) * KB / p.tail_parts, j * p.tail_parts + part};
+}
+
 // One workgroup per (tile of BM tokens x BN / 2 output columns, K split).
 template <int BM, int BN, int WM, int WN, int SCHED, int WL>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_gated_std_kernel(GatedArgs p) {
     using Shape = StdShape<BM, BN, WM, WN, SCHED>;
     constexpr int SM = Shape::SM, SG = Shape::SN / 2, BNO = BN / 2;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-    const int64_t M = p.M, F = p.N, KB = p.K / 128;
+    const int64_t M = p.M, F = p.N;
     const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (F + BNO - 1) / BNO;
+    const GatedWork w = gated_work(p, tiles_m * tiles_n);
     int64_t pid_m, pid_n;
-    tile_coords(blockIdx.x, tiles_m, tiles_n, p.group_m, p.raster, pid_m, pid_n);
+    tile_coords(w.tile, tiles_m, tiles_n, p.group_m, p.raster, pid_m, pid_n);
     const int64_t m0 = pid_m * BM, n0 = pid_n * BNO;
-    const int split = p.split, z = blockIdx.z;
     typename Shape::AccT acc[SM][2 * SG];
-    std_tile<BM, BN, WM, WN, Q_FP8, SCHED, 2, WL, 0, 1>(p, lds, m0, n0, (int64_t)z * KB / split,
-                                                        (int64_t)(z + 1) * KB / split, acc);
-    gated_finish_tile<BM, BNO, WM, WN, SM, SG>(p, lds, acc, m0, n0);
+    std_tile<BM, BN, WM, WN, Q_FP8, SCHED, 2, WL, 0, 1>(p, lds, m0, n0, w.kb0, w.kb1, acc);
+    gated_finish_tile<BM, BNO, WM, WN, SM, SG>(p, lds, acc, m0, n0, w.slot);
 }
 
 // Tiles for tens to hundreds of tokens on short products, where a K block's trip to memory costs
@@ -281,7 +306,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_gated_std_kernel(GatedArgs 
 // rows are swizzled as in the standard tiles, packed weights are fragment halves. Scales travel in
 // registers, counted with the loads. Against tiles of two stages, which wait out the trip every K
 // block: F 4096 x K 4096, 512 tokens, 28.7 us for 38.8; F 2304 x K 7168, 128 tokens, 20.2 for 26.7;
-// F 18432 x K 7168, 512 tokens, 204 for 223. At those sizes the fixed costs lead: some 3 us to start
+// F 18432 x K 7168, 333 tokens, 138 for 150. At those sizes the fixed costs lead: some 3 us to start
 // and drain, 3 us for a split's second launch.
 template <int BM, int BNO, int WM, int WN, int D, int SCHED, int WL>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_gated_pipe_kernel(GatedArgs p) {
@@ -296,10 +321,11 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_gated_pipe_kernel(GatedArgs
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int64_t M = p.M, F = p.N, K = p.K, KB = K / 128;
+    const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = F / BNO;
+    const GatedWork item = gated_work(p, tiles_m * tiles_n);
     int64_t pid_m, pid_n;
-    tile_coords(blockIdx.x, (M + BM - 1) / BM, F / BNO, p.group_m, p.raster, pid_m, pid_n);
-    const int64_t m0 = pid_m * BM, n0 = pid_n * BNO;
-    const int64_t kb0 = (int64_t)blockIdx.z * KB / p.split, L = (int64_t)(blockIdx.z + 1) * KB / p.split - kb0;
+    tile_coords(item.tile, tiles_m, tiles_n, p.group_m, p.raster, pid_m, pid_n);
+    const int64_t m0 = pid_m * BM, n0 = pid_n * BNO, kb0 = item.kb0, L = item.kb1 - kb0;
     constexpr uint32_t kNoLoad = 0x80000000u;           // past every resource here
 
     const uint8_t* w = static_cast<const uint8_t*>(p.w);
@@ -423,7 +449,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_gated_pipe_kernel(GatedArgs
     }
     wait_vmem_all();       // no copy into LDS may still be in flight
     __syncthreads();
-    gated_finish_tile<BM, BNO, WM, WN, SM, SG>(p, lds, acc, m0, n0);
+    gated_finish_tile<BM, BNO, WM, WN, SM, SG>(p, lds, acc, m0, n0, item.slot);
 }
 
 // ---------------------------------------------------------------- swap-AB strips ----
@@ -649,26 +675,15 @@ __global__ __launch_bounds__(64 * KW) void gemm_gated_ring_kernel(GatedArgs p) {
 
 // ---------------------------------------------------------------- reduce ----
 
-// Eight columns a thread: g and u summed over the K ranges in order, then as the epilogues above.
-// Groups of 128 columns are 16 lanes; the grid's rows past M (packed words only) write zeros.
-// Bytes bound it, its launch at decode sizes (2.7 us): 5.2 us for 333 x 2048 in two parts.
-__global__ __launch_bounds__(256) void gated_reduce_kernel(GatedArgs p) {
+// Eight columns of a token (chunk c of its row; `live`: inside the row, `real`: a token, not a padding
+// row of packed words): pre-activations, activation, product, output. Groups of 128 columns are 16
+// lanes of a wave.
+__device__ __forceinline__ void gated_finish8(const GatedArgs& p, int64_t m, int64_t c, bool live,
+                                              bool real, const float* g, const float* u) {
     const int lane = threadIdx.x & 63;
-    const int64_t m = blockIdx.x, F = p.N, c = (int64_t)blockIdx.y * 256 + threadIdx.x;
-    const bool live = c * 8 < F, real = m < p.M;
+    const int64_t F = p.N;
     float h[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (live && real) {
-        const float* s = p.partials + m * 2 * F + c * 8;
-        v4f g0{}, g1{}, u0{}, u1{};
-        for (int z = 0; z < p.split; ++z, s += p.M * 2 * F) {
-            const v4f a = *reinterpret_cast<const v4f*>(s), b = *reinterpret_cast<const v4f*>(s + 4);
-            const v4f d = *reinterpret_cast<const v4f*>(s + F), e = *reinterpret_cast<const v4f*>(s + F + 4);
-            if (z == 0) { g0 = a; g1 = b; u0 = d; u1 = e; }
-            else { g0 += a; g1 += b; u0 += d; u1 += e; }
-        }
-        float g[8], u[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) { g[i] = g0[i]; g[i + 4] = g1[i]; u[i] = u0[i]; u[i + 4] = u1[i]; }
         if (p.pre) {
             static_cast<uint4*>(p.pre)[(m * 2 * F) / 8 + c] = pack8(g);
             static_cast<uint4*>(p.pre)[(m * 2 * F + F) / 8 + c] = pack8(u);
@@ -692,6 +707,53 @@ __global__ __launch_bounds__(256) void gated_reduce_kernel(GatedArgs p) {
                     real ? s : 0.f);
 }
 
+// Sums over `parts` partials in order, `step` floats apart: gate columns at s, up columns at s + up.
+__device__ __forceinline__ void gated_sum8(const float* s, int parts, int64_t step, int64_t up, float* g, float* u) {
+    v4f g0{}, g1{}, u0{}, u1{};
+    for (int z = 0; z < parts; ++z, s += step) {
+        const v4f a = *reinterpret_cast<const v4f*>(s), b = *reinterpret_cast<const v4f*>(s + 4);
+        const v4f d = *reinterpret_cast<const v4f*>(s + up), e = *reinterpret_cast<const v4f*>(s + up + 4);
+        if (z == 0) { g0 = a; g1 = b; u0 = d; u1 = e; }
+        else { g0 += a; g1 += b; u0 += d; u1 += e; }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { g[i] = g0[i]; g[i + 4] = g1[i]; u[i] = u0[i]; u[i + 4] = u1[i]; }
+}
+
+// Eight columns a thread: g and u summed over the K ranges in order, then as the epilogues above.
+// The grid's rows past M (packed words only) write zeros. Bytes bound it, its launch at decode sizes
+// (2.7 us): 5.2 us for 333 x 2048 in two parts.
+__global__ __launch_bounds__(256) void gated_reduce_kernel(GatedArgs p) {
+    const int64_t m = blockIdx.x, F = p.N, c = (int64_t)blockIdx.y * 256 + threadIdx.x;
+    const bool live = c * 8 < F, real = m < p.M;
+    float g[8], u[8];
+    if (live && real) gated_sum8(p.partials + m * 2 * F + c * 8, p.split, p.M * 2 * F, F, g, u);
+    gated_finish8(p, m, c, live, real, g, u);
+}
+
+// The same for the tiles that were split (GatedArgs::tail): tail_bn / 8 threads a row of the tile.
+__global__ __launch_bounds__(256) void gated_tail_kernel(GatedArgs p) {
+    const int bm = p.tail_bm, bn = p.tail_bn, per_row = bn / 8;
+    const int64_t M = p.M, F = p.N, r = (int64_t)blockIdx.y * (256 / per_row) + threadIdx.x / per_row;
+    const int col = threadIdx.x % per_row * 8;
+    int64_t pid_m, pid_n;
+    tile_coords(p.tail_first + blockIdx.x, (M + bm - 1) / bm, F / bn, p.group_m, p.raster, pid_m, pid_n);
+    const int64_t m = pid_m * bm + r;
+    const bool live = r < bm && m < (p.otype == O_CODES && p.os_packed ? (M + 3) / 4 * 4 : M), real = live && m < M;
+    float g[8], u[8];
+    if (real)
+        gated_sum8(p.tail + ((int64_t)blockIdx.x * p.tail_parts * bm + r) * (2 * bn) + col, p.tail_parts,
+                   (int64_t)bm * 2 * bn, bn, g, u);
+    gated_finish8(p, m, (pid_n * bn + col) / 8, live, real, g, u);
+}
+
+hipError_t launch_gated_tail(const GatedArgs& a, int64_t tiles, hipStream_t stream) {
+    const int rows = 256 / (a.tail_bn / 8);
+    hipLaunchKernelGGL(gated_tail_kernel, dim3((unsigned)(tiles - a.tail_first), (unsigned)((a.tail_bm + rows - 1) / rows)),
+                       dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_gated_reduce(const GatedArgs& a, hipStream_t stream) {
     const int64_t rows = a.otype == O_CODES && a.os_packed ? (a.M + 3) / 4 * 4 : a.M;
     hipLaunchKernelGGL(gated_reduce_kernel, dim3((unsigned)rows, (unsigned)((a.N / 8 + 255) / 256)),
@@ -707,6 +769,10 @@ void gated_activation(int act, float* c1, float* c3) {
 
 // ---------------------------------------------------------------- registry ----
 
+static int64_t gated_grid(const GatedArgs& a, int64_t tiles) {
+    return a.tail_parts > 1 ? a.tail_first + (tiles - a.tail_first) * a.tail_parts : tiles;
+}
+
 template <int BM, int BN, int WM, int WN, int SCHED, int WL>
 hipError_t launch_gated_std(const GatedArgs& a, hipStream_t stream) {
     constexpr int LDS_BYTES = StdShape<BM, BN, WM, WN, SCHED>::lds_bytes(2);
@@ -716,7 +782,7 @@ hipError_t launch_gated_std(const GatedArgs& a, hipStream_t stream) {
         opted, reinterpret_cast<const void*>(&gemm_gated_std_kernel<BM, BN, WM, WN, SCHED, WL>), LDS_BYTES);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((gemm_gated_std_kernel<BM, BN, WM, WN, SCHED, WL>),
-                       dim3((unsigned)tiles, 1, (unsigned)a.split), dim3(64 * WM * WN), LDS_BYTES,
+                       dim3((unsigned)gated_grid(a, tiles), 1, (unsigned)a.split), dim3(64 * WM * WN), LDS_BYTES,
                        stream, a);
     return hipGetLastError();
 }
@@ -731,7 +797,7 @@ hipError_t launch_gated_pipe(const GatedArgs& a, hipStream_t stream) {
         opted, reinterpret_cast<const void*>(&gemm_gated_pipe_kernel<BM, BNO, WM, WN, D, SCHED, WL>), LDS_BYTES);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((gemm_gated_pipe_kernel<BM, BNO, WM, WN, D, SCHED, WL>),
-                       dim3((unsigned)tiles, 1, (unsigned)a.split), dim3(64 * WM * WN), LDS_BYTES,
+                       dim3((unsigned)gated_grid(a, tiles), 1, (unsigned)a.split), dim3(64 * WM * WN), LDS_BYTES,
                        stream, a);
     return hipGetLastError();
 }

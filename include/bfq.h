@@ -382,12 +382,13 @@ bfq_status bfq_gated_gemm(const void* a_q, const float* a_scales, bfq_scale_layo
 /* The tile that bfq_gated_gemm takes: a rule on M, F, K, the layout, the scale format and whether
  * codes are wanted (bn counts output columns: 2 * bn weight rows). Variant 1 with sched 2 (gated
  * tiles only): the waves take every waves_m-th K block and copy the weights through LDS, stages K
- * blocks ahead. Batch-invariant mode applies as in bfq_select_tile. */
+ * blocks ahead. Variant 2: the tiles of variant 0 in rounds of one workgroup per compute unit, the K
+ * range of those left over in as many parts as fill a last round (split_k 1; for codes bn 128). Batch-invariant mode applies as in bfq_select_tile. */
 bfq_status bfq_gated_select_tile(int64_t M, int64_t F, int64_t K, bfq_dtype out_dtype,
                                  bfq_weight_layout w_layout, bfq_scale_format scale_fmt,
                                  bfq_tile* tile_out);
 /* split_k * M * 2F * 4 bytes when the tile's split_k > 1, or when codes are wanted and the tile's
- * bn is not 128; else 0. tile NULL -> the selected one. SIZE_MAX for shapes bfq_gated_gemm
+ * bn is not 128; variant 2: at most 256 partial tiles of bm * 2 bn * 4 bytes; else 0. tile NULL -> the selected one. SIZE_MAX for shapes bfq_gated_gemm
  * rejects as too large. */
 size_t     bfq_gated_gemm_workspace_bytes(int64_t M, int64_t F, int64_t K, bfq_dtype out_dtype,
                                           bfq_weight_layout w_layout, bfq_scale_format scale_fmt,

@@ -84,6 +84,29 @@ def test_gated_queries(bfq):
     assert bfq.bfq_gated_gemm_workspace_bytes(1 << 30, 256, 256) == ctypes.c_size_t(-1).value
 
 
+def test_gated_split_last_round_refusals(bfq):
+    tiles = [bfq.bfq_gated_get_tile_candidate(i) for i in range(bfq.bfq_gated_num_tile_candidates())]
+    codes = dict(out_dtype=bfq.BFQ_E4M3FN, out_scales=P, out_ld=2)
+    for t in tiles:
+        v2 = bfq.bfq_tile.from_dict({**t.as_dict(), "variant": 2})
+        # a last round needs whole rounds before it: no workspace, and the next check is the alignment
+        assert bfq.bfq_gated_gemm_workspace_bytes(4, 256, 256, tile=v2) == 0
+        if t.variant == 1:
+            assert _gated(bfq, tile=ctypes.byref(v2)) == bfq.BFQ_ERR_TILE       # strips have no such form
+            continue
+        for kw in (dict(split_k=2), dict(group_m=0), dict(raster=2)):
+            bad = bfq.bfq_tile.from_dict({**v2.as_dict(), **kw})
+            assert _gated(bfq, tile=ctypes.byref(bad)) == bfq.BFQ_ERR_TILE, kw
+        if t.bn != 128:                              # codes need whole groups in a tile
+            assert _gated(bfq, tile=ctypes.byref(v2), **codes) == bfq.BFQ_ERR_TILE
+        M, F = 256 * t.bm + 1, t.bn if t.bn == 128 else 128
+        n = bfq.bfq_gated_gemm_workspace_bytes(M, F, 7168, tile=v2)
+        rest = -(-M // t.bm) * (F // t.bn) % 256
+        assert n == rest * min(256 // rest, 16) * t.bm * 2 * t.bn * 4 > 0
+        assert _gated(bfq, M=M, F=F, K=7168, a_ld=56, tile=ctypes.byref(v2)) == bfq.BFQ_ERR_WORKSPACE
+        assert _gated(bfq, M=M, F=F, K=7168, a_ld=56, tile=ctypes.byref(v2), ws=P, wsb=n - 1) == bfq.BFQ_ERR_WORKSPACE
+
+
 @pytest.mark.parametrize("wl", [0, 1])
 @pytest.mark.parametrize("sfmt", [0, 1])
 def test_gated_rule_names_compiled_tiles(bfq, wl, sfmt):
@@ -98,19 +121,28 @@ def test_gated_rule_names_compiled_tiles(bfq, wl, sfmt):
                         t = bfq.bfq_gated_select_tile(M, F, K, w_layout=wl, scale_fmt=sfmt)
                         assert 1 <= t.split_k <= max(1, K // 128 // 2) and t.bm > 0
                         assert not inv or t.split_k == 1
+                        def kw(dt):
+                            return dict(M=M, F=F, K=K, w_layout=wl, sfmt=sfmt, a_ld=K // 128, out_dtype=dt,
+                                        out_scales=P, out_ld=F // 128)
+
                         for dt, codes in ((bfq.BFQ_BF16, False), (bfq.BFQ_E4M3FN, True)):
                             n = bfq.bfq_gated_gemm_workspace_bytes(M, F, K, dt, wl, sfmt)
                             tc = bfq.bfq_gated_select_tile(M, F, K, dt, wl, sfmt)
                             want = tc.split_k * M * 2 * F * 4 if tc.split_k > 1 or (codes and tc.bn != 128) else 0
+                            if tc.variant == 2:      # the last round's tiles in parts that fill it
+                                rest = -(-M // tc.bm) * (F // tc.bn) % 256
+                                parts = min(256 // rest, K // 256, 16)
+                                assert want == 0 and parts > 1 and not inv
+                                want = rest * parts * tc.bm * 2 * tc.bn * 4
+                                bad = tc.from_dict({**tc.as_dict(), "split_k": 2})
+                                assert _gated(bfq, **kw(dt), tile=bad) == bfq.BFQ_ERR_TILE
                             assert n == want
                             # host pointers: refused for its missing workspace, or (none needed) for
                             # an alignment that is checked after the tile is known to be fine
-                            kw = dict(M=M, F=F, K=K, w_layout=wl, sfmt=sfmt, a_ld=K // 128, out_dtype=dt,
-                                      out_scales=P, out_ld=F // 128)
                             if n:
-                                assert _gated(bfq, **kw) == bfq.BFQ_ERR_WORKSPACE
+                                assert _gated(bfq, **kw(dt)) == bfq.BFQ_ERR_WORKSPACE
                                 if sfmt:
-                                    assert _gated(bfq, **{**kw, "a_layout": 2, "a_ld": M}) == bfq.BFQ_ERR_WORKSPACE
+                                    assert _gated(bfq, **{**kw(dt), "a_layout": 2, "a_ld": M}) == bfq.BFQ_ERR_WORKSPACE
         finally:
             bfq.bfq_set_batch_invariant(False)
 

@@ -884,3 +884,46 @@ def test_gated_longest_k(bfq, wl):
         out, _, pre = _run_gated(bfq, qa, sa, qw, sw, torch.float32, 0, t, wl, 0, True)
         _within(out, h, tol + U * h.abs() + TINY[torch.float32], f"{t.as_dict()}")
         assert torch.equal(pre, gu.bfloat16())
+
+
+@pytest.mark.parametrize("wl,sfmt", [(0, 0), (1, 0), (1, 1)])
+def test_gated_split_last_round(bfq, wl, sfmt):
+    """Variant 2 (tiles in plain row order): the first 256 tiles have the sums of whole tiles, the
+    others those of a split K range; a batch with too few tiles for a round, and one with none left
+    over, are plain launches."""
+    K = 1152
+    seen = set()
+    for t0 in _gated_tiles(bfq, wl, sfmt):
+        if t0.variant != 0 or (t0.bm, t0.bn) in seen:
+            continue
+        seen.add((t0.bm, t0.bn))
+        F = 128 * 34
+        M = t0.bm * (-(-300 // (F // t0.bn))) - 3           # a little over a round of tiles
+        tiles = -(-M // t0.bm) * (F // t0.bn)
+        parts = min(256 // (tiles - 256), K // 256)
+        assert 256 < tiles < 384 and parts > 1
+        t = bfq.bfq_tile.from_dict({**t0.as_dict(), "variant": 2, "raster": 1, "group_m": 1})
+        print("last round", wl, sfmt, M, t.as_dict(), tiles, parts, flush=True)
+        n = bfq.bfq_gated_gemm_workspace_bytes(M, F, K, bfq.BFQ_BF16, wl, sfmt, t)
+        assert n == (tiles - 256) * parts * t.bm * 2 * t.bn * 4
+        qa, sa, qw, sw, _ = _pair(bfq, M, F, K, 300 + t.bm, sfmt, wl)
+        whole, split = [_gu(bfq, qa, sa, qw, sw, bfq.bfq_tile.from_dict({**t0.as_dict(), "split_k": s}), wl, sfmt)
+                        for s in (1, parts)]
+        late = (torch.arange(tiles, device=DEV) >= 256).view(-1, F // t.bn)             # [tile row, tile column]
+        pick = late.repeat_interleave(t.bm, 0)[:M].repeat_interleave(t.bn, 1).repeat(1, 2)
+        gu = torch.where(pick, split, whole)
+        h, tol = _h_ref(gu, 0)
+        for odt in (torch.float32, torch.bfloat16) + ((torch.uint8,) if t.bn == 128 else ()):
+            out, s, pre = _run_gated(bfq, qa, sa, qw, sw, odt, 0, t, wl, sfmt, True)
+            assert torch.equal(pre, gu.bfloat16()), t.as_dict()
+            if odt == torch.uint8:
+                _check_codes(out, s[:, :F // 128], h, tol, sfmt == 1, f"{t.as_dict()}")
+            else:
+                _within(out, h, tol + H[odt] * h.abs() + TINY[odt], f"{odt} {t.as_dict()}")
+        for m in (5, t.bm * 8 if t.bn == 128 else t.bm * 4):     # no whole round, one whole round
+            f = F if m == 5 else 32 * 128
+            qa2, sa2, qw2, sw2, _ = _pair(bfq, m, f, 384, 7, sfmt, wl)
+            assert bfq.bfq_gated_gemm_workspace_bytes(m, f, 384, bfq.BFQ_BF16, wl, sfmt, t) == 0
+            a = bfq.gated_gemm(qa2, sa2, qw2, sw2, tile=t, w_layout=wl, scale_fmt=sfmt)
+            assert torch.equal(a, bfq.gated_gemm(qa2, sa2, qw2, sw2, tile=t0, w_layout=wl, scale_fmt=sfmt))
+    assert len(seen) == 6
