@@ -162,7 +162,7 @@ __global__ __launch_bounds__(kNormThreads<P>) void norm_residual_kernel(NormArgs
         unpack(ones_unless(wpost[u], p.w_post != nullptr), w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            r[u][i] = __builtin_fmaf(y[i] * c * w[i], g[i], r[u][i]);
+            r[u][i] = __builtin_fmaf(y[i] * w[i] * g[i], c, r[u][i]);   // three bf16: exact in fp32
             s[0] = __builtin_fmaf(r[u][i], r[u][i], s[0]);
         }
         Chunk<RF32, S>::store(r_out, voff[u], r[u]);
