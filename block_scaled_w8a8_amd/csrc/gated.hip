@@ -526,9 +526,11 @@ __device__ __forceinline__ void dma16_weights(__amdgpu_buffer_rsrc_t r, uint8_t*
 
 // Strips for a few tokens, the weights through LDS; the weight stream bounds them. A workgroup
 // takes 16 output columns (16 gate rows, 16 up rows) and its waves every KW-th K block, so that
-// together they walk neighbouring bytes of the weights. Each wave copies 1 KB a load (row-major:
+// together they walk neighbouring bytes of the weights. Where that leaves CUs without work it takes
+// eight (BNO 8: one fragment of eight gate and eight up rows, the factors of an output in lanes l and
+// l + 32): F 2048 x K 7168 row-major, 1 token 7.9 us against 10.0, 16 tokens 9.3 against 10.6. Each wave copies 1 KB a load (row-major:
 // whole 128-byte lines of 8 rows; packed: a fragment half) into a ring of its own, D K blocks of
-// 4 KB, and reads its fragments back: no barrier in the K loop, the wave waits until the loads of
+// 4 KB (2 KB), and reads its fragments back: no barrier in the K loop, the wave waits until the loads of
 // its oldest block have landed, and what is in flight takes no registers, so a CU holds up to 10
 // waves of 16 KB in flight each. Row-major chunk c of row r sits in slot c ^ swz(r), as in the
 // standard tiles.
@@ -539,27 +541,29 @@ __device__ __forceinline__ void dma16_weights(__amdgpu_buffer_rsrc_t r, uint8_t*
 // loads straight from the rows take half a line of each of 16 rows a request: 61 and 62 us. Packed:
 // ahead of the strips above where the products are short (F 4096 x K 4096, 16 tokens: 8.8 us against
 // 11.5) and behind on long streams (F 18432 x K 7168, 1 token: 49 against 43).
-template <int MT, int KW, int D, int WL, int CH, int ONCE>
+template <int MT, int BNO, int KW, int D, int WL, int CH, int ONCE>
 __global__ __launch_bounds__(64 * KW) void gemm_gated_ring_kernel(GatedArgs p) {
-    constexpr int SM = MT / 16, BLOCK = 4096;
+    constexpr int SM = MT / 16, NF = BNO / 8, BLOCK = NF * 2048;   // NF fragments of 16 weight rows
     constexpr bool PK = CH == 2;
-    constexpr int kOps = 6 + 3 * SM;                    // vector loads of one K block
+    constexpr int kOps = 2 * NF + 2 + 3 * SM;           // vector loads of one K block
     static_assert((D - 1) * kOps <= 63, "the wait counts loads in six bits");
-    static_assert((KW - 1) * SM * 2048 <= KW * D * BLOCK, "the slices' sums fit the rings");
+    static_assert((KW - 1) * SM * NF * 1024 <= KW * D * BLOCK, "the slices' sums fit the rings");
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const int lane = threadIdx.x & 63;
     const int wk = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int frow = lane & 15, fgrp = lane >> 4;
     const int64_t M = p.M, F = p.N, K = p.K, KB = K / 128;
-    const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * MT;
+    const int64_t n0 = (int64_t)blockIdx.x * BNO, m0 = (int64_t)blockIdx.y * MT;
     const int split = p.split, z = blockIdx.z;
     const int64_t ks0 = (int64_t)z * KB / split, ks1 = (int64_t)(z + 1) * KB / split;
     const int64_t L = (ks1 - ks0 - wk + KW - 1) / KW;   // K blocks ks0 + wk, + KW, ..
     constexpr uint32_t kNoLoad = 0x80000000u;           // past every resource here
 
     const uint8_t* w = static_cast<const uint8_t*>(p.w);
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(w + n0 * K, (uint32_t)(16 * K));
-    const __amdgpu_buffer_rsrc_t ru = make_rsrc(w + (F + n0) * K, (uint32_t)(16 * K));
+    // rows n0 / 16 * 16 on: packed weights come as groups of 16 rows
+    const int64_t g0 = n0 / 16 * 16, sub = n0 - g0;
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(w + g0 * K, (uint32_t)(16 * K));
+    const __amdgpu_buffer_rsrc_t ru = make_rsrc(w + (F + g0) * K, (uint32_t)(16 * K));
     const int64_t rows_a = M - m0 < MT ? M - m0 : MT;
     const int64_t ssm = p.sa_stride_m, ssk = p.sa_stride_k, sa_krows = PK ? (KB - 1) / 4 : KB - 1;
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(static_cast<const uint8_t*>(p.a) + m0 * K, (uint32_t)(rows_a * K));
@@ -573,16 +577,21 @@ __global__ __launch_bounds__(64 * KW) void gemm_gated_ring_kernel(GatedArgs p) {
     }
     const __amdgpu_buffer_rsrc_t rsg = make_rsrc(p.sw + (n0 / 128) * KB, (uint32_t)(KB * 4));
     const __amdgpu_buffer_rsrc_t rsu = make_rsrc(p.sw + (F / 128 + n0 / 128) * KB, (uint32_t)(KB * 4));
-    // copy of rows: lane l takes row l / 8 (+ 8), slot l % 8; swz of the second eight differs by 1
+    // copy of rows: lane l takes row l / 8 (BNO 16: + 8), slot l % 8; swz of the second eight differs
+    // by 1. Eight columns: the fragment's first eight rows are gate rows, the second eight up rows.
     constexpr bool rows = WL == W_ROW;
-    const uint32_t c0 = rows ? (uint32_t)((lane >> 3) * K + (((lane & 7) ^ (lane >> 3)) << 4))
-                             : (uint32_t)(lane * 16);
-    const uint32_t c1 = rows ? (uint32_t)(((lane >> 3) + 8) * K + (((lane & 7) ^ (lane >> 3) ^ 1) << 4))
-                             : (uint32_t)(1024 + lane * 16);
+    const uint32_t row8 = (uint32_t)(((lane >> 3) + (BNO == 8 ? sub : 0)) * K), slot8 = (lane & 7) ^ (lane >> 3);
+    const uint32_t c0 = rows ? row8 + (slot8 << 4)
+                        : BNO == 8 ? (uint32_t)((lane >> 5) * 1024 + ((lane >> 3) & 3) * 256 + (lane & 7) * 16 + sub * 16)
+                                   : (uint32_t)(lane * 16);
+    const uint32_t c1 = rows ? row8 + (uint32_t)(BNO == 8 ? 0 : 8 * K) + ((slot8 ^ 1) << 4)
+                             : BNO == 8 ? c0 : (uint32_t)(1024 + lane * 16);
     const uint32_t ring = (uint32_t)(wk * D * BLOCK);
-    const uint32_t f0 = rows ? (uint32_t)(frow * 128 + ((fgrp ^ swz(frow)) << 4)) : (uint32_t)(lane * 16);
+    const uint32_t half8 = (uint32_t)((frow >> 3) * 1024 + fgrp * 128 + (frow & 7) * 16);
+    const uint32_t f0 = rows ? (uint32_t)(frow * 128 + ((fgrp ^ swz(frow)) << 4))
+                             : BNO == 8 ? half8 : (uint32_t)(lane * 16);
     const uint32_t f1 = rows ? (uint32_t)(frow * 128 + (((fgrp + 4) ^ swz(frow)) << 4))
-                             : (uint32_t)(1024 + lane * 16);
+                             : BNO == 8 ? half8 + 512 : (uint32_t)(1024 + lane * 16);
 
     v4i abuf[D][SM][2];
     float sab[D][SM], swb[D], swu[D];
@@ -599,9 +608,13 @@ __global__ __launch_bounds__(64 * KW) void gemm_gated_ring_kernel(GatedArgs p) {
         swu[slot] = buf_f32(rsu, 0, sws);
         kbs[slot] = (int)(kb & 3);
         dma16_weights<ONCE>(rw, lds, at, c0, ws);
-        dma16_weights<ONCE>(rw, lds, at + 1024, c1, ws);
-        dma16_weights<ONCE>(ru, lds, at + 2 * 1024, c0, ws);
-        dma16_weights<ONCE>(ru, lds, at + 3 * 1024, c1, ws);
+        if constexpr (BNO == 16) {
+            dma16_weights<ONCE>(rw, lds, at + 1024, c1, ws);
+            dma16_weights<ONCE>(ru, lds, at + 2 * 1024, c0, ws);
+            dma16_weights<ONCE>(ru, lds, at + 3 * 1024, c1, ws);
+        } else {
+            dma16_weights<ONCE>(ru, lds, at + 1024, c1, ws);
+        }
 #pragma unroll
         for (int sm = 0; sm < SM; ++sm) {
             abuf[slot][sm][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, a_voff[sm], s, 0);
@@ -609,14 +622,16 @@ __global__ __launch_bounds__(64 * KW) void gemm_gated_ring_kernel(GatedArgs p) {
             sab[slot][sm] = buf_f32(rsa, sa_voff[sm], ss);
         }
     };
-    v4f acc[SM][2];
+    v4f acc[SM][NF];
 #pragma unroll
-    for (int sm = 0; sm < SM; ++sm) acc[sm][0] = acc[sm][1] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int sm = 0; sm < SM; ++sm)
+#pragma unroll
+        for (int h = 0; h < NF; ++h) acc[sm][h] = v4f{0.f, 0.f, 0.f, 0.f};
     auto consume = [&](int slot) {
         const uint8_t* at = lds + ring + slot * BLOCK;
-        v8i wf[2];
+        v8i wf[NF];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < NF; ++h) {
             const v4i lo = *reinterpret_cast<const v4i*>(at + h * 2048 + f0);
             const v4i hi = *reinterpret_cast<const v4i*>(at + h * 2048 + f1);
             wf[h] = v8i{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -627,9 +642,10 @@ __global__ __launch_bounds__(64 * KW) void gemm_gated_ring_kernel(GatedArgs p) {
             const v4i a0 = abuf[slot][sm][0], a1 = abuf[slot][sm][1];
             const v8i af = v8i{a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < NF; ++h) {
                 const v4f q = mfma_fp8_16x16x128(wf[h], af);
-                const float c = sav * (h ? swu[slot] : swb[slot]);
+                const bool up = BNO == 16 ? h != 0 : fgrp >= 2;
+                const float c = sav * (up ? swu[slot] : swb[slot]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[sm][h][j] = __builtin_fmaf(q[j], c, acc[sm][h][j]);
             }
@@ -659,7 +675,7 @@ __global__ __launch_bounds__(64 * KW) void gemm_gated_ring_kernel(GatedArgs p) {
 #pragma unroll
         for (int sm = 0; sm < SM; ++sm)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) red[(((wk - 1) * SM + sm) * 2 + h) * 64 + lane] = acc[sm][h];
+            for (int h = 0; h < NF; ++h) red[(((wk - 1) * SM + sm) * NF + h) * 64 + lane] = acc[sm][h];
     }
     __syncthreads();
     if (wk == 0) {
@@ -668,9 +684,33 @@ __global__ __launch_bounds__(64 * KW) void gemm_gated_ring_kernel(GatedArgs p) {
 #pragma unroll
             for (int sm = 0; sm < SM; ++sm)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) acc[sm][h] += red[((w2 * SM + sm) * 2 + h) * 64 + lane];
+                for (int h = 0; h < NF; ++h) acc[sm][h] += red[((w2 * SM + sm) * NF + h) * 64 + lane];
     }
-    gated_finish<MT, 16, 1, SM, 1>(p, acc, m0, n0, rows_a, 0, wk, lane);
+    if constexpr (BNO == 16) {
+        gated_finish<MT, 16, 1, SM, 1>(p, acc, m0, n0, rows_a, 0, wk, lane);
+    } else {
+        // lanes 0-31 hold columns n0 + 4 * fgrp .. +3 of the gate, lanes 32-63 the same of up
+        if (wk > 0) return;
+        const int64_t n = n0 + 4 * (fgrp & 1);
+#pragma unroll
+        for (int sm = 0; sm < SM; ++sm) {
+            const int64_t m = m0 + sm * 16 + frow;
+            v4f g = acc[sm][0], u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = __shfl_xor(g[j], 32, 64);
+            if (m >= M) continue;
+            const int64_t own = fgrp >= 2 ? F : 0;
+            if (p.partials) {
+                *reinterpret_cast<v4f*>(p.partials + ((int64_t)z * M + m) * 2 * F + own + n) = g;
+                continue;
+            }
+            if (p.pre) store4_any(O_BF16, p.pre, m * 2 * F + own + n, g);
+            if (fgrp >= 2) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) g[j] = act_f32(g[j], p.c1, p.c3) * u[j];
+            store4_any(p.otype, p.out, m * F + n, g);
+        }
+    }
 }
 
 // ---------------------------------------------------------------- reduce ----
@@ -816,22 +856,22 @@ hipError_t launch_gated_swapab(const GatedArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int MT, int KW, int D, int WL, int CH, int ONCE>
+template <int MT, int BNO, int KW, int D, int WL, int CH, int ONCE>
 hipError_t launch_gated_ring_once(const GatedArgs& a, hipStream_t stream) {
-    constexpr int LDS_BYTES = KW * D * 4096;
+    constexpr int LDS_BYTES = KW * D * BNO * 256;
     static std::atomic<uint64_t> opted{0};
     const hipError_t e =
-        opt_in_lds(opted, reinterpret_cast<const void*>(&gemm_gated_ring_kernel<MT, KW, D, WL, CH, ONCE>), LDS_BYTES);
+        opt_in_lds(opted, reinterpret_cast<const void*>(&gemm_gated_ring_kernel<MT, BNO, KW, D, WL, CH, ONCE>), LDS_BYTES);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)(a.N / 16), (unsigned)((a.M + MT - 1) / MT), (unsigned)a.split);
-    hipLaunchKernelGGL((gemm_gated_ring_kernel<MT, KW, D, WL, CH, ONCE>), grid, dim3(64 * KW), LDS_BYTES, stream, a);
+    const dim3 grid((unsigned)(a.N / BNO), (unsigned)((a.M + MT - 1) / MT), (unsigned)a.split);
+    hipLaunchKernelGGL((gemm_gated_ring_kernel<MT, BNO, KW, D, WL, CH, ONCE>), grid, dim3(64 * KW), LDS_BYTES, stream, a);
     return hipGetLastError();
 }
 
-template <int MT, int KW, int D, int WL, int CH>
+template <int MT, int BNO, int KW, int D, int WL, int CH>
 hipError_t launch_gated_ring(const GatedArgs& a, hipStream_t stream) {
-    return a.M <= MT ? launch_gated_ring_once<MT, KW, D, WL, CH, 1>(a, stream)
-                     : launch_gated_ring_once<MT, KW, D, WL, CH, 0>(a, stream);
+    return a.M <= MT ? launch_gated_ring_once<MT, BNO, KW, D, WL, CH, 1>(a, stream)
+                     : launch_gated_ring_once<MT, BNO, KW, D, WL, CH, 0>(a, stream);
 }
 
 // The last four arguments are what the tile rule knows of a kernel: the workgroups a CU holds, and
@@ -847,12 +887,12 @@ hipError_t launch_gated_ring(const GatedArgs& a, hipStream_t stream) {
     BFQ_GATED_SAB1(MT, NWR, NW, KW, D, 0, L, OCC, LAT, THR, FIX),                           \
         BFQ_GATED_SAB1(MT, NWR, NW, KW, D, 2, L, OCC, LAT, THR, FIX)
 
-#define BFQ_GATED_RING1(MT, KW, D, WL, CH, OCC, LAT, THR, FIX)                                  \
-    GatedKernel{bfq_tile{1, MT, 16, 128, 1, KW, 1, D, 1, 2, 0, 0}, WL,                          \
-                (CH) == 2 ? S_PACKED : S_FP32, &launch_gated_ring<MT, KW, D, WL, CH>, OCC, LAT, THR, FIX}
-#define BFQ_GATED_RING(MT, KW, D, WL, OCC, LAT, THR, FIX)                                       \
-    BFQ_GATED_RING1(MT, KW, D, WL, 0, OCC, LAT, THR, FIX),                                      \
-        BFQ_GATED_RING1(MT, KW, D, WL, 2, OCC, LAT, THR, FIX)
+#define BFQ_GATED_RING1(MT, BNO, KW, D, WL, CH, OCC, LAT, THR, FIX)                             \
+    GatedKernel{bfq_tile{1, MT, BNO, 128, 1, KW, 1, D, 1, 2, 0, 0}, WL, (CH) == 2 ? S_PACKED : S_FP32, \
+                &launch_gated_ring<MT, BNO, KW, D, WL, CH>, OCC, LAT, THR, FIX}
+#define BFQ_GATED_RING(MT, BNO, KW, D, WL, OCC, LAT, THR, FIX)                                  \
+    BFQ_GATED_RING1(MT, BNO, KW, D, WL, 0, OCC, LAT, THR, FIX),                                 \
+        BFQ_GATED_RING1(MT, BNO, KW, D, WL, 2, OCC, LAT, THR, FIX)
 
 #define BFQ_GATED_PIPE(BM, BNO, WM, WN, D, SC, WL, OCC, LAT, THR, FIX)                          \
     GatedKernel{bfq_tile{0, BM, BNO, 128, 1, WM, WN, D, 8, SC, 0, 0}, WL,                       \
@@ -883,12 +923,14 @@ static const GatedKernel kGatedKernels[] = {
     BFQ_GATED_STD(256, 256, 4, 2, 1, W_ROW, 1, 1.951f, 0.000f, 4.198f),
     BFQ_GATED_STD(256, 256, 4, 2, 3, W_ROW, 1, 1.862f, 0.531f, 3.938f),
     BFQ_GATED_STD(256, 256, 4, 2, 3, W_PACKED16, 1, 1.793f, 0.524f, 4.234f),
-    BFQ_GATED_RING(16, 1, 4, W_ROW, 10, 0.164f, 0.103f, 3.870f),
-    BFQ_GATED_RING(16, 1, 4, W_PACKED16, 10, 0.164f, 0.102f, 3.902f),
-    BFQ_GATED_RING(16, 2, 4, W_ROW, 5, 0.000f, 0.129f, 3.611f),
-    BFQ_GATED_RING(16, 2, 4, W_PACKED16, 5, 0.000f, 0.126f, 3.507f),
-    BFQ_GATED_RING(32, 2, 4, W_ROW, 5, 0.000f, 0.175f, 3.802f),
-    BFQ_GATED_RING(32, 2, 4, W_PACKED16, 5, 0.000f, 0.169f, 3.685f),
+    BFQ_GATED_RING(16, 16, 1, 4, W_ROW, 10, 0.164f, 0.103f, 3.870f),
+    BFQ_GATED_RING(16, 16, 1, 4, W_PACKED16, 10, 0.164f, 0.102f, 3.902f),
+    BFQ_GATED_RING(16, 16, 2, 4, W_ROW, 5, 0.000f, 0.129f, 3.611f),
+    BFQ_GATED_RING(16, 16, 2, 4, W_PACKED16, 5, 0.000f, 0.126f, 3.507f),
+    BFQ_GATED_RING(32, 16, 2, 4, W_ROW, 5, 0.000f, 0.175f, 3.802f),
+    BFQ_GATED_RING(32, 16, 2, 4, W_PACKED16, 5, 0.000f, 0.169f, 3.685f),
+    BFQ_GATED_RING(16, 8, 4, 4, W_ROW, 5, 0.001f, 0.099f, 3.127f),
+    BFQ_GATED_RING(16, 8, 4, 4, W_PACKED16, 5, 0.001f, 0.096f, 3.168f),
     BFQ_GATED_SAB(16, 32, 1, 4, 4, 0, 4, 0.002f, 0.093f, 3.957f),
     BFQ_GATED_SAB(32, 32, 8, 1, 4, 1, 2, 0.000f, 0.750f, 6.568f),
     BFQ_GATED_SAB(64, 32, 8, 1, 4, 1, 1, 0.283f, 0.780f, 7.093f),

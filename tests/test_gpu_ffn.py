@@ -132,7 +132,8 @@ def _gu_interleaved(bfq, qa, sa, qw, sw, t, wl, sfmt):
     for z in range(t.split_k):
         part = None
         for v in range(t.waves_m):
-            blocks = torch.arange(z * KB // t.split_k + v, (z + 1) * KB // t.split_k, t.waves_m, device=DEV)
+            blocks = torch.tensor(range(z * KB // t.split_k + v, (z + 1) * KB // t.split_k, t.waves_m),
+                                  dtype=torch.long, device=DEV)
             if len(blocks):
                 cols = (blocks[:, None] * 128 + torch.arange(128, device=DEV)).flatten()
                 x = bfq.block_gemm(qa[:, cols].contiguous(), sa[:, blocks].contiguous(),
