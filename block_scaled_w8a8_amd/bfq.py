@@ -6,6 +6,8 @@ library is missing, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import warnings
 
@@ -185,13 +187,13 @@ def last_error() -> str:
     return lib.bfq_last_error().decode()
 
 
-def _check(status: int, where: str, warn_key=None) -> int:
+def _check(status: int, where: str, warn_key=None, depth=3) -> int:
     if status < 0:
         raise BfqError(status, where)
     if status > 0 and warn_key not in _warned:
         _warned.add(warn_key)
         warnings.warn(f"{where}: {status_string(status)} (no tuned tile for {warn_key}; "
-                      "using the default tile)", RuntimeWarning, stacklevel=3)
+                      "using the default tile)", RuntimeWarning, stacklevel=depth)   # the caller's line
     return status
 
 
@@ -879,7 +881,53 @@ def bfq_norm_residual_backward(res_out, d_res, y=None, w_post=None, gate=None,
 
 
 # ------------------------------------------------------------ allocating conveniences
+#
+# With `stream`, tensors are allocated under that stream, and outputs and operands are marked as used
+# by both: the caching allocator orders a block's next use only behind the work of the stream that it
+# was allocated under and of those it is told of, so a workspace from the caller's stream would be
+# given out again while the launch still uses it. As with any work on a side stream, the caller orders
+# the writes of the operands before the call and the use of the outputs after it.
 
+def _side_stream(stream):
+    """The torch stream of `stream` (a Stream or a raw handle) if it is not the current one."""
+    torch = _torch or _torch_module()
+    if not torch.cuda.is_initialized():          # no GPU tensor exists: the call is refused below
+        return None
+    handle = _stream(stream)
+    if handle == _stream(None):
+        return None
+    if not isinstance(stream, int):
+        return stream
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+
+def _used_on(stream, values):
+    for t in values:
+        if isinstance(t, _Tensor):
+            t.record_stream(stream)
+
+
+def _under_stream(fn):
+    """Runs an allocating convenience with its `stream` as torch's current one."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        side = None if stream is None else _side_stream(stream)
+        if side is None:
+            return fn(*args, **kw)
+        caller = _torch.cuda.current_stream()
+        with _torch.cuda.stream(side):
+            out = fn(*args, **kw)
+        # either may be dropped with the other stream's work on it in flight
+        _used_on(side, (*args, *kw.values()))
+        _used_on(caller, out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,))
+        return out
+    return call
+
+
+@_under_stream
 def quant_tokens(x, q_dtype=BFQ_E4M3FN, layout=BFQ_SCALES_ROW_MAJOR, eps=DEFAULT_EPS,
                  stream=None, scale_fmt=BFQ_SCALE_FP32, per_token=False):
     """Allocate (q, scales) with torch and run bfq_quant_tokens. Returns (q, scales); with
@@ -902,6 +950,7 @@ def quant_tokens(x, q_dtype=BFQ_E4M3FN, layout=BFQ_SCALES_ROW_MAJOR, eps=DEFAULT
     return q, s
 
 
+@_under_stream
 def quant_weight_blocks(w, q_dtype=BFQ_E4M3FN, eps=DEFAULT_EPS, stream=None,
                         scale_fmt=BFQ_SCALE_FP32, per_channel=False):
     """Allocate (q, scales) with torch and run bfq_quant_weight_blocks; per_channel gives one
@@ -920,6 +969,7 @@ def quant_weight_blocks(w, q_dtype=BFQ_E4M3FN, eps=DEFAULT_EPS, stream=None,
     return q, s
 
 
+@_under_stream
 def moe_align(topk_ids, E, stream=None):
     """Allocate and run bfq_moe_align. Returns (expert_offsets int32 [E+1], sorted_pairs
     int32 [T*topk])."""
@@ -934,6 +984,7 @@ def moe_align(topk_ids, E, stream=None):
     return off, srt
 
 
+@_under_stream
 def moe_block_gemm(a_q, a_scales, sorted_pairs, expert_offsets, topk, w_q, w_scales,
                    out_dtype=None, a_layout=BFQ_SCALES_ROW_MAJOR, tile=None, stream=None,
                    w_layout=BFQ_W_ROW_MAJOR, scale_fmt=BFQ_SCALE_FP32):
@@ -945,7 +996,7 @@ def moe_block_gemm(a_q, a_scales, sorted_pairs, expert_offsets, topk, w_q, w_sca
     out = torch.empty((T * topk, N), dtype=out_dtype, device=a_q.device)
     if tile is None:
         st, tile = bfq_moe_select_tile(T, topk, E, N, K, _odtype(out), w_layout, scale_fmt)
-        _check(st, "bfq_moe_select_tile", warn_key=("moe", E, N, K))
+        _check(st, "bfq_moe_select_tile", warn_key=("moe", E, N, K), depth=4)
     ws_bytes = bfq_moe_gemm_workspace_bytes(T, topk, N, tile)
     ws = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=a_q.device) if ws_bytes else None
     bfq_moe_block_gemm(a_q, a_scales, sorted_pairs, expert_offsets, topk, w_q, w_scales, out,
@@ -954,6 +1005,7 @@ def moe_block_gemm(a_q, a_scales, sorted_pairs, expert_offsets, topk, w_q, w_sca
     return out
 
 
+@_under_stream
 def pack_weights(w_q, stream=None):
     """Allocate a packed copy of row-major weight codes (same dtype and shape) with torch and
     run bfq_pack_weights. [E, N, K] expert weights pack as one [E*N, K] matrix, which is each
@@ -965,6 +1017,7 @@ def pack_weights(w_q, stream=None):
     return p
 
 
+@_under_stream
 def block_gemm(a_q, a_scales, w_q, w_scales, out_dtype=None, a_layout=BFQ_SCALES_ROW_MAJOR,
                tile=None, stream=None, w_layout=BFQ_W_ROW_MAJOR, scale_fmt=BFQ_SCALE_FP32,
                per_channel=False):
@@ -979,7 +1032,7 @@ def block_gemm(a_q, a_scales, w_q, w_scales, out_dtype=None, a_layout=BFQ_SCALES
     if tile is None:
         st, tile = bfq_select_tile(M, N, K, _qdtype(a_q), _odtype(out), w_layout=w_layout,
                                    scale_fmt=scale_fmt, block_shape=bs)
-        _check(st, "bfq_select_tile", warn_key=(N, K))
+        _check(st, "bfq_select_tile", warn_key=(N, K), depth=4)
     ws_bytes = bfq_gemm_workspace_bytes(M, N, K, tile)
     ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=a_q.device) if ws_bytes else None
     bfq_block_gemm(a_q, a_scales, w_q, w_scales, out, a_layout=a_layout, tile=tile,
@@ -997,6 +1050,7 @@ def _alloc_scales(M, groups, layout, device):
     return torch.empty(shape, dtype=torch.float32, device=device)
 
 
+@_under_stream
 def gated_gemm(a_q, a_scales, w_q, w_scales, act=BFQ_ACT_SILU, out_dtype=None, codes=False,
                keep_preact=False, a_layout=BFQ_SCALES_ROW_MAJOR, out_layout=BFQ_SCALES_ROW_MAJOR,
                tile=None, stream=None, w_layout=BFQ_W_ROW_MAJOR, scale_fmt=BFQ_SCALE_FP32):
@@ -1018,6 +1072,7 @@ def gated_gemm(a_q, a_scales, w_q, w_scales, act=BFQ_ACT_SILU, out_dtype=None, c
     return res if len(res) > 1 else out
 
 
+@_under_stream
 def gated_backward(preact, dh, act=BFQ_ACT_SILU, codes=False, want_h=False,
                    layout=BFQ_SCALES_ROW_MAJOR, q_dtype=BFQ_E4M3FN, scale_fmt=BFQ_SCALE_FP32,
                    stream=None):
@@ -1040,6 +1095,7 @@ def gated_backward(preact, dh, act=BFQ_ACT_SILU, codes=False, want_h=False,
     return res if len(res) > 1 else dpre
 
 
+@_under_stream
 def transpose_weights(w_q, w_scales, stream=None):
     """Allocate and run bfq_transpose_weights: (codes [K, N], scales [K/128, N/128])."""
     import torch
@@ -1050,6 +1106,7 @@ def transpose_weights(w_q, w_scales, stream=None):
     return wt, st
 
 
+@_under_stream
 def norm_residual(residual, y=None, w_post=None, gate=None, gate_kind=BFQ_GATE_NONE, res_scale=1.0,
                   w_pre=None, norm_eps=NORM_EPS, codes=False, q_dtype=BFQ_E4M3FN, per_token=False,
                   layout=BFQ_SCALES_ROW_MAJOR, scale_fmt=BFQ_SCALE_FP32, stream=None):
@@ -1073,6 +1130,7 @@ def norm_residual(residual, y=None, w_post=None, gate=None, gate_kind=BFQ_GATE_N
     return tuple(t for t in (res_out, normed, q, scales) if t is not None)
 
 
+@_under_stream
 def norm_residual_backward(res_out, y=None, w_post=None, gate=None, gate_kind=BFQ_GATE_NONE,
                            res_scale=1.0, w_pre=None, norm_eps=NORM_EPS, d_normed=None,
                            d_res_out=None, stream=None) -> dict:
