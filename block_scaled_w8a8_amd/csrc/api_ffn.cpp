@@ -503,6 +503,7 @@ bfq_status bfq_norm_residual(const void* y, const void* residual, bfq_dtype res_
     a.normed = normed;
     a.q = q;
     a.scales = scales;
+    a.invariant = batch_invariant() ? 1 : 0;
     const hipError_t e = launch_norm_residual(a, res_dtype == BFQ_FP32, (hipStream_t)stream);
     if (e != hipSuccess) return fail(BFQ_ERR_HIP, hipGetErrorString(e));
     return BFQ_OK;

@@ -62,6 +62,7 @@ struct NormArgs {
     int64_t s_stride_m, s_stride_g;   // scale strides of a token and of a group (packed: word row)
     int qtype, per_token, ue8m0, packed;
     float q_eps;
+    int invariant;          // batch-invariant mode: the kernel by K alone
     // backward
     const void* d_normed;   // [M][K] bf16
     const void* d_res_out;  // [M][K] as the residual

@@ -476,11 +476,13 @@ static hipError_t launch_norm_s(const NormArgs& a, hipStream_t stream) {
 // Chunks a thread. Few waves a row start and reduce sooner (one row of 1536: 3.4 us with one chunk
 // a thread, 3.8 with two); fewer, fatter threads leave room for more rows on a CU (4096 rows of
 // 7168: 62.5 us with one chunk, 47.8 with two, 47.2 with four; 1024 rows of 16384: 29.2 with two,
-// 25.8 with four).
+// 25.8 with four). The chunks decide which elements a thread adds up, so past 8192 channels the last
+// bits of a row depend on M; in batch-invariant mode four serve every M (one row of
+// 16384, codes out: 6.3 us for 6.1; 256 rows 11.9 either way).
 template <int RF32>
 static hipError_t launch_norm_p(const NormArgs& a, hipStream_t stream) {
     if (a.K <= 2048) return launch_norm_s<1, RF32>(a, stream);
-    if (a.K <= 8192 || a.M <= 256) return launch_norm_s<2, RF32>(a, stream);
+    if (a.K <= 8192 || (a.M <= 256 && !a.invariant)) return launch_norm_s<2, RF32>(a, stream);
     return launch_norm_s<4, RF32>(a, stream);
 }
 

@@ -430,7 +430,8 @@ bfq_status bfq_transpose_weights(const void* w_q, const float* w_scales, int64_t
  *   bfq_quant_tokens: group_size 128 or K, q_dtype E4M3FN | INT8), or both; both are formed from
  *   the fp32 n, and n from the fp32 r'. Without w_pre, normed and q must be NULL.
  * K a positive multiple of 8 (of 128 with q), at most 16384; M < 2^24 - 4; norm_eps positive and
- * finite. Row sums of squares are fp32: values past about 1e17 overflow them. */
+ * finite. Row sums of squares are fp32: values past about 1e17 overflow them. A token's rows do not
+ * depend on M for K <= 8192, and in batch-invariant mode for any K. */
 bfq_status bfq_norm_residual(const void* y, const void* residual, bfq_dtype res_dtype,
                              const void* w_post, const void* gate, bfq_gate_kind gate_kind,
                              float res_scale, const void* w_pre, float norm_eps, void* res_out,
