@@ -72,19 +72,27 @@ __device__ __forceinline__ float pow2_ceil(float s) {
     return (u & 0x007FFFFFu) ? __uint_as_float((u & 0xFF800000u) + 0x00800000u) : s;
 }
 
-// Encode 8 fp32 values of a finite group (|x| <= amax of the group that s was formed from): the
-// product with the reciprocal, which is within 2 units of the quotient x / s, the size of the
-// roundings x itself carries when it comes out of fp32 arithmetic. (encode8 above corrects that
-// product, 3 operations a value more, so that codes of given bf16 inputs are the IEEE quotient's.)
-// Scales outside [2^-100, 2^100] (a tiny eps, or amax near the range's ends) take the division.
+// Encode 8 fp32 values of a finite group (|x| <= amax of the group that s was formed from) to the code
+// of the IEEE quotient x / s: q = x * r, r the correctly rounded 1 / s, corrected once by the remainder
+// e = q * s - x. With any mantissa of x and s the code of q - e * r is that of the quotient (checked on
+// the CPU around every midpoint of two codes: tests/native/quotient_codes_fp32.c; with r a unit off it
+// is not), and a zero keeps its sign. v_rcp_f32 is within a unit of 1 / s and one Newton step then
+// rounds it correctly, on gfx950 for each of the 2^23 mantissas. The remainder is exact while nothing in
+// it is subnormal; scales outside [2^-60, 2^100] (a tiny eps, or amax near the range's ends) take the
+// division. Bare products x * r, two operations a value less, gave another code in 2.6e-4 of the places
+// where the values are products of two bf16, which meet ties. (encode8 above, on bf16 values, divides
+// once a lane and restores signs.)
 template <int QT>
 __device__ __forceinline__ uint2 encode8_f32(const float* x, float s) {
     float y[8];
-    if (s >= 0x1p-100f && s <= 0x1p100f) {
+    if (s >= 0x1p-60f && s <= 0x1p100f) {
         const float r0 = __builtin_amdgcn_rcpf(s);
         const float rs = __builtin_fmaf(__builtin_fmaf(-s, r0, 1.f), r0, r0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i] * rs;
+        for (int i = 0; i < 8; ++i) {
+            const float q = x[i] * rs, e = __builtin_fmaf(q, s, -x[i]);
+            y[i] = __builtin_fmaf(e, -rs, q);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = x[i] / s;
