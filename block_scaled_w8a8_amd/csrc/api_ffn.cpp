@@ -9,7 +9,8 @@ using namespace bfq;
 
 namespace {
 
-// Rows of the row-per-workgroup kernels: a grid dimension holds fewer than 2^32 threads, 256 a row.
+// Rows of the kernels with a workgroup of 256 threads a row: a grid dimension holds fewer than 2^32
+// threads. (The norm step takes more threads a row, and a launch for each slice of rows that fits.)
 constexpr int64_t kMaxRows = (int64_t(1) << 24) - 4;
 constexpr int64_t kMaxScaleLd = int64_t(1) << 40;
 

@@ -55,6 +55,7 @@ struct NormArgs {
     float res_scale, norm_eps;
     int64_t M, K;
     // forward
+    int64_t row0;           // the first row of this launch
     void* res_out;          // [M][K] as the residual
     void* normed;           // [M][K] bf16
     void* q;                // [M][K] codes

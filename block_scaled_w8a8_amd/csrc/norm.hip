@@ -91,7 +91,7 @@ template <int P> constexpr int kNormThreads = P == 4 ? 512 : 1024;
 template <int P, int RF32, int Q, int S>
 __global__ __launch_bounds__(kNormThreads<P>) void norm_residual_kernel(NormArgs p) {
     const int t = threadIdx.x, lane = t & 63, T = blockDim.x;
-    const int64_t m = blockIdx.x, K = p.K;
+    const int64_t m = p.row0 + blockIdx.x, K = p.K;
     const uint32_t row16 = (uint32_t)(2 * K), row_res = RF32 ? 2 * row16 : row16;   // bytes of a row
     const float fK = (float)K;
     __shared__ __attribute__((aligned(16))) float red[2][16];
@@ -457,14 +457,21 @@ static unsigned threads_for(int64_t K, int P) {
 template <int P, int RF32, int S>
 static hipError_t launch_norm_q(const NormArgs& a, hipStream_t stream) {
     const int64_t rows = a.packed ? (a.M + 3) / 4 * 4 : a.M;
-    const dim3 grid((unsigned)rows), block(threads_for(a.K, P));
-    if (!a.q)
-        hipLaunchKernelGGL((norm_residual_kernel<P, RF32, -1, S>), grid, block, 0, stream, a);
-    else if (a.qtype == Q_FP8)
-        hipLaunchKernelGGL((norm_residual_kernel<P, RF32, Q_FP8, S>), grid, block, 0, stream, a);
-    else
-        hipLaunchKernelGGL((norm_residual_kernel<P, RF32, Q_INT8, S>), grid, block, 0, stream, a);
-    return hipGetLastError();
+    // a grid dimension holds fewer than 2^32 threads: at K = 8192 rows past 2^23 - 4 take a second launch
+    const int64_t most = ((int64_t(1) << 32) - 1) / threads_for(a.K, P);
+    NormArgs b = a;
+    for (b.row0 = 0; b.row0 < rows; b.row0 += most) {
+        const dim3 grid((unsigned)(rows - b.row0 < most ? rows - b.row0 : most)), block(threads_for(a.K, P));
+        if (!a.q)
+            hipLaunchKernelGGL((norm_residual_kernel<P, RF32, -1, S>), grid, block, 0, stream, b);
+        else if (a.qtype == Q_FP8)
+            hipLaunchKernelGGL((norm_residual_kernel<P, RF32, Q_FP8, S>), grid, block, 0, stream, b);
+        else
+            hipLaunchKernelGGL((norm_residual_kernel<P, RF32, Q_INT8, S>), grid, block, 0, stream, b);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 template <int P, int RF32>
