@@ -10,7 +10,8 @@
 kernel and scales each by what the same counter reads for a plain device copy of known size
 (bytes moved by the copy / counter reading), so the result is HBM bytes per launch. It also
 records a hash of the kernel sources, so bench.py can tell whether the counters still
-describe the current kernel.
+describe the current kernel. `stats` stamps its summary with the same hash, or (--feed-forward) with
+one that covers the feed-forward operators' kernels as well.
 """
 from __future__ import annotations
 
@@ -24,11 +25,14 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 KERNEL_SOURCES = ("csrc/gemm_std.hip", "csrc/gemm_swapab.hip", "csrc/quant.hip",
                   "csrc/moe.hip", "csrc/device_common.h", "csrc/gemm_std_tile.h",
                   "csrc/gemm_swapab_body.h", "csrc/quant_device.h")
+# the feed-forward operators' kernels, beside the routines above that they share
+FEED_FORWARD_SOURCES = KERNEL_SOURCES + ("csrc/gated.hip", "csrc/norm.hip", "csrc/activation.h",
+                                         "csrc/bfq_internal.h")
 
 
-def source_hash() -> str:
+def source_hash(sources=KERNEL_SOURCES) -> str:
     h = hashlib.sha256()
-    for rel in KERNEL_SOURCES:
+    for rel in sources:
         with open(os.path.join(HERE, rel), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]
@@ -49,8 +53,9 @@ def _rows(path_or_dir, name):
 def cmd_stats(args):
     rows = _rows(args.csv, "*kernel_stats.csv")
     rows.sort(key=lambda r: -float(r["TotalDurationNs"]))
+    digest = source_hash(FEED_FORWARD_SOURCES if args.feed_forward else KERNEL_SOURCES)
     lines = [f"# rocprofv3 kernel statistics", f"# command: {args.command}",
-             f"# kernel sources: {source_hash()}", "",
+             f"# kernel sources: {digest}", "",
              f"{'calls':>6} {'avg_us':>10} {'min_us':>10} {'max_us':>10} {'total%':>7}  kernel"]
     for r in rows[: args.top]:
         lines.append(f"{int(r['Calls']):6d} {float(r['AverageNs']) / 1e3:10.2f} "
@@ -213,6 +218,8 @@ def main():
     s.add_argument("--command", default="")
     s.add_argument("--out")
     s.add_argument("--top", type=int, default=12)
+    s.add_argument("--feed-forward", action="store_true",
+                   help="stamp with the sources of the feed-forward operators' kernels too")
     s.add_argument("--trace", help="kernel_trace.csv (or its directory) for per-grid averages")
     t = sub.add_parser("traffic")
     for k in ("fetch", "write", "copy_fetch", "copy_write"):
