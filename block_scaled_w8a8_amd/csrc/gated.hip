@@ -13,9 +13,12 @@
 //
 // What bounds the forward kernels is what bounds the block GEMM's: the weight stream at decode
 // sizes, the operand bytes through a CU's L1 and the scale step at large M. Measured, F 18432 x
-// K 7168, packed weights, SILU, bf16 out: 1 token 42 us (6.3 TB/s of weights), 64 tokens 56 us,
-// 512 tokens 152 us, 4096 tokens 965 us with fp32 scales (2.24 PFLOP/s) and 890 us with powers of
-// two, 25 to 80 us more, by the box, where the pre-activations are kept (302 MB).
+// K 7168, packed weights, SILU, bf16 out, on a card under load: 1 token 42 us (6.3 TB/s of weights), 64
+// tokens 55 us, 512 tokens 171 us, 1024 tokens 292 us, 4096 tokens 1012 us with fp32 scales (2.14 PFLOP/s)
+// and 923 us with powers of two; 1025 to 1055 us where the pre-activations (302 MB) are kept, by the box
+// and its clock, which takes some thirty calls to settle (the third one after an idle card: 1370 us, the
+// tenth 1145). Pairs of times further down compare two forms in short runs on one box: what they show is
+// the difference.
 // The two sums carry the e4m3 MFMA's own error, as the block GEMM's do: 3.5e-5 to 4.6e-5 of the
 // result (relative, Frobenius) on outlier-bearing tokens, whichever schedule or tile. Where codes
 // are wanted it decides the values that lie that near to a rounding boundary: 333 x 2048 codes
@@ -326,7 +329,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_gated_pipe_kernel(GatedArgs
     int64_t pid_m, pid_n;
     tile_coords(item.tile, tiles_m, tiles_n, p.group_m, p.raster, pid_m, pid_n);
     const int64_t m0 = pid_m * BM, n0 = pid_n * BNO, kb0 = item.kb0, L = item.kb1 - kb0;
-    constexpr uint32_t kNoLoad = 0x80000000u;           // past every resource here
+    // past every resource here (inside scales that span over 2 GiB, whose value then goes unused)
+    constexpr uint32_t kNoLoad = 0x80000000u;
 
     const uint8_t* w = static_cast<const uint8_t*>(p.w);
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(w + n0 * K, (uint32_t)(BNO * K));
@@ -528,12 +532,12 @@ __device__ __forceinline__ void dma16_weights(__amdgpu_buffer_rsrc_t r, uint8_t*
 // takes 16 output columns (16 gate rows, 16 up rows) and its waves every KW-th K block, so that
 // together they walk neighbouring bytes of the weights. Where that leaves CUs without work it takes
 // eight (BNO 8: one fragment of eight gate and eight up rows, the factors of an output in lanes l and
-// l + 32): F 2048 x K 7168 row-major, 1 token 7.9 us against 10.0, 16 tokens 9.3 against 10.6. Each wave copies 1 KB a load (row-major:
-// whole 128-byte lines of 8 rows; packed: a fragment half) into a ring of its own, D K blocks of
-// 4 KB (2 KB), and reads its fragments back: no barrier in the K loop, the wave waits until the loads of
-// its oldest block have landed, and what is in flight takes no registers, so a CU holds up to 10
-// waves of 16 KB in flight each. Row-major chunk c of row r sits in slot c ^ swz(r), as in the
-// standard tiles.
+// l + 32): F 2048 x K 7168 row-major, 1 token 7.9 us against 10.0, 16 tokens 9.3 against 10.6. Each wave
+// copies 1 KB a load (row-major: whole 128-byte lines of 8 rows; packed: a fragment half) into a ring of
+// its own, D K blocks of 4 KB (2 KB), and reads its fragments back: no barrier in the K loop, the wave
+// waits until the loads of its oldest block have landed, and what is in flight takes no registers, so a
+// CU holds up to 10 waves of 16 KB in flight each. Row-major chunk c of row r sits in slot c ^ swz(r), as
+// in the standard tiles.
 // ONCE (M <= MT): no other workgroup reads these weights, and they are loaded with the non-temporal
 // hint: 10 % off the time at F 18432 and 5 to 13 % on short products. With more tokens it would cost
 // up to 6 %: the tiles above find the weights in L2.
@@ -557,7 +561,8 @@ __global__ __launch_bounds__(64 * KW) void gemm_gated_ring_kernel(GatedArgs p) {
     const int split = p.split, z = blockIdx.z;
     const int64_t ks0 = (int64_t)z * KB / split, ks1 = (int64_t)(z + 1) * KB / split;
     const int64_t L = (ks1 - ks0 - wk + KW - 1) / KW;   // K blocks ks0 + wk, + KW, ..
-    constexpr uint32_t kNoLoad = 0x80000000u;           // past every resource here
+    // past every resource here (inside scales that span over 2 GiB, whose value then goes unused)
+    constexpr uint32_t kNoLoad = 0x80000000u;
 
     const uint8_t* w = static_cast<const uint8_t*>(p.w);
     // rows n0 / 16 * 16 on: packed weights come as groups of 16 rows
@@ -954,10 +959,10 @@ template <int S> __device__ __forceinline__ void stream_store(uint4* p, const ui
 }
 
 // With a = act(g): dg = dh * u * act'(g), du = dh * a, and the product h = a * u again. Eight
-// columns a thread, read once and written once; bytes bound it: 4096 x 18432 takes 170 us for the
-// pair's gradient and h as bf16 (906 MB, 5.3 TB/s; 179 without the non-temporal hints) and 116 us
-// for its codes (604 MB, 5.2 TB/s; a large copy reaches 4.8). Codes: 128-column groups of the 2F-wide row, one scale each, 16 lanes a
-// group; rows past M (packed words only) write zeros.
+// columns a thread, read once and written once; bytes bound it: 4096 x 18432 takes 165 to 169 us, by the
+// box, for the pair's gradient and h as bf16 (906 MB, 5.4 TB/s; some 9 us more without the non-temporal
+// hints) and 109 us for its codes (604 MB, 5.5 TB/s; a large copy reaches 4.8). Codes: 128-column groups
+// of the 2F-wide row, one scale each, 16 lanes a group; rows past M (packed words only) write zeros.
 template <int Q, int S>
 __global__ __launch_bounds__(256) void gated_bwd_kernel(GatedBwdArgs p) {
     const int lane = threadIdx.x & 63;

@@ -6,11 +6,12 @@
 // GEMMs read (the token quantizer's formats), or both. All of it in fp32; n is taken from the
 // unrounded r' and quantized unrounded, so storing r' or n as bf16 costs the codes nothing.
 //
-// What bounds it: bytes. 4096 rows of 7168 with post norm, codes out: 44.8 us, 206 MB at 4.6 TB/s
-// (a large copy reaches 4.8; without the non-temporal hints 48.8). A row is read once (y, r) and written once (r', codes), everything
-// between stays in registers: P chunks of 8 elements a thread, chunk c of the row held by thread
-// c % T in slot c / T, so 16 neighbouring lanes own one 128-element group as in the token
-// quantizer. Each norm costs one reduction over the workgroup (DPP within a wave, LDS across).
+// What bounds it: bytes. 4096 rows of 7168 with post norm, codes out: 206 MB in 43 us, 4.8 TB/s, the rate
+// of a large copy, and in 47 us on average over a hundred calls back to back (without the non-temporal
+// hints some 4 us more). A row is read once (y, r) and written once (r', codes), everything between stays
+// in registers: P chunks of 8 elements a thread, chunk c of the row held by thread c % T in slot c / T, so
+// 16 neighbouring lanes own one 128-element group as in the token quantizer. Each norm costs one
+// reduction over the workgroup (DPP within a wave, LDS across).
 #include "bfq_internal.h"
 #include "quant_device.h"
 
@@ -239,10 +240,12 @@ __global__ __launch_bounds__(kNormThreads<P>) void norm_residual_kernel(NormArgs
 // (K > 8192): registers hold a row only, so the sums live in LDS (each thread its own slots), the
 // vectors come from L2, and the next row's loads start once their registers are free, all but y's
 // before the second reduction.
-// Bytes bound it. Measured: 4096 rows of 7168 bf16 with a channel gate 81 us with the column sums
-// (352 MB, 4.3 TB/s; two chunks a thread there some 10 more), 4096 of 8192 fp32 127 us (4.8 TB/s; 140),
-// 1024 of 16384 fp32 85 us (3.6 TB/s: four rows a CU, the first and last uncovered; with the sums
-// of two chunks in registers, which spill, 138).
+// Bytes bound it. Measured: 4096 rows of 7168 bf16 with a channel gate 77 us with the column sums (352 MB,
+// 4.6 TB/s; 86 on average over a hundred calls back to back), 4096 of 8192 fp32 121 us (5.0 TB/s; two
+// chunks a thread were 10 to 13 us slower on both), 1024 of 16384 fp32 78 us (3.9 TB/s: four rows a CU,
+// the first and last uncovered; with the sums of two chunks in registers, which spill, more than 50 us
+// slower). The column sums' launch is 3 to 5 us of it, and the shares it reads are 8 K bytes a workgroup:
+// on a few hundred short rows nearly as many as the operands' (257 rows of 1544: 7 and 3.6 us).
 template <int P, int RF32, int S>
 __global__ __launch_bounds__(1024) void norm_residual_bwd_kernel(NormArgs p) {
     const int t = threadIdx.x, T = blockDim.x;
@@ -484,8 +487,8 @@ static hipError_t launch_norm_s(const NormArgs& a, hipStream_t stream) {
 // a thread, 3.8 with two); fewer, fatter threads leave room for more rows on a CU (4096 rows of
 // 7168: 62.5 us with one chunk, 47.8 with two, 47.2 with four; 1024 rows of 16384: 29.2 with two,
 // 25.8 with four). The chunks decide which elements a thread adds up, so past 8192 channels the last
-// bits of a row depend on M; in batch-invariant mode four serve every M (one row of
-// 16384, codes out: 6.3 us for 6.1; 256 rows 11.9 either way).
+// bits of a row depend on M; in batch-invariant mode four serve every M (one row of 16384, codes out:
+// 6.3 us for 6.1; 256 rows 11.9 either way).
 template <int RF32>
 static hipError_t launch_norm_p(const NormArgs& a, hipStream_t stream) {
     if (a.K <= 2048) return launch_norm_s<1, RF32>(a, stream);

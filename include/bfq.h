@@ -367,8 +367,8 @@ bfq_status bfq_moe_get_tile_candidate(bfq_weight_layout w_layout, bfq_scale_form
  *   out_layout, out_scale_ld and out_eps are not read otherwise).
  *   preact: bf16 [M][2F] = (g, u), what bfq_gated_backward reads, or NULL.
  * M in [0, 2^24 - 4), F and K positive multiples of 128, F < 2^26, K <= 2^23, M * 2F < 2^40,
- * F * K < 2^40; activation scales as bfq_block_gemm. tile NULL -> bfq_gated_select_tile. The workspace holds
- * bfq_gated_gemm_workspace_bytes bytes (NULL when that is 0). */
+ * F * K < 2^40; activation scales as bfq_block_gemm. tile NULL -> bfq_gated_select_tile. The workspace
+ * holds bfq_gated_gemm_workspace_bytes bytes (NULL when that is 0). */
 bfq_status bfq_gated_gemm(const void* a_q, const float* a_scales, bfq_scale_layout a_layout,
                           int64_t a_scale_ld, const void* w_q, const float* w_scales,
                           bfq_weight_layout w_layout, bfq_scale_format scale_fmt,
@@ -383,13 +383,14 @@ bfq_status bfq_gated_gemm(const void* a_q, const float* a_scales, bfq_scale_layo
  * codes are wanted (bn counts output columns: 2 * bn weight rows). Variant 1 with sched 2 (gated
  * tiles only): the waves take every waves_m-th K block and copy the weights through LDS, stages K
  * blocks ahead. Variant 2: the tiles of variant 0 in rounds of one workgroup per compute unit, the K
- * range of those left over in as many parts as fill a last round (split_k 1; for codes bn 128). Batch-invariant mode applies as in bfq_select_tile. */
+ * range of those left over in as many parts as fill a last round (split_k 1; for codes bn 128).
+ * Batch-invariant mode applies as in bfq_select_tile. */
 bfq_status bfq_gated_select_tile(int64_t M, int64_t F, int64_t K, bfq_dtype out_dtype,
                                  bfq_weight_layout w_layout, bfq_scale_format scale_fmt,
                                  bfq_tile* tile_out);
 /* split_k * M * 2F * 4 bytes when the tile's split_k > 1, or when codes are wanted and the tile's
- * bn is not 128; variant 2: at most 256 partial tiles of bm * 2 bn * 4 bytes; else 0. tile NULL -> the selected one. SIZE_MAX for shapes bfq_gated_gemm
- * rejects as too large. */
+ * bn is not 128; variant 2: at most 256 partial tiles of bm * 2 bn * 4 bytes; else 0. tile NULL -> the
+ * selected one. SIZE_MAX for shapes bfq_gated_gemm rejects as too large. */
 size_t     bfq_gated_gemm_workspace_bytes(int64_t M, int64_t F, int64_t K, bfq_dtype out_dtype,
                                           bfq_weight_layout w_layout, bfq_scale_format scale_fmt,
                                           const bfq_tile* tile);
