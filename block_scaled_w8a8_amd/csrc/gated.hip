@@ -15,9 +15,9 @@
 // sizes, the operand bytes through a CU's L1 and the scale step at large M. Measured, F 18432 x
 // K 7168, packed weights, SILU, bf16 out, on a card under load: 1 token 42 us (6.3 TB/s of weights), 64
 // tokens 55 us, 512 tokens 171 us, 1024 tokens 292 us, 4096 tokens 1012 us with fp32 scales (2.14 PFLOP/s)
-// and 923 us with powers of two; 1025 to 1055 us where the pre-activations (302 MB) are kept, by the box
+// and 923 us with powers of two; 1025 to 1055 us where the pre-activations (302 MB) are kept, by the card
 // and its clock, which takes some thirty calls to settle (the third one after an idle card: 1370 us, the
-// tenth 1145). Pairs of times further down compare two forms in short runs on one box: what they show is
+// tenth 1145). Pairs of times further down compare two forms in short runs on one card: what they show is
 // the difference.
 // The two sums carry the e4m3 MFMA's own error, as the block GEMM's do: 3.5e-5 to 4.6e-5 of the
 // result (relative, Frobenius) on outlier-bearing tokens, whichever schedule or tile. Where codes
@@ -960,7 +960,7 @@ template <int S> __device__ __forceinline__ void stream_store(uint4* p, const ui
 
 // With a = act(g): dg = dh * u * act'(g), du = dh * a, and the product h = a * u again. Eight
 // columns a thread, read once and written once; bytes bound it: 4096 x 18432 takes 165 to 169 us, by the
-// box, for the pair's gradient and h as bf16 (906 MB, 5.4 TB/s; some 9 us more without the non-temporal
+// card, for the pair's gradient and h as bf16 (906 MB, 5.4 TB/s; some 9 us more without the non-temporal
 // hints) and 109 us for its codes (604 MB, 5.5 TB/s; a large copy reaches 4.8). Codes: 128-column groups
 // of the 2F-wide row, one scale each, 16 lanes a group; rows past M (packed words only) write zeros.
 template <int Q, int S>
