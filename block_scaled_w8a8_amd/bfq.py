@@ -48,6 +48,10 @@ BFQ_ACT_GELU_TANH = 1
 # what one gate value of the norm step covers (bfq_gate_kind)
 BFQ_GATE_NONE, BFQ_GATE_CHANNEL, BFQ_GATE_TOKEN, BFQ_GATE_FULL = range(4)
 
+# score functions of the router (bfq_score)
+BFQ_SCORE_SOFTMAX = 0
+BFQ_SCORE_SIGMOID = 1
+
 DEFAULT_EPS = 1e-10
 NORM_EPS = 1e-6
 # Maximum K of the norm step (a row stays in a workgroup's registers).
@@ -76,6 +80,9 @@ EXPORTED = (
     "bfq_gated_num_tile_candidates", "bfq_gated_get_tile_candidate", "bfq_gated_backward",
     "bfq_transpose_weights", "bfq_norm_residual", "bfq_norm_residual_backward",
     "bfq_norm_residual_backward_workspace_bytes",
+    "bfq_moe_route", "bfq_moe_route_backward", "bfq_moe_sort_workspace_bytes", "bfq_moe_sort",
+    "bfq_moe_dispatch", "bfq_moe_combine", "bfq_moe_combine_backward", "bfq_gated_checkpoint",
+    "bfq_gated_checkpoint_backward",
 )
 
 
@@ -166,6 +173,18 @@ def _load():
         "bfq_norm_residual_backward_workspace_bytes": (sz, [i64, i64]),
         "bfq_norm_residual_backward": (i32, [p, p, i32, p, p, i32, f32, p, f32, p, p, p, p, p, p, p,
                                              i64, i64, p, sz, p]),
+        "bfq_moe_route": (i32, [p, i32, p, i64, i32, i32, i32, i32, i32, i32, f32, p, p, p]),
+        "bfq_moe_route_backward": (i32, [p, i32, p, p, i64, i32, i32, i32, i32, f32, p, p]),
+        "bfq_moe_sort_workspace_bytes": (sz, [i64, i32, i32]),
+        "bfq_moe_sort": (i32, [p, i64, i32, i32, p, p, p, p, sz, p]),
+        "bfq_moe_dispatch": (i32, [p, i32, p, i32, i64, p, p, p, i32, p, i32, i64, f32, i32, i64, i32,
+                                   i64, i64, p]),
+        "bfq_moe_combine": (i32, [p, i32, p, p, p, i32, p, p, i32, p, i32, p, f32, i64, i32, i64, i64, p]),
+        "bfq_moe_combine_backward": (i32, [p, i32, p, p, i32, p, p, p, i32, p, p, i32, p, i32, i64, f32,
+                                           i32, p, i64, i32, i64, i64, p]),
+        "bfq_gated_checkpoint": (i32, [p, i32, p, p, i32, p, i32, i64, f32, i32, p, i32, p, p, i64, i64, p]),
+        "bfq_gated_checkpoint_backward": (i32, [p, i32, p, p, i32, p, p, i32, p, i32, i64, f32, i32, p, p,
+                                                i64, i64, p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -878,6 +897,239 @@ def bfq_norm_residual_backward(res_out, d_res, y=None, w_post=None, gate=None,
                                         _ptr(d_w_pre), _ptr(d_w_post), _ptr(d_gate), M, K,
                                         _ptr(workspace), workspace_bytes, _stream(stream))
     return _check(st, "bfq_norm_residual_backward")
+
+
+# ------------------------------------------------ MoE layer around the grouped GEMM
+
+def _route_operands(logits, topk_ids, w, wname):
+    T, E = _shape2(logits, "logits")
+    topk = _shape2(topk_ids, "topk_ids")[1]
+    _rows(logits, "logits", OUT_DTYPES, T, E)
+    _rows(topk_ids, "topk_ids", ("int32",), T, topk)
+    _rows(w, wname, ("float32",), T, topk)
+    return T, E, topk
+
+
+def bfq_moe_route(logits, topk_ids, topk_weights, bias=None, score=BFQ_SCORE_SOFTMAX, n_groups=1,
+                  topk_groups=1, renorm=False, weight_scale=1.0, stream=None) -> int:
+    """logits [T, E] bf16 / fp16 / fp32; topk_ids int32 and topk_weights fp32 [T, topk] receive each
+    token's experts, best first, and their weights. bias fp32 [E] moves the choice only."""
+    T, E, topk = _route_operands(logits, topk_ids, topk_weights, "topk_weights")
+    if bias is not None:
+        _flat(bias, "bias", ("float32",), E)
+    _devices(logits=logits, bias=bias, topk_ids=topk_ids, topk_weights=topk_weights)
+    st = lib.bfq_moe_route(_ptr(logits), _odtype(logits), _ptr(bias), T, E, topk, score, n_groups,
+                           topk_groups, int(renorm), weight_scale, _ptr(topk_ids), _ptr(topk_weights),
+                           _stream(stream))
+    return _check(st, "bfq_moe_route")
+
+
+def bfq_moe_route_backward(logits, topk_ids, d_weights, d_logits, score=BFQ_SCORE_SOFTMAX,
+                           renorm=False, weight_scale=1.0, stream=None) -> int:
+    """d_logits ([T, E], logits' dtype) receives the gradient of the weights of topk_ids at the
+    logits, for d_weights fp32 [T, topk]."""
+    T, E, topk = _route_operands(logits, topk_ids, d_weights, "d_weights")
+    _rows(d_logits, "d_logits", (_dt(logits),), T, E)
+    _devices(logits=logits, topk_ids=topk_ids, d_weights=d_weights, d_logits=d_logits)
+    st = lib.bfq_moe_route_backward(_ptr(logits), _odtype(logits), _ptr(topk_ids), _ptr(d_weights), T, E,
+                                    topk, score, int(renorm), weight_scale, _ptr(d_logits),
+                                    _stream(stream))
+    return _check(st, "bfq_moe_route_backward")
+
+
+def bfq_moe_sort_workspace_bytes(T, topk, E) -> int:
+    return int(lib.bfq_moe_sort_workspace_bytes(T, topk, E))
+
+
+def bfq_moe_sort(topk_ids, E, expert_offsets, sorted_pairs, pair_rows, workspace=None,
+                 workspace_bytes=None, stream=None) -> int:
+    """The outputs of bfq_moe_align, and pair_rows int32 [T, topk]: each pair's place in
+    sorted_pairs, -1 for an id outside [0, E)."""
+    T, topk = _shape2(topk_ids, "topk_ids")
+    workspace_bytes = _workspace_arg(workspace, workspace_bytes)
+    _rows(topk_ids, "topk_ids", ("int32",), T, topk)
+    _rows(pair_rows, "pair_rows", ("int32",), T, topk)
+    _flat(expert_offsets, "expert_offsets", ("int32",), E + 1)
+    _flat(sorted_pairs, "sorted_pairs", ("int32",), T * topk, exact=False)
+    _workspace(workspace, workspace_bytes)
+    _devices(topk_ids=topk_ids, expert_offsets=expert_offsets, sorted_pairs=sorted_pairs,
+             pair_rows=pair_rows, workspace=workspace)
+    st = lib.bfq_moe_sort(_ptr(topk_ids), T, topk, E, _ptr(expert_offsets), _ptr(sorted_pairs),
+                          _ptr(pair_rows), _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check(st, "bfq_moe_sort")
+
+
+def _codes_out(q, scales, layout, scale_ld, R, N):
+    """Checks of output codes [R, N] with their scales; returns (q_dtype, scale_ld)."""
+    if (q is None) != (scales is None):
+        raise BfqArgumentError("q and scales go together")
+    if q is None:
+        return BFQ_E4M3FN, 0
+    _rows(q, "q", CODE_DTYPES, R, N)
+    if scale_ld is None:
+        scale_ld = scales.stride(0)
+    _scales(scales, "scales", layout, scale_ld, R, N // 128, write=True)
+    return _qdtype(q), scale_ld
+
+
+def bfq_moe_dispatch(x, pair_rows, rows=None, q=None, scales=None, x_scales=None,
+                     x_layout=BFQ_SCALES_ROW_MAJOR, x_scale_ld=None, layout=BFQ_SCALES_ROW_MAJOR,
+                     scale_ld=None, q_eps=DEFAULT_EPS, scale_fmt=BFQ_SCALE_FP32, stream=None) -> int:
+    """Row pair_rows[t, j] of the outputs receives row t of x: bf16 [T, K] as rows (bf16 [R, K]) and
+    / or as codes q [R, K] with scales; or codes x with x_scales as codes."""
+    T, K = _shape2(x, "x")
+    topk = _shape2(pair_rows, "pair_rows")[1]
+    R = _shape2(q if q is not None else rows, "q" if q is not None else "rows")[0]
+    copy = x_scales is not None
+    _rows(x, "x", CODE_DTYPES if copy else ("bfloat16",), T, K)
+    _rows(pair_rows, "pair_rows", ("int32",), T, topk)
+    if copy:
+        if x_scale_ld is None:
+            x_scale_ld = x_scales.stride(0)
+        _scales(x_scales, "x_scales", x_layout, x_scale_ld, T, K // 128, write=False)
+    if rows is not None:
+        _rows(rows, "rows", ("bfloat16",), R, K)
+    qt, scale_ld = _codes_out(q, scales, layout, scale_ld, R, K)
+    _devices(x=x, x_scales=x_scales, pair_rows=pair_rows, rows=rows, q=q, scales=scales)
+    st = lib.bfq_moe_dispatch(_ptr(x), _qdtype(x) if copy else BFQ_BF16, _ptr(x_scales), x_layout,
+                              x_scale_ld or 0, _ptr(pair_rows), _ptr(rows), _ptr(q), qt, _ptr(scales),
+                              layout, scale_ld, q_eps, scale_fmt, T, topk, K, R, _stream(stream))
+    return _check(st, "bfq_moe_dispatch")
+
+
+def _pair_operands(T, topk, weights, pair_rows, topk_ids):
+    for n, t, dt in (("weights", weights, "float32"), ("pair_rows", pair_rows, "int32"),
+                     ("topk_ids", topk_ids, "int32")):
+        if t is not None:
+            _rows(t, n, (dt,), T, topk)
+
+
+def bfq_moe_combine(rows, out, topk, weights=None, pair_rows=None, topk_ids=None, E=0, base=None,
+                    ckpt=None, ckpt_scales=None, q_eps=DEFAULT_EPS, stream=None) -> int:
+    """out [T, K] = base + sum over a token's pairs of weights [T, topk] (None: ones) times their rows
+    of rows [R, K]: row pair_rows[t, j], or (None) row t*topk + j unless topk_ids [T, topk] has an id
+    outside [0, E) there. base: out's dtype, None for zeros, may be out. ckpt (codes [R, K]) and
+    ckpt_scales (fp32 [R, K/128]) receive the rows in 8 bits."""
+    T, K = _shape2(out, "out")
+    R = _shape2(rows, "rows")[0]
+    _rows(rows, "rows", OUT_DTYPES, R, K)
+    _rows(out, "out", OUT_DTYPES, T, K)
+    _pair_operands(T, topk, weights, pair_rows, topk_ids)
+    if base is not None:
+        _rows(base, "base", (_dt(out),), T, K)
+    if (ckpt is None) != (ckpt_scales is None):
+        raise BfqArgumentError("ckpt and ckpt_scales go together")
+    if ckpt is not None:
+        _rows(ckpt, "ckpt", CODE_DTYPES, R, K)
+        _rows(ckpt_scales, "ckpt_scales", ("float32",), R, K // 128)
+    _devices(rows=rows, out=out, weights=weights, pair_rows=pair_rows, topk_ids=topk_ids, base=base,
+             ckpt=ckpt, ckpt_scales=ckpt_scales)
+    st = lib.bfq_moe_combine(_ptr(rows), _odtype(rows), _ptr(weights), _ptr(pair_rows), _ptr(topk_ids), E,
+                             _ptr(base), _ptr(out), _odtype(out), _ptr(ckpt),
+                             _qdtype(ckpt) if ckpt is not None else BFQ_E4M3FN, _ptr(ckpt_scales), q_eps,
+                             T, topk, K, R, _stream(stream))
+    return _check(st, "bfq_moe_combine")
+
+
+ROW_DTYPES = OUT_DTYPES + CODE_DTYPES
+
+
+def bfq_moe_combine_backward(dout, topk, weights=None, rows=None, rows_scales=None, pair_rows=None,
+                             topk_ids=None, E=0, d_rows=None, q=None, scales=None,
+                             layout=BFQ_SCALES_ROW_MAJOR, scale_ld=None, q_eps=DEFAULT_EPS,
+                             scale_fmt=BFQ_SCALE_FP32, d_weights=None, stream=None) -> int:
+    """Gradients of bfq_moe_combine for dout bf16 / fp32 [T, K]: weights times dout as d_rows (bf16
+    [R, K]) and / or codes q [R, K] with scales; d_weights fp32 [T, topk] from rows [R, K] (bf16, fp16,
+    fp32, or codes with rows_scales fp32 [R, K/128])."""
+    T, K = _shape2(dout, "dout")
+    given = [(n, t) for n, t in (("rows", rows), ("d_rows", d_rows), ("q", q)) if t is not None]
+    if not given:
+        raise BfqArgumentError("one of d_rows, q and d_weights (with rows) must be given")
+    R = _shape2(given[0][1], given[0][0])[0]
+    _rows(dout, "dout", RES_DTYPES, T, K)
+    _pair_operands(T, topk, weights, pair_rows, topk_ids)
+    if (rows is None) != (d_weights is None):
+        raise BfqArgumentError("rows and d_weights go together")
+    rt = BFQ_BF16
+    if rows is not None:
+        _rows(rows, "rows", ROW_DTYPES, R, K)
+        rt = _OUT_TYPES.get(_dt(rows))
+        if rt is None:
+            rt = _qdtype(rows)
+            if rows_scales is None:
+                raise BfqArgumentError("rows of codes need rows_scales")
+        if rows_scales is not None:
+            _rows(rows_scales, "rows_scales", ("float32",), R, K // 128)
+        _rows(d_weights, "d_weights", ("float32",), T, topk)
+    if d_rows is not None:
+        _rows(d_rows, "d_rows", ("bfloat16",), R, K)
+    qt, scale_ld = _codes_out(q, scales, layout, scale_ld, R, K)
+    _devices(dout=dout, weights=weights, rows=rows, rows_scales=rows_scales, pair_rows=pair_rows,
+             topk_ids=topk_ids, d_rows=d_rows, q=q, scales=scales, d_weights=d_weights)
+    st = lib.bfq_moe_combine_backward(_ptr(dout), BFQ_BF16 if _dt(dout) == "bfloat16" else BFQ_FP32,
+                                      _ptr(weights), _ptr(rows), rt, _ptr(rows_scales), _ptr(pair_rows),
+                                      _ptr(topk_ids), E, _ptr(d_rows), _ptr(q), qt, _ptr(scales), layout,
+                                      scale_ld, q_eps, scale_fmt, _ptr(d_weights), T, topk, K, R,
+                                      _stream(stream))
+    return _check(st, "bfq_moe_combine_backward")
+
+
+def _live_rows(t):
+    if t is not None:
+        _flat(t, "live_rows", ("int32",), 1)
+
+
+def bfq_gated_checkpoint(preact, act=BFQ_ACT_SILU, h=None, q=None, scales=None,
+                         layout=BFQ_SCALES_ROW_MAJOR, scale_ld=None, q_eps=DEFAULT_EPS,
+                         scale_fmt=BFQ_SCALE_FP32, ckpt=None, ckpt_scales=None, live_rows=None,
+                         stream=None) -> int:
+    """From preact = (g, u) bf16 [M, 2F]: act(g) * u as h (bf16 [M, F]) and / or codes q [M, F] with
+    scales, and preact in 8 bits as ckpt (codes [M, 2F]) with ckpt_scales (fp32 [M, 2F/128]).
+    live_rows: int32 tensor of one element, the rows that exist (None: all)."""
+    M, F2 = _shape2(preact, "preact")
+    F = F2 // 2
+    _rows(preact, "preact", ("bfloat16",), M, 2 * F)
+    if h is not None:
+        _rows(h, "h", ("bfloat16",), M, F)
+    if (ckpt is None) != (ckpt_scales is None):
+        raise BfqArgumentError("ckpt and ckpt_scales go together")
+    if ckpt is not None:
+        _rows(ckpt, "ckpt", CODE_DTYPES, M, 2 * F)
+        _rows(ckpt_scales, "ckpt_scales", ("float32",), M, 2 * F // 128)
+    _live_rows(live_rows)
+    qt, scale_ld = _codes_out(q, scales, layout, scale_ld, M, F)
+    _devices(preact=preact, h=h, q=q, scales=scales, ckpt=ckpt, ckpt_scales=ckpt_scales,
+             live_rows=live_rows)
+    st = lib.bfq_gated_checkpoint(_ptr(preact), act, _ptr(h), _ptr(q), qt, _ptr(scales), layout, scale_ld,
+                                  q_eps, scale_fmt, _ptr(ckpt),
+                                  _qdtype(ckpt) if ckpt is not None else BFQ_E4M3FN, _ptr(ckpt_scales),
+                                  _ptr(live_rows), M, F, _stream(stream))
+    return _check(st, "bfq_gated_checkpoint")
+
+
+def bfq_gated_checkpoint_backward(ckpt, ckpt_scales, dh, act=BFQ_ACT_SILU, dpre=None, q=None,
+                                  scales=None, layout=BFQ_SCALES_ROW_MAJOR, scale_ld=None,
+                                  q_eps=DEFAULT_EPS, scale_fmt=BFQ_SCALE_FP32, h=None, live_rows=None,
+                                  stream=None) -> int:
+    """bfq_gated_backward from the 8-bit checkpoint ckpt [M, 2F] with ckpt_scales [M, 2F/128]: for dh
+    bf16 [M, F], dpre (bf16 [M, 2F]) and / or codes q [M, 2F] with scales; h (bf16 [M, F]) receives the
+    product again."""
+    M, F = _shape2(dh, "dh")
+    _rows(ckpt, "ckpt", CODE_DTYPES, M, 2 * F)
+    _rows(ckpt_scales, "ckpt_scales", ("float32",), M, 2 * F // 128)
+    _rows(dh, "dh", ("bfloat16",), M, F)
+    if dpre is not None:
+        _rows(dpre, "dpre", ("bfloat16",), M, 2 * F)
+    if h is not None:
+        _rows(h, "h", ("bfloat16",), M, F)
+    _live_rows(live_rows)
+    qt, scale_ld = _codes_out(q, scales, layout, scale_ld, M, 2 * F)
+    _devices(ckpt=ckpt, ckpt_scales=ckpt_scales, dh=dh, dpre=dpre, q=q, scales=scales, h=h,
+             live_rows=live_rows)
+    st = lib.bfq_gated_checkpoint_backward(_ptr(ckpt), _qdtype(ckpt), _ptr(ckpt_scales), _ptr(dh), act,
+                                           _ptr(dpre), _ptr(q), qt, _ptr(scales), layout, scale_ld, q_eps,
+                                           scale_fmt, _ptr(h), _ptr(live_rows), M, F, _stream(stream))
+    return _check(st, "bfq_gated_checkpoint_backward")
 
 
 # ------------------------------------------------------------ allocating conveniences

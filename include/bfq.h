@@ -128,6 +128,14 @@ typedef enum {
     BFQ_GATE_INT32_RANGE_ = 0x7FFFFFFF
 } bfq_gate_kind;
 
+/* A router's score function. SOFTMAX: over the token's experts. SIGMOID: each expert by itself. */
+typedef enum {
+    BFQ_SCORE_SOFTMAX = 0,
+    BFQ_SCORE_SIGMOID = 1,
+    BFQ_SCORE_INT32_MIN_ = -0x7FFFFFFF - 1,
+    BFQ_SCORE_INT32_RANGE_ = 0x7FFFFFFF
+} bfq_score;
+
 /* One launch configuration of the block GEMM ([CONFIG] §2: per-M launch parameters).
  *   variant 0 "standard": bm x bn output tile per workgroup, A and W tiles staged through
  *             LDS (double-buffered), waves_m x waves_n waves, group_m = grouped tile order.
@@ -458,6 +466,130 @@ bfq_status bfq_norm_residual_backward(const void* y, const void* res_out, bfq_dt
                                       void* d_res, void* d_y, float* d_w_pre, float* d_w_post,
                                       void* d_gate, int64_t M, int64_t K, void* workspace,
                                       size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------ MoE layer around the grouped GEMM ----
+ * Forward: bfq_moe_route picks each token's experts and weights, bfq_moe_sort groups the pairs,
+ * bfq_moe_block_gemm gathers the tokens itself, or bfq_moe_dispatch lays their rows out in expert
+ * order (what an exchange between GPUs sends; bfq_moe_block_gemm then takes them with topk 1 and
+ * sorted_pairs 0, 1, 2, ..), bfq_gated_checkpoint forms the product between the experts' two GEMMs,
+ * and bfq_moe_combine brings their rows back to the tokens. Backward: bfq_moe_combine_backward,
+ * bfq_moe_block_gemm with the transposed weights (bfq_transpose_weights on [E * N][K] transposes the
+ * whole stack, not each expert: transpose them one by one), bfq_gated_checkpoint_backward, and
+ * bfq_moe_combine without weights, which is the dispatch's gradient; bfq_moe_route_backward takes the
+ * weights' gradient to the logits.
+ *
+ * Pairs are q = t*topk + j as above, 0 <= T < 2^22 and 1 <= topk <= 64 (the sort: any with T * topk <
+ * 2^31). Rows tensors hold R rows, in expert order (pair_rows given) or in pair order (R = T*topk).
+ * A pair without a row (pair_rows[q] outside [0, R), or in pair order an id outside [0, E)) is left
+ * out: it adds nothing, whatever its weight, and its row is neither read nor written. In what is
+ * written, each row is some pair's at most once, as bfq_moe_sort's places are; where two pairs share
+ * one, its contents are those of either, mixed. K a positive multiple of 8, of 128 where codes are
+ * read or written, at most 2^23. */
+
+/* Router: s = score(logits) over a token's E experts, the topk largest keys in descending order
+ * (ties: the lowest index first), and their weights
+ *   w_j = weight_scale * s_j / (renorm ? sum_k s_k + 1e-20 : 1).
+ * The key of an expert is its logit; with a bias ([E], which moves the choice and not the weights) or
+ * n_groups > 1 it is s (+ bias), formed in 64 bits. With groups (n_groups of E / n_groups neighbouring
+ * experts) only the topk_groups groups with the largest sum of their two largest keys take part (ties:
+ * the lowest group). A logit of -inf masks an expert, as does a key of -inf: it is never taken, and
+ * where fewer than topk are left (in the groups that take part) the last ids are -1 with weight 0. A
+ * logit of +inf counts as the largest finite value; a NaN counts as larger than any key.
+ *   logits [T][E] BF16 | FP16 | FP32; topk_ids [T][topk] int32; topk_weights [T][topk] fp32.
+ * 1 <= E <= 1023, topk <= min(E, 64, the experts of topk_groups groups), n_groups <= 64. */
+bfq_status bfq_moe_route(const void* logits, bfq_dtype logits_dtype, const float* bias, int64_t T,
+                         int32_t E, int32_t topk, bfq_score score, int32_t n_groups,
+                         int32_t topk_groups, int32_t renorm, float weight_scale, int32_t* topk_ids,
+                         float* topk_weights, void* stream);
+
+/* Gradient of the weights at the logits, for the ids that were chosen: d_logits [T][E] of
+ * logits_dtype, overwritten. Ids outside [0, E) have no weight and no gradient; an id that occurs
+ * twice collects both. Sums are fp32 in a fixed order. */
+bfq_status bfq_moe_route_backward(const void* logits, bfq_dtype logits_dtype, const int32_t* topk_ids,
+                                  const float* d_weights, int64_t T, int32_t E, int32_t topk,
+                                  bfq_score score, int32_t renorm, float weight_scale, void* d_logits,
+                                  void* stream);
+
+/* The outputs of bfq_moe_align, and the places of the pairs: pair_rows [T][topk] int32 is the
+ * position of pair q in sorted_pairs, its row in expert order, or -1 for an id outside [0, E).
+ * sorted_pairs holds T*topk entries. workspace of bfq_moe_sort_workspace_bytes bytes, NULL when that
+ * is 0 (up to 1024 pairs, which take one launch). */
+size_t     bfq_moe_sort_workspace_bytes(int64_t T, int32_t topk, int32_t E);
+bfq_status bfq_moe_sort(const int32_t* topk_ids, int64_t T, int32_t topk, int32_t E,
+                        int32_t* expert_offsets, int32_t* sorted_pairs, int32_t* pair_rows,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Tokens' rows laid out in expert order: row pair_rows[t*topk + j] of the outputs is row t of x.
+ *   x_dtype BF16: x [T][K]; rows [R][K] bf16 receives the rows, and / or q [R][K] their codes with
+ *   scales, exactly as bfq_quant_tokens would write them for these rows (group_size 128; layout,
+ *   scale_ld, q_eps and scale_fmt over the R rows); x_scales NULL.
+ *   x_dtype E4M3FN | INT8: x [T][K] codes with x_scales (x_layout, x_scale_ld over the T tokens), copied
+ *   to q (q_dtype the same) and scales in `layout`; packed words stay packed words (both layouts
+ *   packed, scale_fmt BFQ_SCALE_UE8M0); rows NULL.
+ * Rows without a pair are left as they were (packed words also in rows R .. round_up(R, 4) - 1: 0). */
+bfq_status bfq_moe_dispatch(const void* x, bfq_dtype x_dtype, const float* x_scales,
+                            bfq_scale_layout x_layout, int64_t x_scale_ld, const int32_t* pair_rows,
+                            void* rows, void* q, bfq_dtype q_dtype, float* scales,
+                            bfq_scale_layout layout, int64_t scale_ld, float q_eps,
+                            bfq_scale_format scale_fmt, int64_t T, int32_t topk, int64_t K, int64_t R,
+                            void* stream);
+
+/* Experts' rows back to their tokens:
+ *   out[t] = base[t] + sum_j weights[t][j] * rows[row of pair (t, j)]
+ * in fp32, added in pair order, rounded once. rows [R][K] BF16 | FP16 | FP32; weights [T][topk] fp32,
+ * NULL for ones; out [T][K] BF16 | FP16 | FP32, base of the same type, NULL for zeros (may be out
+ * itself). pair_rows [T][topk] (rows in expert order), or NULL (pair order); there topk_ids [T][topk]
+ * with E names the pairs that have a row, NULL: all of them.
+ * ckpt: codes [R][K] (ckpt_dtype E4M3FN | INT8) with ckpt_scales fp32 [R][K/128], the rows' 8-bit
+ * checkpoint for bfq_moe_combine_backward, as bfq_quant_tokens would write it (with floor q_eps; of
+ * FP16 and FP32 rows in the same way); both NULL without. Rows without a pair stay as they were. */
+bfq_status bfq_moe_combine(const void* rows, bfq_dtype rows_dtype, const float* weights,
+                           const int32_t* pair_rows, const int32_t* topk_ids, int32_t E,
+                           const void* base, void* out, bfq_dtype out_dtype, void* ckpt,
+                           bfq_dtype ckpt_dtype, float* ckpt_scales, float q_eps, int64_t T,
+                           int32_t topk, int64_t K, int64_t R, void* stream);
+
+/* Gradients of bfq_moe_combine for dout [T][K] BF16 | FP32 (the base's gradient is dout itself):
+ *   d_rows[row of pair (t, j)] = weights[t][j] * dout[t], as d_rows bf16 [R][K] and / or codes q [R][K]
+ *   with scales (formats of bfq_quant_tokens over R rows, from the fp32 products); rows without a pair
+ *   are left as they were (packed words also in rows R .. round_up(R, 4) - 1: 0).
+ *   d_weights fp32 [T][topk]: sum over K of dout[t] * rows[..], 0 without a row; needs rows [R][K] as
+ *   BF16 | FP16 | FP32, or as codes E4M3FN | INT8 with rows_scales fp32 [R][K/128].
+ * Any output may be NULL, not all; rows NULL without d_weights. Sums are fp32 in a fixed order. */
+bfq_status bfq_moe_combine_backward(const void* dout, bfq_dtype dout_dtype, const float* weights,
+                                    const void* rows, bfq_dtype rows_dtype, const float* rows_scales,
+                                    const int32_t* pair_rows, const int32_t* topk_ids, int32_t E,
+                                    void* d_rows, void* q, bfq_dtype q_dtype, float* scales,
+                                    bfq_scale_layout layout, int64_t scale_ld, float q_eps,
+                                    bfq_scale_format scale_fmt, float* d_weights, int64_t T,
+                                    int32_t topk, int64_t K, int64_t R, void* stream);
+
+/* ---------------------------------------- 8-bit checkpoints of a gated product ----
+ * From pre-activations preact bf16 [M][2F] = (g, u) (a 2F-wide bfq_block_gemm or bfq_moe_block_gemm,
+ * or bfq_gated_gemm's preact): h = act(g) * u in fp32, as h bf16 [M][F] and / or codes q [M][F] with
+ * scales (formats of bfq_quant_tokens), and the checkpoint that a backward pass keeps in place of
+ * preact: ckpt codes [M][2F] (ckpt_dtype E4M3FN | INT8) with ckpt_scales fp32 [M][2F/128], the codes
+ * of bfq_quant_tokens with fp32 scales. Half the bytes of preact; a value is off by at most half a
+ * step of its code (e4m3: 2^-4 of itself, int8: 1/254 of its group's largest). Any output may be
+ * NULL, not all. live_rows (device, one int32, or NULL for M): rows from *live_rows on are neither
+ * read nor written, for instance expert_offsets + E with rows in expert order. F a positive multiple
+ * of 128 below 2^26, M < 2^24 - 4; q_eps floors the scales of both. */
+bfq_status bfq_gated_checkpoint(const void* preact, bfq_activation act, void* h, void* q,
+                                bfq_dtype q_dtype, float* scales, bfq_scale_layout layout,
+                                int64_t scale_ld, float q_eps, bfq_scale_format scale_fmt, void* ckpt,
+                                bfq_dtype ckpt_dtype, float* ckpt_scales, const int32_t* live_rows,
+                                int64_t M, int64_t F, void* stream);
+
+/* bfq_gated_backward from the checkpoint: with (g, u) = codes times scales, dg = dh * u * act'(g) and
+ * du = dh * act(g) in fp32, as dpre bf16 [M][2F] and / or codes q [M][2F] with scales; h bf16 [M][F],
+ * the product of the checkpoint's values. dh bf16 [M][F] (h may be dh itself). Any output may be NULL,
+ * not all. */
+bfq_status bfq_gated_checkpoint_backward(const void* ckpt, bfq_dtype ckpt_dtype,
+                                         const float* ckpt_scales, const void* dh, bfq_activation act,
+                                         void* dpre, void* q, bfq_dtype q_dtype, float* scales,
+                                         bfq_scale_layout layout, int64_t scale_ld, float q_eps,
+                                         bfq_scale_format scale_fmt, void* h, const int32_t* live_rows,
+                                         int64_t M, int64_t F, void* stream);
 
 const char* bfq_status_string(bfq_status s);
 const char* bfq_last_error(void);
