@@ -1407,3 +1407,156 @@ def norm_residual_backward(res_out, y=None, w_post=None, gate=None, gate_kind=BF
                                d_normed=d_normed, d_res_out=d_res_out, workspace=ws, stream=stream,
                                **g)
     return g
+
+
+@_under_stream
+def moe_route(logits, topk, bias=None, score=BFQ_SCORE_SOFTMAX, n_groups=1, topk_groups=1,
+              renorm=False, weight_scale=1.0, stream=None):
+    """Allocate and run bfq_moe_route: (topk_ids int32 [T, topk], topk_weights fp32 [T, topk])."""
+    import torch
+    T, dev = logits.shape[0], logits.device
+    ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
+    w = torch.empty((T, topk), dtype=torch.float32, device=dev)
+    bfq_moe_route(logits, ids, w, bias=bias, score=score, n_groups=n_groups, topk_groups=topk_groups,
+                  renorm=renorm, weight_scale=weight_scale, stream=stream)
+    return ids, w
+
+
+@_under_stream
+def moe_route_backward(logits, topk_ids, d_weights, score=BFQ_SCORE_SOFTMAX, renorm=False,
+                       weight_scale=1.0, stream=None):
+    """Allocate and run bfq_moe_route_backward: the gradient at the logits, in their dtype."""
+    import torch
+    d = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    bfq_moe_route_backward(logits, topk_ids, d_weights, d, score=score, renorm=renorm,
+                           weight_scale=weight_scale, stream=stream)
+    return d
+
+
+@_under_stream
+def moe_sort(topk_ids, E, stream=None):
+    """Allocate and run bfq_moe_sort: (expert_offsets int32 [E+1], sorted_pairs int32 [T*topk],
+    pair_rows int32 [T, topk])."""
+    import torch
+    T, topk = topk_ids.shape
+    dev = topk_ids.device
+    off = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    srt = torch.empty(T * topk, dtype=torch.int32, device=dev)
+    places = torch.empty((T, topk), dtype=torch.int32, device=dev)
+    n = bfq_moe_sort_workspace_bytes(T, topk, E)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    bfq_moe_sort(topk_ids, E, off, srt, places, workspace=ws, stream=stream)
+    return off, srt, places
+
+
+def _code_dtype(q_dtype):
+    import torch
+    return torch.uint8 if q_dtype == BFQ_E4M3FN else torch.int8
+
+
+@_under_stream
+def moe_dispatch(x, pair_rows, R=None, codes=False, x_scales=None, x_layout=BFQ_SCALES_ROW_MAJOR,
+                 layout=BFQ_SCALES_ROW_MAJOR, q_dtype=BFQ_E4M3FN, scale_fmt=BFQ_SCALE_FP32, stream=None):
+    """Allocate R rows (default: one a pair) and run bfq_moe_dispatch. Returns bf16 rows, or (codes,
+    scales) with `codes` or with x_scales (x then holds codes). Rows without a pair hold anything."""
+    import torch
+    T, K = x.shape
+    R = pair_rows.numel() if R is None else R
+    if not codes and x_scales is None:
+        rows = torch.empty((R, K), dtype=torch.bfloat16, device=x.device)
+        bfq_moe_dispatch(x, pair_rows, rows=rows, stream=stream)
+        return rows
+    q = torch.empty((R, K), dtype=_code_dtype(q_dtype) if x_scales is None else x.dtype, device=x.device)
+    scales = _alloc_scales(R, K // 128, layout, x.device)
+    bfq_moe_dispatch(x, pair_rows, q=q, scales=scales, x_scales=x_scales, x_layout=x_layout,
+                     layout=layout, scale_fmt=scale_fmt, stream=stream)
+    return q, scales
+
+
+@_under_stream
+def moe_combine(rows, topk, weights=None, pair_rows=None, topk_ids=None, E=0, base=None,
+                out_dtype=None, ckpt_dtype=None, stream=None):
+    """Allocate out [T, K] (out_dtype: base's, else rows' by default) and run bfq_moe_combine.
+    Returns out, with ckpt_dtype (BFQ_E4M3FN, BFQ_INT8) followed by the rows' codes and scales."""
+    import torch
+    R, K = rows.shape
+    T = R // topk if pair_rows is None else pair_rows.shape[0]
+    dev = rows.device
+    out = torch.empty((T, K), dtype=out_dtype or (rows if base is None else base).dtype, device=dev)
+    ckpt = scales = None
+    if ckpt_dtype is not None:
+        ckpt = torch.empty((R, K), dtype=_code_dtype(ckpt_dtype), device=dev)
+        scales = torch.empty((R, K // 128), dtype=torch.float32, device=dev)
+    bfq_moe_combine(rows, out, topk, weights=weights, pair_rows=pair_rows, topk_ids=topk_ids, E=E,
+                    base=base, ckpt=ckpt, ckpt_scales=scales, stream=stream)
+    return out if ckpt is None else (out, ckpt, scales)
+
+
+@_under_stream
+def moe_combine_backward(dout, topk, weights=None, rows=None, rows_scales=None, pair_rows=None,
+                         topk_ids=None, E=0, R=None, codes=False, layout=BFQ_SCALES_ROW_MAJOR,
+                         q_dtype=BFQ_E4M3FN, scale_fmt=BFQ_SCALE_FP32, stream=None) -> dict:
+    """Allocate and run bfq_moe_combine_backward. Returns {"d_rows"}, or {"q", "scales"} with `codes`,
+    of R rows (default: rows' or one a pair), and "d_weights" with rows."""
+    import torch
+    T, K = dout.shape
+    dev = dout.device
+    if R is None:
+        R = T * topk if rows is None else rows.shape[0]
+    g = {}
+    if codes:
+        g["q"] = torch.empty((R, K), dtype=_code_dtype(q_dtype), device=dev)
+        g["scales"] = _alloc_scales(R, K // 128, layout, dev)
+    else:
+        g["d_rows"] = torch.empty((R, K), dtype=torch.bfloat16, device=dev)
+    if rows is not None:
+        g["d_weights"] = torch.empty((T, topk), dtype=torch.float32, device=dev)
+    bfq_moe_combine_backward(dout, topk, weights=weights, rows=rows, rows_scales=rows_scales,
+                             pair_rows=pair_rows, topk_ids=topk_ids, E=E, layout=layout,
+                             scale_fmt=scale_fmt, stream=stream, **g)
+    return g
+
+
+@_under_stream
+def gated_checkpoint(preact, act=BFQ_ACT_SILU, codes=False, ckpt_dtype=BFQ_E4M3FN,
+                     layout=BFQ_SCALES_ROW_MAJOR, q_dtype=BFQ_E4M3FN, scale_fmt=BFQ_SCALE_FP32,
+                     live_rows=None, stream=None):
+    """Allocate and run bfq_gated_checkpoint. Returns (h, ckpt, ckpt_scales), or with `codes`
+    (q, scales, ckpt, ckpt_scales)."""
+    import torch
+    M, F2 = preact.shape
+    F, dev = F2 // 2, preact.device
+    h = q = scales = None
+    if codes:
+        q = torch.empty((M, F), dtype=_code_dtype(q_dtype), device=dev)
+        scales = _alloc_scales(M, F // 128, layout, dev)
+    else:
+        h = torch.empty((M, F), dtype=torch.bfloat16, device=dev)
+    ckpt = torch.empty((M, F2), dtype=_code_dtype(ckpt_dtype), device=dev)
+    cs = torch.empty((M, F2 // 128), dtype=torch.float32, device=dev)
+    bfq_gated_checkpoint(preact, act=act, h=h, q=q, scales=scales, layout=layout, scale_fmt=scale_fmt,
+                         ckpt=ckpt, ckpt_scales=cs, live_rows=live_rows, stream=stream)
+    return ((q, scales) if codes else (h,)) + (ckpt, cs)
+
+
+@_under_stream
+def gated_checkpoint_backward(ckpt, ckpt_scales, dh, act=BFQ_ACT_SILU, codes=False, want_h=False,
+                              layout=BFQ_SCALES_ROW_MAJOR, q_dtype=BFQ_E4M3FN,
+                              scale_fmt=BFQ_SCALE_FP32, live_rows=None, stream=None):
+    """Allocate and run bfq_gated_checkpoint_backward. Returns dpre (bf16), or (codes, scales) with
+    `codes`; with want_h followed by the product act(g) * u."""
+    import torch
+    M, F = dh.shape
+    dev = dh.device
+    q = scales = dpre = None
+    if codes:
+        q = torch.empty((M, 2 * F), dtype=_code_dtype(q_dtype), device=dev)
+        scales = _alloc_scales(M, 2 * F // 128, layout, dev)
+    else:
+        dpre = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dev)
+    h = torch.empty((M, F), dtype=torch.bfloat16, device=dev) if want_h else None
+    bfq_gated_checkpoint_backward(ckpt, ckpt_scales, dh, act=act, dpre=dpre, q=q, scales=scales,
+                                  layout=layout, scale_fmt=scale_fmt, h=h, live_rows=live_rows,
+                                  stream=stream)
+    res = ((q, scales) if codes else (dpre,)) + ((h,) if want_h else ())
+    return res if len(res) > 1 else dpre
