@@ -11,7 +11,7 @@ kernel and scales each by what the same counter reads for a plain device copy of
 (bytes moved by the copy / counter reading), so the result is HBM bytes per launch. It also
 records a hash of the kernel sources, so bench.py can tell whether the counters still
 describe the current kernel. `stats` stamps its summary with the same hash, or (--feed-forward) with
-one that covers the feed-forward operators' kernels as well.
+one that covers the kernels of the feed-forward operators and the mixture-of-experts layer as well.
 """
 from __future__ import annotations
 
@@ -25,9 +25,11 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 KERNEL_SOURCES = ("csrc/gemm_std.hip", "csrc/gemm_swapab.hip", "csrc/quant.hip",
                   "csrc/moe.hip", "csrc/device_common.h", "csrc/gemm_std_tile.h",
                   "csrc/gemm_swapab_body.h", "csrc/quant_device.h")
-# the feed-forward operators' kernels, beside the routines above that they share
+# the kernels of the feed-forward operators and of the mixture-of-experts layer, beside the routines
+# above that they share
 FEED_FORWARD_SOURCES = KERNEL_SOURCES + ("csrc/gated.hip", "csrc/norm.hip", "csrc/activation.h",
-                                         "csrc/bfq_internal.h")
+                                         "csrc/bfq_internal.h", "csrc/route.hip", "csrc/moe_rows.hip",
+                                         "csrc/checkpoint.hip", "csrc/row_access.h", "csrc/moe_layer.h")
 
 
 def source_hash(sources=KERNEL_SOURCES) -> str:
