@@ -51,8 +51,8 @@ typedef enum {
     BFQ_ERR_ARG = -9            /* invalid scalar argument (eps, enum value, index) */
 } bfq_status;
 
-/* The *_INT32_RANGE_ enumerators below are not values of their enums: they make each enum a
- * 32-bit type in which every int32 is representable, so that an out-of-range argument from a
+/* The *_INT32_MIN_ and *_INT32_RANGE_ enumerators below are not values of their enums: they make each
+ * enum a 32-bit type in which every int32 is representable, so that an out-of-range argument from a
  * C or ctypes caller is rejected (BFQ_ERR_ARG / BFQ_ERR_DTYPE) rather than undefined. */
 typedef enum {
     BFQ_BF16 = 0,
@@ -61,6 +61,7 @@ typedef enum {
     BFQ_E4M3FN = 3,   /* OCP float8 e4m3fn, max 448 */
     BFQ_INT8 = 4,     /* symmetric int8 in [-127, 127] */
     BFQ_INT32 = 5,
+    BFQ_DTYPE_INT32_MIN_ = -0x7FFFFFFF - 1,
     BFQ_DTYPE_INT32_RANGE_ = 0x7FFFFFFF  /* not a dtype: see below */
 } bfq_dtype;
 
@@ -78,6 +79,7 @@ typedef enum {
     BFQ_SCALES_ROW_MAJOR = 0,    /* s[m * ld + g], ld >= K/128 */
     BFQ_SCALES_COL_MAJOR = 1,    /* s[g * ld + m], ld >= M     */
     BFQ_SCALES_PACKED_UE8M0 = 2, /* words[w * ld + m], see above */
+    BFQ_SCALES_INT32_MIN_ = -0x7FFFFFFF - 1,
     BFQ_SCALES_INT32_RANGE_ = 0x7FFFFFFF
 } bfq_scale_layout;
 
@@ -93,6 +95,7 @@ typedef enum {
 typedef enum {
     BFQ_W_ROW_MAJOR = 0,
     BFQ_W_PACKED16 = 1,
+    BFQ_W_INT32_MIN_ = -0x7FFFFFFF - 1,
     BFQ_W_INT32_RANGE_ = 0x7FFFFFFF
 } bfq_weight_layout;
 
@@ -105,6 +108,7 @@ typedef enum {
 typedef enum {
     BFQ_SCALE_FP32 = 0,
     BFQ_SCALE_UE8M0 = 1,
+    BFQ_SCALE_INT32_MIN_ = -0x7FFFFFFF - 1,
     BFQ_SCALE_INT32_RANGE_ = 0x7FFFFFFF
 } bfq_scale_format;
 
@@ -113,7 +117,7 @@ typedef enum {
 typedef enum {
     BFQ_ACT_SILU = 0,
     BFQ_ACT_GELU_TANH = 1,
-    BFQ_ACT_INT32_MIN_ = -0x7FFFFFFF - 1,   /* every int32 is representable, as above */
+    BFQ_ACT_INT32_MIN_ = -0x7FFFFFFF - 1,
     BFQ_ACT_INT32_RANGE_ = 0x7FFFFFFF
 } bfq_activation;
 
