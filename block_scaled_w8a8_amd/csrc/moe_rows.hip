@@ -14,13 +14,14 @@
 namespace bfq {
 
 // ------------------------------------------------------------------------- sort ----
-// A stable counting sort in two launches: a histogram a workgroup, then every workgroup adds up what
-// lies before it (at most 256 histograms of E + 1 counts, from L2) and places its pairs. One
-// workgroup (1024 pairs or fewer) needs no first launch. Against counting, a scan in a workgroup of
-// its own and the placing, as three launches, one less round trip through the queue; a decode
-// step's pairs take one launch in place of three.
+// A stable counting sort. Every workgroup places its share of the pairs; what lies before them in other
+// shares it takes from the histograms of an earlier launch (at most 256 of E + 1 counts, from L2), or, up
+// to kSortAlone pairs, counts itself: reading all ids again costs less than a launch. Latency bounds it:
+// 6216 pairs 5.4 us in one launch, 65536 pairs of 256 experts 8.9 us in two (32768: 9.3 in one, and more
+// where a router has collapsed onto one expert, whose counts follow one another).
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kSortGroups = 256;
+constexpr int64_t kSortAlone = 8192;
 
 __device__ __forceinline__ int sort_bucket(int32_t id, int E) { return (uint32_t)id < (uint32_t)E ? id : E; }
 
@@ -34,6 +35,25 @@ static int64_t sort_groups(int64_t pairs) {
     return share > 0 ? (pairs + share - 1) / share : 0;
 }
 
+// Inclusive prefix over the wave, through DPP (row_shr within 16 lanes, row_bcast across them).
+__device__ __forceinline__ int32_t wave_prefix(int32_t x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);
+    return x + __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
+}
+
+// Counts a wave's buckets in LDS. Additions to one address follow one another, so the pairs of no expert
+// here, most of them where several GPUs share the experts, are one addition (6216 pairs, three quarters of
+// them elsewhere: 8.0 -> 5.4 us).
+__device__ __forceinline__ void count_buckets(int32_t* hist, bool in, int b, int E) {
+    const uint64_t none = __ballot(in && b == E);
+    if (in && b < E) atomicAdd(&hist[b], 1);
+    else if (in && __builtin_ctzll(none) == (threadIdx.x & 63)) atomicAdd(&hist[E], __builtin_popcountll(none));
+}
+
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const int32_t* __restrict__ ids, int64_t pairs,
                                                                   int64_t share, int E,
                                                                   int32_t* __restrict__ counts) {
@@ -41,7 +61,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const int32_t*
     for (int b = threadIdx.x; b <= E; b += kSortThreads) hist[b] = 0;
     __syncthreads();
     const int64_t lo = blockIdx.x * share, hi = lo + share < pairs ? lo + share : pairs;
-    for (int64_t q = lo + threadIdx.x; q < hi; q += kSortThreads) atomicAdd(&hist[sort_bucket(ids[q], E)], 1);
+    for (int64_t q0 = lo; q0 < hi; q0 += kSortThreads) {
+        const int64_t q = q0 + threadIdx.x;
+        count_buckets(hist, q < hi, q < hi ? sort_bucket(ids[q], E) : 0, E);
+    }
     __syncthreads();
     for (int b = threadIdx.x; b <= E; b += kSortThreads) counts[(int64_t)blockIdx.x * (E + 1) + b] = hist[b];
 }
@@ -52,19 +75,28 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t*
                                                                   int32_t* __restrict__ offsets,
                                                                   int32_t* __restrict__ sorted,
                                                                   int32_t* __restrict__ pair_rows) {
-    __shared__ int32_t base[1024], sums[kSortWaves];
+    __shared__ int32_t base[1024], prior[1024], sums[kSortWaves];
     __shared__ uint16_t wave_counts[kSortWaves][1024];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, B = E + 1, G = gridDim.x, g = blockIdx.x;
     const int64_t lo = g * share, hi = lo + share < pairs ? lo + share : pairs;
-    // pairs of bucket `tid` in all, and in earlier workgroups
+    // pairs of bucket `tid` in all, and in earlier shares
     int32_t total = 0, before = 0;
-    if (G == 1) {
-        if (tid < B) base[tid] = 0;
+    if (!counts) {
+        base[tid] = prior[tid] = 0;
         __syncthreads();
-        for (int64_t q = lo + tid; q < hi; q += kSortThreads) atomicAdd(&base[sort_bucket(ids[q], E)], 1);
+        constexpr int rounds = kSortAlone / kSortThreads;
+        const int n = (int)pairs;
+        int id[rounds];                                  // loads in flight together
+#pragma unroll
+        for (int i = 0; i < rounds; ++i) id[i] = ids[min(i * kSortThreads + tid, n - 1)];
+#pragma unroll
+        for (int i = 0; i < rounds; ++i)                 // a round lies within a share
+            count_buckets(i * kSortThreads < lo ? prior : base, i * kSortThreads + tid < n, sort_bucket(id[i], E), E);
         __syncthreads();
-        if (tid < B) total = base[tid];
+        before = prior[tid];
+        total = before + base[tid];
     } else if (tid < B) {
+#pragma unroll 8
         for (int i = 0; i < G; ++i) {
             const int32_t c = counts[(int64_t)i * B + tid];
             before += i < g ? c : 0;
@@ -72,16 +104,11 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t*
         }
     }
     // exclusive prefix over the buckets
-    int32_t inc = total;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int32_t v = __shfl_up(inc, d, 64);
-        if (lane >= d) inc += v;
-    }
+    const int32_t inc = wave_prefix(total);
     if (lane == 63) sums[wave] = inc;
     __syncthreads();
-    int32_t first = inc - total;
-    for (int w = 0; w < wave; ++w) first += sums[w];
+    const int32_t earlier = __builtin_amdgcn_readlane(wave_prefix(lane < wave ? sums[lane] : 0), 63);
+    const int32_t first = earlier + inc - total;
     if (tid < B) {
         base[tid] = first + before;
         if (g == 0) offsets[tid] = first;
@@ -98,9 +125,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t*
             const uint64_t bit = __ballot((b >> k) & 1);
             same &= (b >> k) & 1 ? bit : ~bit;
         }
-        for (int i = tid; i < kSortWaves * 1024 / 2; i += kSortThreads)
-            reinterpret_cast<uint32_t*>(&wave_counts[0][0])[i] = 0;
-        __syncthreads();
+        for (int i = lane; 2 * i < B; i += 64) reinterpret_cast<uint32_t*>(wave_counts[wave])[i] = 0;   // its own
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
         const int rank = __builtin_popcountll(same & below);
         if (in && rank == 0) wave_counts[wave][b] = (uint16_t)__builtin_popcountll(same);
         __syncthreads();
@@ -131,7 +157,7 @@ __global__ __launch_bounds__(1024) void sort_empty_kernel(int E, int32_t* __rest
 
 size_t moe_sort_workspace_bytes(int64_t pairs, int E) {
     const int64_t G = sort_groups(pairs);
-    return G > 1 ? (size_t)G * (size_t)(E + 1) * sizeof(int32_t) : 0;
+    return pairs > kSortAlone ? (size_t)G * (size_t)(E + 1) * sizeof(int32_t) : 0;
 }
 
 hipError_t launch_moe_sort(const int32_t* ids, int64_t pairs, int E, int32_t* offsets, int32_t* sorted,
@@ -141,14 +167,14 @@ hipError_t launch_moe_sort(const int32_t* ids, int64_t pairs, int E, int32_t* of
         hipLaunchKernelGGL(sort_empty_kernel, dim3(1), dim3(1024), 0, stream, E, offsets);
         return hipGetLastError();
     }
-    if (G > 1) {
+    if (pairs > kSortAlone) {
         hipLaunchKernelGGL(sort_count_kernel, dim3((unsigned)G), dim3(kSortThreads), 0, stream, ids, pairs, share, E,
                            counts);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL(sort_place_kernel, dim3((unsigned)G), dim3(kSortThreads), 0, stream, ids, pairs, share, E,
-                       counts, offsets, sorted, pair_rows);
+                       pairs > kSortAlone ? counts : nullptr, offsets, sorted, pair_rows);
     return hipGetLastError();
 }
 
@@ -195,9 +221,7 @@ __global__ __launch_bounds__(256) void dispatch_codes_kernel(DispatchArgs p) {
         unpack8(make_uint4(raw0.x, raw0.y, raw0.z, raw0.w), x);
         unpack8(make_uint4(raw1.x, raw1.y, raw1.z, raw1.w), x + 8);
         uint32_t mx = max(amax8(x), amax8(x + 8));       // NaN > Inf > finite as unsigned integers
-        mx = max(mx, dpp_u32<kDppQuadXor1>(mx));
-        mx = max(mx, dpp_u32<kDppQuadXor2>(mx));
-        mx = max(mx, dpp_u32<kDppHalfMirror>(mx));
+        mx = group_max<8>(mx);
         s = group_scale<Q>(mx, p.out.eps, p.out.ue8m0);
         const uint2 lo = encode8_group<Q>(x, mx, s), hi = encode8_group<Q>(x + 8, mx, s);
         code = v4u{lo.x, lo.y, hi.x, hi.y};
@@ -336,79 +360,144 @@ hipError_t launch_combine(const CombineArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Eight values of a row through its address (for a row that exists), S: the non-temporal hint.
+template <int S, typename V> __device__ __forceinline__ V stream_load(const void* p) {
+    if constexpr (S) return __builtin_nontemporal_load(static_cast<const V*>(p));
+    else return *static_cast<const V*>(p);
+}
+template <int S, typename V> __device__ __forceinline__ void stream_store(void* p, const V& v) {
+    if constexpr (S) __builtin_nontemporal_store(v, static_cast<V*>(p));
+    else *static_cast<V*>(p) = v;
+}
+
+// A scalar that the compiler takes for a new one: what is formed from it is formed where it stands, not
+// ahead of the loop for all rows at once, which the scalar registers have no room for.
+__device__ __forceinline__ int here(int x) {
+    asm volatile("" : "+s"(x));
+    return x;
+}
+
 // A workgroup takes a token's whole row, because the weights' gradients are sums over it; eight pairs
 // at a time, their rows in flight together. The codes of w * dout come from one maximum for all
 // pairs: rounding is monotone, so the largest |w * dout| is |w| times the largest |dout|, rounded.
+// Columns of a thread: 16 where rows of codes are read (16-byte loads and stores), else 8. A pair
+// without a row reads that of another (which is in the caches) and writes nothing: the loads of a
+// batch have no branch between them. Bytes bound it: 4096 x 7168, eight pairs, codes in and out, 543 MB
+// in 107 to 113 us (4.8 to 5.1 TB/s; a large copy 5.2). Rows through buffer resources, eight times four
+// scalar registers that spilled, 8 columns a thread: 142 us; scalar bases and 16 columns, 448 threads
+// a token: 121; at most 256 threads, two rounds a row and more tokens on a CU: 107 (192: 114, 128: 114,
+// 64: 108; batches of four pairs: 109). One size for every batch: a token's sums do not depend on T.
 template <int RK, int Q, int S>
-__global__ __launch_bounds__(512) void combine_bwd_kernel(CombineBwdArgs p) {
-    constexpr int NB = 8;
+__global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
+    constexpr int NB = 8, U = RK == R_FP8 || RK == R_INT8 ? 2 : 1, W = 8 * U, LG = 16 / U;   // lanes of a group
     typedef RowChunk<RK == R_NONE ? (int)R_BF16 : RK, S> Chunk;
+    typedef unsigned int v2u __attribute__((ext_vector_type(2)));
     const int64_t t = blockIdx.x, K = p.K, G = K / 128;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    __shared__ float part[8][NB];
+    __shared__ float part[4][NB];
     if constexpr (Q >= 0) {
         if (t >= p.T) {                                  // uniform: a padding row of packed words
             for (int64_t w = tid; w < (G + 3) / 4; w += blockDim.x) p.out.scales[w * p.out.stride_g + p.at.R + (t - p.T)] = 0.f;
             return;
         }
     }
-    const uint32_t row_bytes = (uint32_t)(K * Chunk::size);
     const int place = pair_place(p.at, t, lane);
+    const uint64_t there = __ballot(place >= 0);         // bit j: pair j has a row
     const float weight = p.weights && lane < p.at.topk ? p.weights[t * p.at.topk + lane] : 1.f;
-    const __amdgpu_buffer_rsrc_t rd = pair_row(p.dout, t, (uint32_t)(K * (p.dout_f32 ? 4 : 2)));
+    const uint32_t chunks = (uint32_t)(K / W);
     for (int j0 = 0; j0 < p.at.topk; j0 += NB) {
+        const uint32_t alive = (uint32_t)(there >> j0) & 0xFFu;
         float acc[NB];
         int r[NB];
+        // lane k of a group stores pair k's scale (taken here, where every lane of the wave takes part)
+        const int k = lane & (LG - 1), rs = __shfl(place, (j0 + k) & 63, 64);
+        const int some = alive ? __builtin_amdgcn_readlane(place, j0 + __builtin_ctz(alive)) : 0;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             acc[i] = 0.f;
-            r[i] = __builtin_amdgcn_readlane(place, (j0 + i) & 63);
+            r[i] = (alive >> i) & 1 ? __builtin_amdgcn_readlane(place, (j0 + i) & 63) : some;
         }
-        for (uint32_t c0 = 0; c0 < (uint32_t)(K / 8); c0 += blockDim.x) {
+        for (uint32_t c0 = 0; alive && c0 < chunks; c0 += blockDim.x) {
             const uint32_t c = c0 + tid;
-            const bool live = (int64_t)c * 8 < K;
-            float d[8];
-            Chunk v[NB];
+            if (c >= chunks) continue;                   // whole groups: K is a multiple of 128 with codes
+            float d[W];
+            v4u v[NB][RK == R_FP32 ? 2 : 1];
             float sv[NB];
             if constexpr (RK != R_NONE) {
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
-                    v[i].load(pair_row(p.rows, r[i], row_bytes), c);
-                    if constexpr (Chunk::codes) sv[i] = buf_f32(pair_row(p.rows_scales, r[i], (uint32_t)(4 * G)), (c >> 4) * 4, 0);
+                    const int64_t ri = here(r[i]);
+                    const uint8_t* row = static_cast<const uint8_t*>(p.rows) + ri * (K * Chunk::size);
+                    const uint32_t at = c * (W * Chunk::size);
+                    v[i][0] = stream_load<S, v4u>(row + at);
+                    if constexpr (RK == R_FP32) v[i][1] = stream_load<S, v4u>(row + at + 16);
+                    if constexpr (Chunk::codes) sv[i] = (p.rows_scales + ri * G)[c / LG];
                 }
             }
-            if (p.dout_f32) { RowChunk<R_FP32, 0> b; b.load(rd, c); b.get(d); }
-            else { RowChunk<R_BF16, 0> b; b.load(rd, c); b.get(d); }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (p.dout_f32) {
+                    const uint8_t* row = static_cast<const uint8_t*>(p.dout) + t * (4 * K);
+                    const v4f a = stream_load<0, v4f>(row + c * (4 * W) + 32 * u), b = stream_load<0, v4f>(row + c * (4 * W) + 32 * u + 16);
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) { d[8 * u + n] = a[n]; d[8 * u + 4 + n] = b[n]; }
+                } else {
+                    const v4u a = stream_load<0, v4u>(static_cast<const uint8_t*>(p.dout) + t * (2 * K) + c * (2 * W) + 16 * u);
+                    unpack8(make_uint4(a.x, a.y, a.z, a.w), d + 8 * u);
+                }
+            }
             uint32_t md = 0;
-            if constexpr (Q >= 0) md = max16(amax8(d));
+            if constexpr (Q >= 0) md = group_max<LG>(U == 2 ? max(amax8(d), amax8(d + W - 8)) : amax8(d));
             float scale = 0.f;
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
-                if (r[i] < 0) continue;                  // uniform
+                if (!((alive >> i) & 1)) continue;       // uniform
                 const float w = lane_f32(weight, (j0 + i) & 63);
+                const int64_t ri = here(r[i]);
                 if constexpr (RK != R_NONE) {
-                    float x[8], s = 0.f;
-                    v[i].get(x);
+                    float s = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) s = __builtin_fmaf(d[k], x[k], s);
+                    for (int u = 0; u < U; ++u) {
+                        float x[8];
+                        Chunk chunk;
+                        if constexpr (U == 2) chunk.a = u ? v4u{v[i][0].z, v[i][0].w, 0, 0} : v[i][0];
+                        else chunk.a = v[i][0];
+                        if constexpr (RK == R_FP32) chunk.b = v[i][1];
+                        chunk.get(x);
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) s = __builtin_fmaf(d[8 * u + n], x[n], s);
+                    }
                     acc[i] += Chunk::codes ? s * sv[i] : s;
                 }
-                float z[8];
+                float z[W];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) z[k] = w * d[k];
-                if (p.d_rows) row_store<S>(pair_row(p.d_rows, r[i], (uint32_t)(2 * K)), c, O_BF16, z);
+                for (int n = 0; n < W; ++n) z[n] = w * d[n];
+                if (p.d_rows) {
+                    uint8_t* row = static_cast<uint8_t*>(p.d_rows) + ri * (2 * K);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const uint4 b = pack8(z + 8 * u);
+                        stream_store<S>(row + c * (2 * W) + 16 * u, v4u{b.x, b.y, b.z, b.w});
+                    }
+                }
                 if constexpr (Q >= 0) {
                     uint32_t mx = __float_as_uint(w * __uint_as_float(md)) & 0x7FFFFFFFu;
-                    if (mx >= 0x7F800000u) mx = max16(amax8(z));          // the 16 lanes of a group agree
+                    if (mx >= 0x7F800000u)               // the lanes of a group agree
+                        mx = group_max<LG>(U == 2 ? max(amax8(z), amax8(z + W - 8)) : amax8(z));
                     const float s = group_scale<Q>(mx, p.out.eps, p.out.ue8m0);
-                    row_store8<S>(pair_row(p.out.q, r[i], (uint32_t)K), c * 8, encode8_group<Q>(z, mx, s));
-                    if ((lane & 15) == i) scale = s;
+                    uint8_t* row = static_cast<uint8_t*>(p.out.q) + ri * K;
+                    const uint2 lo = encode8_group<Q>(z, mx, s);
+                    if constexpr (U == 2) {
+                        const uint2 hi = encode8_group<Q>(z + W - 8, mx, s);
+                        stream_store<S>(row + c * W, v4u{lo.x, lo.y, hi.x, hi.y});
+                    } else {
+                        stream_store<S>(row + c * W, v2u{lo.x, lo.y});
+                    }
+                    if (k == i) scale = s;
                 }
             }
             if constexpr (Q >= 0) {
-                const int rs = __shfl(place, (j0 + (lane & 15)) & 63, 64);
-                if ((lane & 15) < NB && rs >= 0 && j0 + (lane & 15) < p.at.topk && live)
-                    put_scale(p.out, rs, c >> 4, G, scale);
+                if (k < NB && (alive >> k) & 1) put_scale(p.out, rs, c / LG, G, scale);
             }
         }
         if constexpr (RK != R_NONE) {
@@ -429,7 +518,7 @@ __global__ __launch_bounds__(512) void combine_bwd_kernel(CombineBwdArgs p) {
 }
 
 template <int RK, int Q> static void combine_bwd_s(const CombineBwdArgs& a, hipStream_t stream) {
-    const int64_t chunks = a.K / 8, rounds = (chunks + 511) / 512;
+    const int64_t chunks = a.K / (RK == R_FP8 || RK == R_INT8 ? 16 : 8), rounds = (chunks + 255) / 256;
     const dim3 block((unsigned)(((chunks + rounds - 1) / rounds + 63) / 64 * 64));
     const dim3 grid((unsigned)(a.T + (Q >= 0 && a.out.packed ? (4 - a.at.R % 4) % 4 : 0)));
     if (past_caches(a.at.R * a.K * ((a.d_rows ? 2 : 0) + (Q >= 0 ? 1 : 0))))

@@ -105,6 +105,14 @@ __device__ __forceinline__ void row_store(__amdgpu_buffer_rsrc_t r, uint32_t c, 
 
 __device__ __forceinline__ int type_size(int otype) { return otype == O_FP32 ? 4 : 2; }
 
+// Largest over the L (8 or 16) neighbouring lanes that hold a group, in each of them.
+template <int L> __device__ __forceinline__ uint32_t group_max(uint32_t m) {
+    m = max(m, dpp_u32<kDppQuadXor1>(m));
+    m = max(m, dpp_u32<kDppQuadXor2>(m));
+    m = max(m, dpp_u32<kDppHalfMirror>(m));
+    return L == 16 ? max(m, dpp_u32<kDppMirror>(m)) : m;
+}
+
 // One scale of group g of row m; packed: its byte of the word, and by the last group the zero bytes
 // after it.
 __device__ __forceinline__ void put_scale(const CodesOut& o, int64_t m, int64_t g, int64_t groups, float s) {

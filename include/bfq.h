@@ -517,7 +517,7 @@ bfq_status bfq_moe_route_backward(const void* logits, bfq_dtype logits_dtype, co
 /* The outputs of bfq_moe_align, and the places of the pairs: pair_rows [T][topk] int32 is the
  * position of pair q in sorted_pairs, its row in expert order, or -1 for an id outside [0, E).
  * sorted_pairs holds T*topk entries. workspace of bfq_moe_sort_workspace_bytes bytes, NULL when that
- * is 0 (up to 1024 pairs, which take one launch). */
+ * is 0 (up to 8192 pairs, which take one launch). */
 size_t     bfq_moe_sort_workspace_bytes(int64_t T, int32_t topk, int32_t E);
 bfq_status bfq_moe_sort(const int32_t* topk_ids, int64_t T, int32_t topk, int32_t E,
                         int32_t* expert_offsets, int32_t* sorted_pairs, int32_t* pair_rows,

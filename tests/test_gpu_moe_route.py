@@ -236,7 +236,7 @@ def _sorted(ids, E):
 
 
 @pytest.mark.parametrize("T,topk,E", [(1, 1, 1), (1, 8, 256), (3, 5, 1023), (128, 8, 256), (1024, 1, 7), (1025, 1, 7), (205, 5, 1),
-                                      (4096, 8, 256), (777, 8, 1023), (300000, 1, 64), (40000, 33, 1000)])
+                                      (4096, 8, 256), (777, 8, 1023), (1024, 8, 256), (1025, 8, 256), (4097, 8, 256), (300000, 1, 64), (40000, 33, 1000)])
 @pytest.mark.parametrize("kind", ["all", "some", "one"])
 def test_sort(bfq, T, topk, E, kind):
     lo, hi = {"all": (0, E), "some": (-E, 2 * E), "one": (E - 1, E)}[kind]
@@ -253,11 +253,13 @@ def test_sort(bfq, T, topk, E, kind):
 def test_sort_empty_and_guards(bfq):
     off, srt, places = bfq.moe_sort(torch.empty((0, 4), dtype=torch.int32, device=DEV), 1023)
     assert not bool(off.any()) and srt.numel() == 0 and places.shape == (0, 4)
-    ids = torch.randint(0, 5, (400, 3), generator=_gen(1), device=DEV, dtype=torch.int32)
-    off, srt, places = (torch.full((n,), 77777, dtype=torch.int32, device=DEV) for n in (5 + 1 + 2, 1200 + 2, 1200 + 2))
-    n = bfq.bfq_moe_sort_workspace_bytes(400, 3, 5)
-    ws = torch.full((n + 8,), 99, dtype=torch.uint8, device=DEV)
-    bfq.bfq_moe_sort(ids, 5, off[1:7], srt[1:1201], places[1:1201].view(400, 3), workspace=ws[4:4 + n])
-    for t in (off, srt, places):
-        assert t[0] == 77777 and t[-1] == 77777 and not bool((t[1:-1] == 77777).any())
-    assert bool((ws[:4] == 99).all()) and bool((ws[-4:] == 99).all())
+    for T in (400, 12000):                                  # in one launch, in two
+        ids = torch.randint(0, 5, (T, 3), generator=_gen(1), device=DEV, dtype=torch.int32)
+        off, srt, places = (torch.full((n,), 77777, dtype=torch.int32, device=DEV) for n in (5 + 1 + 2, 3 * T + 2, 3 * T + 2))
+        n = bfq.bfq_moe_sort_workspace_bytes(T, 3, 5)
+        assert (n > 0) == (T == 12000)
+        ws = torch.full((n + 8,), 99, dtype=torch.uint8, device=DEV)
+        bfq.bfq_moe_sort(ids, 5, off[1:7], srt[1:-1], places[1:-1].view(T, 3), workspace=ws[4:4 + n])
+        for t in (off, srt, places):
+            assert t[0] == 77777 and t[-1] == 77777 and not bool((t[1:-1] == 77777).any())
+        assert bool((ws[:4] == 99).all()) and bool((ws[-4:] == 99).all())

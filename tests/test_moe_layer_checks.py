@@ -22,7 +22,7 @@ route = _caller("bfq_moe_route", dict(logits=P, dt=2, bias=P, T=4, E=16, topk=4,
                                       renorm=1, scale=1.0, ids=P, w=P))
 route_bwd = _caller("bfq_moe_route_backward", dict(logits=P, dt=2, ids=P, dw=P, T=4, E=16, topk=4, score=0, renorm=1,
                                                    scale=1.0, dl=P))
-sort = _caller("bfq_moe_sort", dict(ids=P, T=300, topk=8, E=16, off=P, srt=P, places=P, ws=P, wsb=1 << 20))
+sort = _caller("bfq_moe_sort", dict(ids=P, T=4800, topk=8, E=16, off=P, srt=P, places=P, ws=P, wsb=1 << 20))
 dispatch = _caller("bfq_moe_dispatch", dict(x=P, xdt=0, xs=None, xl=0, xld=0, places=P, rows=None, q=P, qdt=3, s=P,
                                             layout=0, ld=2, eps=1e-10, fmt=0, T=4, topk=2, K=256, R=8))
 COPY = dict(xdt=3, xs=P, xld=2)
@@ -65,17 +65,17 @@ def test_sort_refusals(bfq):
     _refuses(E, sort, E.BFQ_ERR_NULL, *({n: None} for n in ("ids", "off", "srt", "places")))
     _refuses(E, sort, E.BFQ_ERR_SHAPE, dict(T=-1), dict(topk=0), dict(E=0), dict(E=1024), dict(T=1 << 28), dict(T=1 << 62))
     _refuses(E, sort, E.BFQ_ERR_ALIGN, *({n: P + 2} for n in ("ids", "off", "srt", "places", "ws")))
-    need = E.bfq_moe_sort_workspace_bytes(300, 8, 16)
-    assert need == 3 * 17 * 4                       # three workgroups' histograms
+    need = E.bfq_moe_sort_workspace_bytes(4800, 8, 16)
+    assert need == 38 * 17 * 4                      # 38 workgroups' histograms
     _refuses(E, sort, E.BFQ_ERR_WORKSPACE, dict(ws=None), dict(wsb=need - 1), dict(ws=None, wsb=0))
     assert sort(E, T=0, off=None) == E.BFQ_ERR_NULL   # an empty batch still writes the offsets
 
 
 def test_sort_workspace_sizes(bfq):
     w = bfq.bfq_moe_sort_workspace_bytes
-    assert w(128, 8, 256) == 0 and w(0, 8, 256) == 0 and w(-1, 8, 256) == 0 and w(5, 0, 4) == 0 and w(5, 2, 0) == 0
-    assert w(129, 8, 256) == 2 * 257 * 4
-    assert w(4096, 8, 256) == 32 * 257 * 4
+    assert w(1024, 8, 256) == 0 and w(0, 8, 256) == 0 and w(-1, 8, 256) == 0 and w(5, 0, 4) == 0 and w(5, 2, 0) == 0
+    assert w(1025, 8, 256) == 9 * 257 * 4
+    assert w(8192, 8, 256) == 64 * 257 * 4
     assert w(1 << 22, 64, 1023) == 256 * 1024 * 4     # never more than 256 workgroups
     assert w(1 << 62, 64, 1023) == 0                  # a batch that the sort refuses
 
@@ -243,7 +243,7 @@ def test_conveniences_allocate_under_the_launch_stream(bfq, monkeypatch):
     for name in g:
         monkeypatch.setattr(bfq, name, lambda *a, stream=None, **kw: log.append(("launch", bfq._stream(stream))))
     r, c, k, b = (g[n] for n in ("bfq_moe_route", "bfq_moe_combine", "bfq_gated_checkpoint", "bfq_moe_combine_backward"))
-    big = torch.zeros((300, 8), dtype=torch.int32)
+    big = torch.zeros((4800, 8), dtype=torch.int32)
     calls = [
         (2, 0, 2, lambda s: bfq.moe_route(r["logits"], 2, bias=r["bias"], stream=s)),
         (3, 0, 1, lambda s: bfq.moe_route_backward(r["logits"], r["topk_ids"], r["topk_weights"], stream=s)),
