@@ -42,15 +42,46 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t m) {
                    c = __builtin_amdgcn_readlane(m, 32), d = __builtin_amdgcn_readlane(m, 48);
     return max(max(a, b), max(c, d));
 }
-__device__ __forceinline__ uint64_t wave_max(uint64_t m) {
-    const uint32_t hi = wave_max((uint32_t)(m >> 32));
-    const uint32_t lo = wave_max((uint32_t)(m >> 32) == hi ? (uint32_t)m : 0u);
-    return ((uint64_t)hi << 32) | lo;
+// The lanes that hold the largest key of the wave, and that key. Two keys of 64 bits seldom agree in
+// their upper halves: the lower ones are compared only then.
+__device__ __forceinline__ uint64_t wave_best(uint32_t m, uint32_t& best) {
+    best = wave_max(m);
+    return __ballot(m == best);
 }
-__device__ __forceinline__ double wave_sum_f64(double x) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d, 64);
-    return x;
+__device__ __forceinline__ uint64_t wave_best(uint64_t m, uint64_t& best) {
+    const uint32_t hi = wave_max((uint32_t)(m >> 32));
+    uint64_t lanes = __ballot((uint32_t)(m >> 32) == hi);
+    uint32_t lo;
+    if (lanes & (lanes - 1)) {                           // uniform
+        lo = wave_max((uint32_t)(m >> 32) == hi ? (uint32_t)m : 0u);
+        lanes &= __ballot((uint32_t)m == lo);
+    } else {
+        lo = __builtin_amdgcn_readlane((uint32_t)m, __builtin_ctzll(lanes));
+    }
+    best = ((uint64_t)hi << 32) | lo;
+    return lanes;
+}
+
+// Sum over the wave: DPP within rows of 16 lanes, then the rows' sums as scalars.
+__device__ __forceinline__ float row_of(float x, int lane) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), lane)); }
+__device__ __forceinline__ double row_of(double x, int lane) {
+    const uint64_t u = (uint64_t)__double_as_longlong(x);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, lane), hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), lane);
+    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+template <int CTRL> __device__ __forceinline__ uint64_t dpp_u64(uint64_t x) {
+    return ((uint64_t)dpp_u32<CTRL>((uint32_t)(x >> 32)) << 32) | dpp_u32<CTRL>((uint32_t)x);
+}
+template <int CTRL> __device__ __forceinline__ float dpp_of(float x) { return dpp_f32<CTRL>(x); }
+template <int CTRL> __device__ __forceinline__ double dpp_of(double x) {
+    return __longlong_as_double((long long)dpp_u64<CTRL>((uint64_t)__double_as_longlong(x)));
+}
+template <typename R> __device__ __forceinline__ R wave_total(R x) {
+    x += dpp_of<kDppQuadXor1>(x);
+    x += dpp_of<kDppQuadXor2>(x);
+    x += dpp_of<kDppHalfMirror>(x);
+    x += dpp_of<kDppMirror>(x);
+    return (row_of(x, 0) + row_of(x, 16)) + (row_of(x, 32) + row_of(x, 48));
 }
 
 // Experts lane*V .. of a token's row; those past E count as masked. +inf counts as the largest
@@ -71,14 +102,6 @@ __device__ __forceinline__ void load_logits(const RouteArgs& p, int64_t t, int l
         }
     }
 }
-__device__ __forceinline__ float logit_at(const RouteArgs& p, int64_t i) {
-    float x;
-    if (p.otype == O_FP32) x = static_cast<const float*>(p.logits)[i];
-    else if (p.otype == O_BF16) x = bf16_lo(static_cast<const uint16_t*>(p.logits)[i]);
-    else x = (float)static_cast<const _Float16*>(p.logits)[i];
-    return x == __builtin_inff() ? 0x1.fffffep127f : x;
-}
-
 // The wave's largest logit (a NaN wins); 0 where all are masked, whose exponentials are then 0.
 template <int V> __device__ __forceinline__ float wave_top(const float* x) {
     uint32_t m = 0;
@@ -113,8 +136,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
             if constexpr (K64) s += exp((double)x[i] - top);
             else s += expf(x[i] - top);
         }
-        if constexpr (K64) sum = wave_sum_f64(s);
-        else sum = wave_sum(s);
+        sum = wave_total(s);
     }
     auto score = [&](float v) -> Real {
         if constexpr (SG) {
@@ -157,13 +179,17 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
                     if (v > a) { b = a; a = v; }
                     else if (v > b) b = v;
                 }
-            for (int d = 1; d < L; d <<= 1) {
-                const uint64_t a2 = __shfl_xor(a, d, 64), b2 = __shfl_xor(b, d, 64);
+            auto join = [&](uint64_t a2, uint64_t b2) {
                 const uint64_t lo = a < a2 ? a : a2;
                 a = a < a2 ? a2 : a;
                 b = b < b2 ? b2 : b;
                 b = b < lo ? lo : b;
-            }
+            };
+            if (L > 1) join(dpp_u64<kDppQuadXor1>(a), dpp_u64<kDppQuadXor1>(b));
+            if (L > 2) join(dpp_u64<kDppQuadXor2>(a), dpp_u64<kDppQuadXor2>(b));
+            if (L > 4) join(dpp_u64<kDppHalfMirror>(a), dpp_u64<kDppHalfMirror>(b));
+            if (L > 8) join(dpp_u64<kDppMirror>(a), dpp_u64<kDppMirror>(b));
+            if (L > 16) join(__shfl_xor(a, 16, 64), __shfl_xor(b, 16, 64));
             // sum of the two; a masked one counts as nothing, a group of masked ones never stays
             auto value = [](uint64_t v) {
                 return v == ~0ull ? __builtin_nan("")
@@ -174,9 +200,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
             kept = 0;
             for (int n = 0; n < p.topk_groups; ++n) {    // the best one left, lowest index first
                 const uint64_t mine = g < p.groups && lane % L == 0 && !((kept >> g) & 1) ? total : 0;
-                const uint64_t best = wave_max(mine);
+                uint64_t best;
+                const int at = __builtin_ctzll(wave_best(mine, best));
                 if (best <= kNone64) break;
-                const int at = __builtin_ctzll(__ballot(mine == best));
                 kept |= 1ull << (at / L);
             }
         }
@@ -187,34 +213,66 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
             key[i] = in ? order_bits(k[i]) : 0;
         }
     }
+    // Up to four experts a lane are sorted once (stable), so that a choice takes the head of a list.
+    constexpr bool kSorted = V <= 4;
+    int e[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) e[i] = lane * V + i;
+    if constexpr (kSorted) {
+#pragma unroll
+        for (int n = V - 1; n > 0; --n) {
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const bool swap = key[i + 1] > key[i];
+                const Key k0 = key[i], k1 = key[i + 1];
+                const float x0 = x[i], x1 = x[i + 1];
+                const int e0 = e[i], e1 = e[i + 1];
+                key[i] = swap ? k1 : k0;
+                key[i + 1] = swap ? k0 : k1;
+                x[i] = swap ? x1 : x0;
+                x[i + 1] = swap ? x0 : x1;
+                e[i] = swap ? e1 : e0;
+                e[i + 1] = swap ? e0 : e1;
+            }
+        }
+    }
     // lane j keeps the j-th choice
     int id = -1;
     float xj = 0.f;
     for (int j = 0; j < p.topk; ++j) {
-        Key m = 0;
+        Key m = key[0], best;
+        if constexpr (!kSorted) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) m = key[i] > m ? key[i] : m;
-        const Key best = wave_max(m);
-        if (best <= none) break;                         // uniform: only masked experts are left
-        const int at = __builtin_ctzll(__ballot(m == best));
-        int pick = V - 1;
-        float v = x[V - 1];
-#pragma unroll
-        for (int i = V - 2; i >= 0; --i)
-            if (key[i] == best) { pick = i; v = x[i]; }
-        if (lane == at) {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i == pick) key[i] = 0;
+            for (int i = 1; i < V; ++i) m = key[i] > m ? key[i] : m;
         }
-        const int e = __builtin_amdgcn_readlane(lane * V + pick, at);
-        const float xe = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), at));
-        if (lane == j) { id = e; xj = xe; }
+        const uint64_t lanes = wave_best(m, best);
+        if (best <= none) break;                         // uniform: only masked experts are left
+        const int at = __builtin_ctzll(lanes);
+        int pick = kSorted ? 0 : V - 1;
+        float v = x[pick];
+        if constexpr (!kSorted) {
+#pragma unroll
+            for (int i = V - 2; i >= 0; --i)
+                if (key[i] == best) { pick = i; v = x[i]; }
+        }
+        const int chosen = __builtin_amdgcn_readlane(kSorted ? e[0] : lane * V + pick, at);
+        const float xe = row_of(v, at);
+        if (lane == j) { id = chosen; xj = xe; }
+        if (lane == at) {
+            if constexpr (kSorted) {
+#pragma unroll
+                for (int i = 0; i < V - 1; ++i) { key[i] = key[i + 1]; x[i] = x[i + 1]; e[i] = e[i + 1]; }
+                key[V - 1] = 0;
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (i == pick) key[i] = 0;
+            }
+        }
     }
     Real w = id >= 0 ? score(xj) : (Real)0;
     if (p.renorm) {
-        if constexpr (K64) w = w / (wave_sum_f64(w) + (double)kRouteEps);
-        else w = w / (wave_sum(w) + kRouteEps);
+        w = w / (wave_total(w) + (Real)kRouteEps);
     }
     if (lane < p.topk) {
         p.ids[t * p.topk + lane] = id;
@@ -236,37 +294,44 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_bwd_kernel(RouteArgs p
         if (id < 0 || id >= p.E) id = -1;
         g = p.d_weights[t * p.topk + lane];
     }
-    float xj = id >= 0 ? logit_at(p, t * p.E + id) : -__builtin_inff();
-    float top = 0.f, rsum = 1.f;
+    // the chosen logits from the lanes that hold them
+    float xj = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float v = __shfl(x[i], (id < 0 ? 0 : id) / V, 64);
+        if (id >= 0 && id % V == i) xj = v;
+    }
+    float top = 0.f, rsum = 1.f, pe[V];
     if constexpr (!SG) {
         top = wave_top<V>(x);
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) s += expf(x[i] - top);
-        rsum = 1.f / wave_sum(s);
+        for (int i = 0; i < V; ++i) s += pe[i] = expf(x[i] - top);
+        rsum = 1.f / wave_total(s);
     }
     const float sj = id < 0 ? 0.f : SG ? sigmoid_f32(xj) : expf(xj - top) * rsum;
     float ds = id < 0 ? 0.f : p.weight_scale * g;
     float inner = 0.f;                                   // sum_k ds_k p_k (softmax)
     if (p.renorm) {
-        const float D = wave_sum(sj) + kRouteEps;
+        const float D = wave_total(sj) + kRouteEps;
         float acc = 0.f;
         for (int k = 0; k < p.topk; ++k) {
-            const float gk = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), k)),
-                        sk = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sj), k));
+            const float gk = row_of(g, k), sk = row_of(sj, k);
             if (sk != 0.f) acc += sk * (g - gk);         // uniform; a pair without an expert is none
         }
         if (id >= 0) ds = p.weight_scale * ((acc + kRouteEps * g) / D) / D;
-        if constexpr (!SG) inner = p.weight_scale * (wave_sum(id < 0 ? 0.f : g * sj) * kRouteEps / D) / D;
+        if constexpr (!SG) inner = p.weight_scale * (wave_total(id < 0 ? 0.f : g * sj) * kRouteEps / D) / D;
     } else if constexpr (!SG) {
-        inner = wave_sum(ds * sj);
+        inner = wave_total(ds * sj);
     }
+    // sigmoid: s (1 - s) ds where it is formed, 1 - s without cancellation; the other experts have none
+    if constexpr (SG) ds = id < 0 || ds == 0.f ? 0.f : ds * sj * sigmoid_f32(-xj);
     float d[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) d[i] = 0.f;
     for (int k = 0; k < p.topk; ++k) {                   // in pair order: equal calls, equal sums
         const int e = __builtin_amdgcn_readlane(id, k);
-        const float dk = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ds), k));
+        const float dk = row_of(ds, k);
         if (e < 0) continue;
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -276,14 +341,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_bwd_kernel(RouteArgs p
     for (int i = 0; i < V; ++i) {
         const int e = lane * V + i;
         if (e >= p.E) continue;
-        float r;
-        if constexpr (SG) {
-            const float s = sigmoid_f32(x[i]), c = sigmoid_f32(-x[i]);   // 1 - s without cancellation
-            r = d[i] == 0.f ? 0.f : d[i] * s * c;
-        } else {
-            r = expf(x[i] - top) * rsum * (d[i] - inner);
-            if (x[i] == -__builtin_inff()) r = 0.f;
-        }
+        float r = d[i];
+        if constexpr (!SG) r = x[i] == -__builtin_inff() ? 0.f : pe[i] * rsum * (d[i] - inner);
         const int64_t at = t * p.E + e;
         if (p.otype == O_FP32) static_cast<float*>(p.d_logits)[at] = r;
         else static_cast<uint16_t*>(p.d_logits)[at] =
