@@ -901,40 +901,109 @@ def bfq_norm_residual_backward(res_out, d_res, y=None, w_post=None, gate=None,
 
 # ------------------------------------------------ MoE layer around the grouped GEMM
 
-def _route_operands(logits, topk_ids, w, wname):
+# These calls are short next to the checks of their arguments, so a tensor that fits (its class, type,
+# shape, strides and device) is told by one expression and gives its address at once; anything else goes
+# through the checks above, which say what is wrong. A tensor that fits but for its device gives None, and
+# `_devices` names it once all the others have been looked at.
+
+ROW_DTYPES = OUT_DTYPES + CODE_DTYPES
+_T_I32 = _T_F32 = _T_BF16 = _T_OUT = _T_RES = _T_CODES = _T_ROWS = frozenset()   # torch dtypes, by _current_device
+_TYPE_NAMES: dict = {}                                                           # and their names
+_ready = False          # torch's GPU runtime is initialised (it stays so)
+
+
+def _current_device() -> int:
+    """The current GPU; -2, which no tensor is on, while the runtime is not initialised."""
+    global _ready, _T_I32, _T_F32, _T_BF16, _T_OUT, _T_RES, _T_CODES, _T_ROWS
+    if _ready:
+        return _torch._C._cuda_getDevice()
+    torch = _torch_module()
+    if not _TYPE_NAMES:
+        for names in (("int32",), ("float32",), ("bfloat16",), OUT_DTYPES, RES_DTYPES, CODE_DTYPES, ROW_DTYPES):
+            _TYPE_NAMES[frozenset(getattr(torch, n) for n in names)] = names
+        _T_I32, _T_F32, _T_BF16, _T_OUT, _T_RES, _T_CODES, _T_ROWS = _TYPE_NAMES
+    _ready = torch.cuda.is_initialized()
+    return torch._C._cuda_getDevice() if _ready else -2
+
+
+def _launch_stream(stream, dev):
+    """The handle to launch on: torch's current stream of the current device, or the one given."""
+    return _torch._C._cuda_getCurrentRawStream(dev) if stream is None and dev >= 0 else _stream(stream)
+
+
+def _mat(t, name, types, rows, cols, dev):
+    """Address of a [rows, cols] matrix with packed rows, 0 for None, None if only its device is wrong."""
+    if t is None:
+        return 0
+    if (t.__class__ is _Tensor and t.get_device() == dev and t.dtype in types and t.is_contiguous()
+            and t.shape == (rows, cols)):
+        return t.data_ptr()
+    _rows(t, name, _TYPE_NAMES[types], rows, cols)
+    return t if isinstance(t, int) else t.data_ptr() if t.get_device() == dev else None
+
+
+def _vec(t, name, types, numel, dev, exact=True):
+    """The same for a contiguous buffer of numel elements."""
+    if t is None:
+        return 0
+    if t.__class__ is _Tensor and t.get_device() == dev and t.dtype in types and t.is_contiguous() and t.numel() == numel:
+        return t.data_ptr()
+    _flat(t, name, _TYPE_NAMES[types], numel, exact)
+    return t if isinstance(t, int) else t.data_ptr() if t.get_device() == dev else None
+
+
+def _scale_ptr(t, name, layout, ld, m, groups, write, dev):
+    """The same for scales in `layout`."""
+    if t is None:
+        return 0
+    _scales(t, name, layout, ld, m, groups, write)
+    return t if isinstance(t, int) else t.data_ptr() if t.get_device() == dev else None
+
+
+def _route_operands(logits, topk_ids, w, wname, dev):
     T, E = _shape2(logits, "logits")
     topk = _shape2(topk_ids, "topk_ids")[1]
-    _rows(logits, "logits", OUT_DTYPES, T, E)
-    _rows(topk_ids, "topk_ids", ("int32",), T, topk)
-    _rows(w, wname, ("float32",), T, topk)
-    return T, E, topk
+    return (T, E, topk, _mat(logits, "logits", _T_OUT, T, E, dev), _mat(topk_ids, "topk_ids", _T_I32, T, topk, dev),
+            _mat(w, wname, _T_F32, T, topk, dev))
 
 
 def bfq_moe_route(logits, topk_ids, topk_weights, bias=None, score=BFQ_SCORE_SOFTMAX, n_groups=1,
                   topk_groups=1, renorm=False, weight_scale=1.0, stream=None) -> int:
     """logits [T, E] bf16 / fp16 / fp32; topk_ids int32 and topk_weights fp32 [T, topk] receive each
     token's experts, best first, and their weights. bias fp32 [E] moves the choice only."""
-    T, E, topk = _route_operands(logits, topk_ids, topk_weights, "topk_weights")
-    if bias is not None:
-        _flat(bias, "bias", ("float32",), E)
-    _devices(logits=logits, bias=bias, topk_ids=topk_ids, topk_weights=topk_weights)
-    st = lib.bfq_moe_route(_ptr(logits), _odtype(logits), _ptr(bias), T, E, topk, score, n_groups,
-                           topk_groups, int(renorm), weight_scale, _ptr(topk_ids), _ptr(topk_weights),
-                           _stream(stream))
-    return _check(st, "bfq_moe_route")
+    dev = _current_device()
+    T, E, topk, pl, pi, pw = _route_operands(logits, topk_ids, topk_weights, "topk_weights", dev)
+    pb = _vec(bias, "bias", _T_F32, E, dev)
+    if pl is None or pi is None or pw is None or pb is None:
+        _devices(logits=logits, bias=bias, topk_ids=topk_ids, topk_weights=topk_weights)
+    st = lib.bfq_moe_route(pl, _OUT_TYPES[_dt(logits)], pb, T, E, topk, score, n_groups, topk_groups,
+                           1 if renorm else 0, weight_scale, pi, pw, _launch_stream(stream, dev))
+    return st if st == 0 else _check(st, "bfq_moe_route")
 
 
 def bfq_moe_route_backward(logits, topk_ids, d_weights, d_logits, score=BFQ_SCORE_SOFTMAX,
                            renorm=False, weight_scale=1.0, stream=None) -> int:
     """d_logits ([T, E], logits' dtype) receives the gradient of the weights of topk_ids at the
     logits, for d_weights fp32 [T, topk]."""
-    T, E, topk = _route_operands(logits, topk_ids, d_weights, "d_weights")
-    _rows(d_logits, "d_logits", (_dt(logits),), T, E)
-    _devices(logits=logits, topk_ids=topk_ids, d_weights=d_weights, d_logits=d_logits)
-    st = lib.bfq_moe_route_backward(_ptr(logits), _odtype(logits), _ptr(topk_ids), _ptr(d_weights), T, E,
-                                    topk, score, int(renorm), weight_scale, _ptr(d_logits),
-                                    _stream(stream))
-    return _check(st, "bfq_moe_route_backward")
+    dev = _current_device()
+    T, E, topk, pl, pi, pw = _route_operands(logits, topk_ids, d_weights, "d_weights", dev)
+    pd = _same(d_logits, "d_logits", logits, T, E, dev)
+    if pl is None or pi is None or pw is None or pd is None:
+        _devices(logits=logits, topk_ids=topk_ids, d_weights=d_weights, d_logits=d_logits)
+    st = lib.bfq_moe_route_backward(pl, _OUT_TYPES[_dt(logits)], pi, pw, T, E, topk, score, 1 if renorm else 0,
+                                    weight_scale, pd, _launch_stream(stream, dev))
+    return st if st == 0 else _check(st, "bfq_moe_route_backward")
+
+
+def _same(t, name, like, rows, cols, dev):
+    """Address of a [rows, cols] matrix of another tensor's type."""
+    if t is None:
+        return 0
+    if (t.__class__ is _Tensor and t.get_device() == dev and t.dtype is like.dtype and t.is_contiguous()
+            and t.shape == (rows, cols)):
+        return t.data_ptr()
+    _rows(t, name, (_dt(like),), rows, cols)
+    return t if isinstance(t, int) else t.data_ptr() if t.get_device() == dev else None
 
 
 def bfq_moe_sort_workspace_bytes(T, topk, E) -> int:
@@ -945,31 +1014,34 @@ def bfq_moe_sort(topk_ids, E, expert_offsets, sorted_pairs, pair_rows, workspace
                  workspace_bytes=None, stream=None) -> int:
     """The outputs of bfq_moe_align, and pair_rows int32 [T, topk]: each pair's place in
     sorted_pairs, -1 for an id outside [0, E)."""
+    dev = _current_device()
     T, topk = _shape2(topk_ids, "topk_ids")
-    workspace_bytes = _workspace_arg(workspace, workspace_bytes)
-    _rows(topk_ids, "topk_ids", ("int32",), T, topk)
-    _rows(pair_rows, "pair_rows", ("int32",), T, topk)
-    _flat(expert_offsets, "expert_offsets", ("int32",), E + 1)
-    _flat(sorted_pairs, "sorted_pairs", ("int32",), T * topk, exact=False)
-    _workspace(workspace, workspace_bytes)
-    _devices(topk_ids=topk_ids, expert_offsets=expert_offsets, sorted_pairs=sorted_pairs,
-             pair_rows=pair_rows, workspace=workspace)
-    st = lib.bfq_moe_sort(_ptr(topk_ids), T, topk, E, _ptr(expert_offsets), _ptr(sorted_pairs),
-                          _ptr(pair_rows), _ptr(workspace), workspace_bytes, _stream(stream))
-    return _check(st, "bfq_moe_sort")
+    pi = _mat(topk_ids, "topk_ids", _T_I32, T, topk, dev)
+    pp = _mat(pair_rows, "pair_rows", _T_I32, T, topk, dev)
+    po = _vec(expert_offsets, "expert_offsets", _T_I32, E + 1, dev)
+    ps = _vec(sorted_pairs, "sorted_pairs", _T_I32, T * topk, dev, exact=False)
+    pw = 0
+    if workspace is not None:
+        workspace_bytes = _workspace_arg(workspace, workspace_bytes)
+        _workspace(workspace, workspace_bytes)
+        pw = workspace if isinstance(workspace, int) else workspace.data_ptr() if workspace.get_device() == dev else None
+    if pi is None or pp is None or po is None or ps is None or pw is None:
+        _devices(topk_ids=topk_ids, expert_offsets=expert_offsets, sorted_pairs=sorted_pairs,
+                 pair_rows=pair_rows, workspace=workspace)
+    st = lib.bfq_moe_sort(pi, T, topk, E, po, ps, pp, pw, workspace_bytes or 0, _launch_stream(stream, dev))
+    return st if st == 0 else _check(st, "bfq_moe_sort")
 
 
-def _codes_out(q, scales, layout, scale_ld, R, N):
-    """Checks of output codes [R, N] with their scales; returns (q_dtype, scale_ld)."""
-    if (q is None) != (scales is None):
+def _codes_out(q, scales, layout, scale_ld, R, N, dev):
+    """Checks of output codes [R, N] with their scales; returns (q, scales, q_dtype, scale_ld)."""
+    if q is None and scales is None:
+        return 0, 0, BFQ_E4M3FN, 0
+    if q is None or scales is None:
         raise BfqArgumentError("q and scales go together")
-    if q is None:
-        return BFQ_E4M3FN, 0
-    _rows(q, "q", CODE_DTYPES, R, N)
+    pq = _mat(q, "q", _T_CODES, R, N, dev)
     if scale_ld is None:
         scale_ld = scales.stride(0)
-    _scales(scales, "scales", layout, scale_ld, R, N // 128, write=True)
-    return _qdtype(q), scale_ld
+    return pq, _scale_ptr(scales, "scales", layout, scale_ld, R, N // 128, True, dev), _qdtype(q), scale_ld
 
 
 def bfq_moe_dispatch(x, pair_rows, rows=None, q=None, scales=None, x_scales=None,
@@ -977,31 +1049,26 @@ def bfq_moe_dispatch(x, pair_rows, rows=None, q=None, scales=None, x_scales=None
                      scale_ld=None, q_eps=DEFAULT_EPS, scale_fmt=BFQ_SCALE_FP32, stream=None) -> int:
     """Row pair_rows[t, j] of the outputs receives row t of x: bf16 [T, K] as rows (bf16 [R, K]) and
     / or as codes q [R, K] with scales; or codes x with x_scales as codes."""
+    dev = _current_device()
     T, K = _shape2(x, "x")
     topk = _shape2(pair_rows, "pair_rows")[1]
     R = _shape2(q if q is not None else rows, "q" if q is not None else "rows")[0]
     copy = x_scales is not None
-    _rows(x, "x", CODE_DTYPES if copy else ("bfloat16",), T, K)
-    _rows(pair_rows, "pair_rows", ("int32",), T, topk)
+    px = _mat(x, "x", _T_CODES if copy else _T_BF16, T, K, dev)
+    pp = _mat(pair_rows, "pair_rows", _T_I32, T, topk, dev)
+    pxs = 0
     if copy:
         if x_scale_ld is None:
             x_scale_ld = x_scales.stride(0)
-        _scales(x_scales, "x_scales", x_layout, x_scale_ld, T, K // 128, write=False)
-    if rows is not None:
-        _rows(rows, "rows", ("bfloat16",), R, K)
-    qt, scale_ld = _codes_out(q, scales, layout, scale_ld, R, K)
-    _devices(x=x, x_scales=x_scales, pair_rows=pair_rows, rows=rows, q=q, scales=scales)
-    st = lib.bfq_moe_dispatch(_ptr(x), _qdtype(x) if copy else BFQ_BF16, _ptr(x_scales), x_layout,
-                              x_scale_ld or 0, _ptr(pair_rows), _ptr(rows), _ptr(q), qt, _ptr(scales),
-                              layout, scale_ld, q_eps, scale_fmt, T, topk, K, R, _stream(stream))
-    return _check(st, "bfq_moe_dispatch")
-
-
-def _pair_operands(T, topk, weights, pair_rows, topk_ids):
-    for n, t, dt in (("weights", weights, "float32"), ("pair_rows", pair_rows, "int32"),
-                     ("topk_ids", topk_ids, "int32")):
-        if t is not None:
-            _rows(t, n, (dt,), T, topk)
+        pxs = _scale_ptr(x_scales, "x_scales", x_layout, x_scale_ld, T, K // 128, False, dev)
+    pr = _mat(rows, "rows", _T_BF16, R, K, dev)
+    pq, ps, qt, scale_ld = _codes_out(q, scales, layout, scale_ld, R, K, dev)
+    if px is None or pp is None or pxs is None or pr is None or pq is None or ps is None:
+        _devices(x=x, x_scales=x_scales, pair_rows=pair_rows, rows=rows, q=q, scales=scales)
+    st = lib.bfq_moe_dispatch(px, _qdtype(x) if copy else BFQ_BF16, pxs, x_layout, x_scale_ld or 0, pp, pr,
+                              pq, qt, ps, layout, scale_ld, q_eps, scale_fmt, T, topk, K, R,
+                              _launch_stream(stream, dev))
+    return st if st == 0 else _check(st, "bfq_moe_dispatch")
 
 
 def bfq_moe_combine(rows, out, topk, weights=None, pair_rows=None, topk_ids=None, E=0, base=None,
@@ -1010,28 +1077,29 @@ def bfq_moe_combine(rows, out, topk, weights=None, pair_rows=None, topk_ids=None
     of rows [R, K]: row pair_rows[t, j], or (None) row t*topk + j unless topk_ids [T, topk] has an id
     outside [0, E) there. base: out's dtype, None for zeros, may be out. ckpt (codes [R, K]) and
     ckpt_scales (fp32 [R, K/128]) receive the rows in 8 bits."""
+    dev = _current_device()
     T, K = _shape2(out, "out")
     R = _shape2(rows, "rows")[0]
-    _rows(rows, "rows", OUT_DTYPES, R, K)
-    _rows(out, "out", OUT_DTYPES, T, K)
-    _pair_operands(T, topk, weights, pair_rows, topk_ids)
-    if base is not None:
-        _rows(base, "base", (_dt(out),), T, K)
-    if (ckpt is None) != (ckpt_scales is None):
-        raise BfqArgumentError("ckpt and ckpt_scales go together")
-    if ckpt is not None:
-        _rows(ckpt, "ckpt", CODE_DTYPES, R, K)
-        _rows(ckpt_scales, "ckpt_scales", ("float32",), R, K // 128)
-    _devices(rows=rows, out=out, weights=weights, pair_rows=pair_rows, topk_ids=topk_ids, base=base,
-             ckpt=ckpt, ckpt_scales=ckpt_scales)
-    st = lib.bfq_moe_combine(_ptr(rows), _odtype(rows), _ptr(weights), _ptr(pair_rows), _ptr(topk_ids), E,
-                             _ptr(base), _ptr(out), _odtype(out), _ptr(ckpt),
-                             _qdtype(ckpt) if ckpt is not None else BFQ_E4M3FN, _ptr(ckpt_scales), q_eps,
-                             T, topk, K, R, _stream(stream))
-    return _check(st, "bfq_moe_combine")
-
-
-ROW_DTYPES = OUT_DTYPES + CODE_DTYPES
+    pr = _mat(rows, "rows", _T_OUT, R, K, dev)
+    po = _mat(out, "out", _T_OUT, T, K, dev)
+    pw = _mat(weights, "weights", _T_F32, T, topk, dev)
+    pp = _mat(pair_rows, "pair_rows", _T_I32, T, topk, dev)
+    pi = _mat(topk_ids, "topk_ids", _T_I32, T, topk, dev)
+    pb = _same(base, "base", out, T, K, dev)
+    pc = pcs = 0
+    ct = BFQ_E4M3FN
+    if ckpt is not None or ckpt_scales is not None:
+        if ckpt is None or ckpt_scales is None:
+            raise BfqArgumentError("ckpt and ckpt_scales go together")
+        pc = _mat(ckpt, "ckpt", _T_CODES, R, K, dev)
+        pcs = _mat(ckpt_scales, "ckpt_scales", _T_F32, R, K // 128, dev)
+        ct = _qdtype(ckpt)
+    if None in (pr, po, pw, pp, pi, pb, pc, pcs):
+        _devices(rows=rows, out=out, weights=weights, pair_rows=pair_rows, topk_ids=topk_ids, base=base,
+                 ckpt=ckpt, ckpt_scales=ckpt_scales)
+    st = lib.bfq_moe_combine(pr, _OUT_TYPES[_dt(rows)], pw, pp, pi, E, pb, po, _OUT_TYPES[_dt(out)], pc, ct, pcs, q_eps, T,
+                             topk, K, R, _launch_stream(stream, dev))
+    return st if st == 0 else _check(st, "bfq_moe_combine")
 
 
 def bfq_moe_combine_backward(dout, topk, weights=None, rows=None, rows_scales=None, pair_rows=None,
@@ -1041,42 +1109,42 @@ def bfq_moe_combine_backward(dout, topk, weights=None, rows=None, rows_scales=No
     """Gradients of bfq_moe_combine for dout bf16 / fp32 [T, K]: weights times dout as d_rows (bf16
     [R, K]) and / or codes q [R, K] with scales; d_weights fp32 [T, topk] from rows [R, K] (bf16, fp16,
     fp32, or codes with rows_scales fp32 [R, K/128])."""
+    dev = _current_device()
     T, K = _shape2(dout, "dout")
-    given = [(n, t) for n, t in (("rows", rows), ("d_rows", d_rows), ("q", q)) if t is not None]
-    if not given:
-        raise BfqArgumentError("one of d_rows, q and d_weights (with rows) must be given")
-    R = _shape2(given[0][1], given[0][0])[0]
-    _rows(dout, "dout", RES_DTYPES, T, K)
-    _pair_operands(T, topk, weights, pair_rows, topk_ids)
-    if (rows is None) != (d_weights is None):
-        raise BfqArgumentError("rows and d_weights go together")
-    rt = BFQ_BF16
     if rows is not None:
-        _rows(rows, "rows", ROW_DTYPES, R, K)
+        R = _shape2(rows, "rows")[0]
+    elif d_rows is not None:
+        R = _shape2(d_rows, "d_rows")[0]
+    elif q is not None:
+        R = _shape2(q, "q")[0]
+    else:
+        raise BfqArgumentError("one of d_rows, q and d_weights (with rows) must be given")
+    pd = _mat(dout, "dout", _T_RES, T, K, dev)
+    pw = _mat(weights, "weights", _T_F32, T, topk, dev)
+    pp = _mat(pair_rows, "pair_rows", _T_I32, T, topk, dev)
+    pi = _mat(topk_ids, "topk_ids", _T_I32, T, topk, dev)
+    pr = prs = pdw = 0
+    rt = BFQ_BF16
+    if rows is not None or d_weights is not None:
+        if rows is None or d_weights is None:
+            raise BfqArgumentError("rows and d_weights go together")
+        pr = _mat(rows, "rows", _T_ROWS, R, K, dev)
         rt = _OUT_TYPES.get(_dt(rows))
         if rt is None:
             rt = _qdtype(rows)
             if rows_scales is None:
                 raise BfqArgumentError("rows of codes need rows_scales")
-        if rows_scales is not None:
-            _rows(rows_scales, "rows_scales", ("float32",), R, K // 128)
-        _rows(d_weights, "d_weights", ("float32",), T, topk)
-    if d_rows is not None:
-        _rows(d_rows, "d_rows", ("bfloat16",), R, K)
-    qt, scale_ld = _codes_out(q, scales, layout, scale_ld, R, K)
-    _devices(dout=dout, weights=weights, rows=rows, rows_scales=rows_scales, pair_rows=pair_rows,
-             topk_ids=topk_ids, d_rows=d_rows, q=q, scales=scales, d_weights=d_weights)
-    st = lib.bfq_moe_combine_backward(_ptr(dout), BFQ_BF16 if _dt(dout) == "bfloat16" else BFQ_FP32,
-                                      _ptr(weights), _ptr(rows), rt, _ptr(rows_scales), _ptr(pair_rows),
-                                      _ptr(topk_ids), E, _ptr(d_rows), _ptr(q), qt, _ptr(scales), layout,
-                                      scale_ld, q_eps, scale_fmt, _ptr(d_weights), T, topk, K, R,
-                                      _stream(stream))
-    return _check(st, "bfq_moe_combine_backward")
-
-
-def _live_rows(t):
-    if t is not None:
-        _flat(t, "live_rows", ("int32",), 1)
+        prs = _mat(rows_scales, "rows_scales", _T_F32, R, K // 128, dev)
+        pdw = _mat(d_weights, "d_weights", _T_F32, T, topk, dev)
+    pdr = _mat(d_rows, "d_rows", _T_BF16, R, K, dev)
+    pq, ps, qt, scale_ld = _codes_out(q, scales, layout, scale_ld, R, K, dev)
+    if None in (pd, pw, pp, pi, pr, prs, pdw, pdr, pq, ps):
+        _devices(dout=dout, weights=weights, rows=rows, rows_scales=rows_scales, pair_rows=pair_rows,
+                 topk_ids=topk_ids, d_rows=d_rows, q=q, scales=scales, d_weights=d_weights)
+    st = lib.bfq_moe_combine_backward(pd, _OUT_TYPES[_dt(dout)], pw, pr, rt, prs, pp, pi, E, pdr, pq, qt,
+                                      ps, layout, scale_ld, q_eps, scale_fmt, pdw, T, topk, K, R,
+                                      _launch_stream(stream, dev))
+    return st if st == 0 else _check(st, "bfq_moe_combine_backward")
 
 
 def bfq_gated_checkpoint(preact, act=BFQ_ACT_SILU, h=None, q=None, scales=None,
@@ -1086,25 +1154,27 @@ def bfq_gated_checkpoint(preact, act=BFQ_ACT_SILU, h=None, q=None, scales=None,
     """From preact = (g, u) bf16 [M, 2F]: act(g) * u as h (bf16 [M, F]) and / or codes q [M, F] with
     scales, and preact in 8 bits as ckpt (codes [M, 2F]) with ckpt_scales (fp32 [M, 2F/128]).
     live_rows: int32 tensor of one element, the rows that exist (None: all)."""
+    dev = _current_device()
     M, F2 = _shape2(preact, "preact")
     F = F2 // 2
-    _rows(preact, "preact", ("bfloat16",), M, 2 * F)
-    if h is not None:
-        _rows(h, "h", ("bfloat16",), M, F)
-    if (ckpt is None) != (ckpt_scales is None):
-        raise BfqArgumentError("ckpt and ckpt_scales go together")
-    if ckpt is not None:
-        _rows(ckpt, "ckpt", CODE_DTYPES, M, 2 * F)
-        _rows(ckpt_scales, "ckpt_scales", ("float32",), M, 2 * F // 128)
-    _live_rows(live_rows)
-    qt, scale_ld = _codes_out(q, scales, layout, scale_ld, M, F)
-    _devices(preact=preact, h=h, q=q, scales=scales, ckpt=ckpt, ckpt_scales=ckpt_scales,
-             live_rows=live_rows)
-    st = lib.bfq_gated_checkpoint(_ptr(preact), act, _ptr(h), _ptr(q), qt, _ptr(scales), layout, scale_ld,
-                                  q_eps, scale_fmt, _ptr(ckpt),
-                                  _qdtype(ckpt) if ckpt is not None else BFQ_E4M3FN, _ptr(ckpt_scales),
-                                  _ptr(live_rows), M, F, _stream(stream))
-    return _check(st, "bfq_gated_checkpoint")
+    pp = _mat(preact, "preact", _T_BF16, M, 2 * F, dev)
+    ph = _mat(h, "h", _T_BF16, M, F, dev)
+    pc = pcs = 0
+    ct = BFQ_E4M3FN
+    if ckpt is not None or ckpt_scales is not None:
+        if ckpt is None or ckpt_scales is None:
+            raise BfqArgumentError("ckpt and ckpt_scales go together")
+        pc = _mat(ckpt, "ckpt", _T_CODES, M, 2 * F, dev)
+        pcs = _mat(ckpt_scales, "ckpt_scales", _T_F32, M, 2 * F // 128, dev)
+        ct = _qdtype(ckpt)
+    pl = _vec(live_rows, "live_rows", _T_I32, 1, dev)
+    pq, ps, qt, scale_ld = _codes_out(q, scales, layout, scale_ld, M, F, dev)
+    if None in (pp, ph, pc, pcs, pl, pq, ps):
+        _devices(preact=preact, h=h, q=q, scales=scales, ckpt=ckpt, ckpt_scales=ckpt_scales,
+                 live_rows=live_rows)
+    st = lib.bfq_gated_checkpoint(pp, act, ph, pq, qt, ps, layout, scale_ld, q_eps, scale_fmt, pc, ct, pcs,
+                                  pl, M, F, _launch_stream(stream, dev))
+    return st if st == 0 else _check(st, "bfq_gated_checkpoint")
 
 
 def bfq_gated_checkpoint_backward(ckpt, ckpt_scales, dh, act=BFQ_ACT_SILU, dpre=None, q=None,
@@ -1114,22 +1184,21 @@ def bfq_gated_checkpoint_backward(ckpt, ckpt_scales, dh, act=BFQ_ACT_SILU, dpre=
     """bfq_gated_backward from the 8-bit checkpoint ckpt [M, 2F] with ckpt_scales [M, 2F/128]: for dh
     bf16 [M, F], dpre (bf16 [M, 2F]) and / or codes q [M, 2F] with scales; h (bf16 [M, F]) receives the
     product again."""
+    dev = _current_device()
     M, F = _shape2(dh, "dh")
-    _rows(ckpt, "ckpt", CODE_DTYPES, M, 2 * F)
-    _rows(ckpt_scales, "ckpt_scales", ("float32",), M, 2 * F // 128)
-    _rows(dh, "dh", ("bfloat16",), M, F)
-    if dpre is not None:
-        _rows(dpre, "dpre", ("bfloat16",), M, 2 * F)
-    if h is not None:
-        _rows(h, "h", ("bfloat16",), M, F)
-    _live_rows(live_rows)
-    qt, scale_ld = _codes_out(q, scales, layout, scale_ld, M, 2 * F)
-    _devices(ckpt=ckpt, ckpt_scales=ckpt_scales, dh=dh, dpre=dpre, q=q, scales=scales, h=h,
-             live_rows=live_rows)
-    st = lib.bfq_gated_checkpoint_backward(_ptr(ckpt), _qdtype(ckpt), _ptr(ckpt_scales), _ptr(dh), act,
-                                           _ptr(dpre), _ptr(q), qt, _ptr(scales), layout, scale_ld, q_eps,
-                                           scale_fmt, _ptr(h), _ptr(live_rows), M, F, _stream(stream))
-    return _check(st, "bfq_gated_checkpoint_backward")
+    pc = _mat(ckpt, "ckpt", _T_CODES, M, 2 * F, dev)
+    pcs = _mat(ckpt_scales, "ckpt_scales", _T_F32, M, 2 * F // 128, dev)
+    pd = _mat(dh, "dh", _T_BF16, M, F, dev)
+    pdp = _mat(dpre, "dpre", _T_BF16, M, 2 * F, dev)
+    ph = _mat(h, "h", _T_BF16, M, F, dev)
+    pl = _vec(live_rows, "live_rows", _T_I32, 1, dev)
+    pq, ps, qt, scale_ld = _codes_out(q, scales, layout, scale_ld, M, 2 * F, dev)
+    if None in (pc, pcs, pd, pdp, ph, pl, pq, ps):
+        _devices(ckpt=ckpt, ckpt_scales=ckpt_scales, dh=dh, dpre=dpre, q=q, scales=scales, h=h,
+                 live_rows=live_rows)
+    st = lib.bfq_gated_checkpoint_backward(pc, _qdtype(ckpt), pcs, pd, act, pdp, pq, qt, ps, layout,
+                                           scale_ld, q_eps, scale_fmt, ph, pl, M, F, _launch_stream(stream, dev))
+    return st if st == 0 else _check(st, "bfq_gated_checkpoint_backward")
 
 
 # ------------------------------------------------------------ allocating conveniences
