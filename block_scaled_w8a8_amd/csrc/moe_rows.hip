@@ -251,8 +251,8 @@ __global__ __launch_bounds__(256) void dispatch_codes_kernel(DispatchArgs p) {
         if constexpr (Q >= 0) {
             if (p.rows) {
                 const __amdgpu_buffer_rsrc_t rr = pair_row(p.rows, r, (uint32_t)(2 * K));
-                row_store16<S>(rr, (uint32_t)c * 32, raw0);
-                row_store16<S>(rr, (uint32_t)c * 32, raw1, 16);
+                row_store16<0>(rr, (uint32_t)c * 32, raw0);      // halves of a line: not past the caches
+                row_store16<0>(rr, (uint32_t)c * 32, raw1, 16);
             }
         }
     }
@@ -345,13 +345,15 @@ template <int RK, int CK, int NB> static void combine_s(const CombineArgs& a, hi
         hipLaunchKernelGGL((combine_kernel<RK, CK, NB, 1>), grid, block, 0, stream, a);
     else hipLaunchKernelGGL((combine_kernel<RK, CK, NB, 0>), grid, block, 0, stream, a);
 }
+template <int RK, int CK> static void combine_nb(const CombineArgs& a, hipStream_t stream) {
+    if (a.at.topk <= 2) combine_s<RK, CK, 2>(a, stream);
+    else if (a.at.topk <= 4) combine_s<RK, CK, 4>(a, stream);
+    else combine_s<RK, CK, 8>(a, stream);
+}
 template <int RK> static void combine_rk(const CombineArgs& a, hipStream_t stream) {
-    if (a.ckpt) {
-        if (a.ckpt_type == Q_FP8) combine_s<RK, Q_FP8, 8>(a, stream);
-        else combine_s<RK, Q_INT8, 8>(a, stream);
-    } else if (a.at.topk <= 2) combine_s<RK, -1, 2>(a, stream);
-    else if (a.at.topk <= 4) combine_s<RK, -1, 4>(a, stream);
-    else combine_s<RK, -1, 8>(a, stream);
+    if (!a.ckpt) combine_nb<RK, -1>(a, stream);
+    else if (a.ckpt_type == Q_FP8) combine_nb<RK, Q_FP8>(a, stream);
+    else combine_nb<RK, Q_INT8>(a, stream);
 }
 hipError_t launch_combine(const CombineArgs& a, hipStream_t stream) {
     if (a.rows_type == O_BF16) combine_rk<R_BF16>(a, stream);
@@ -370,6 +372,10 @@ template <int S, typename V> __device__ __forceinline__ void stream_store(void* 
     else *static_cast<V*>(p) = v;
 }
 
+// What a thread loads of a row at once.
+template <int BYTES> struct Load { typedef v4u type; };
+template <> struct Load<8> { typedef unsigned int type __attribute__((ext_vector_type(2))); };
+
 // A scalar that the compiler takes for a new one: what is formed from it is formed where it stands, not
 // ahead of the loop for all rows at once, which the scalar registers have no room for.
 __device__ __forceinline__ int here(int x) {
@@ -380,16 +386,16 @@ __device__ __forceinline__ int here(int x) {
 // A workgroup takes a token's whole row, because the weights' gradients are sums over it; eight pairs
 // at a time, their rows in flight together. The codes of w * dout come from one maximum for all
 // pairs: rounding is monotone, so the largest |w * dout| is |w| times the largest |dout|, rounded.
-// Columns of a thread: 16 where rows of codes are read (16-byte loads and stores), else 8. A pair
+// Columns of a thread: 16 where rows of codes are read and written (16-byte loads and stores), else 8. A pair
 // without a row reads that of another (which is in the caches) and writes nothing: the loads of a
 // batch have no branch between them. Bytes bound it: 4096 x 7168, eight pairs, codes in and out, 543 MB
 // in 107 to 113 us (4.8 to 5.1 TB/s; a large copy 5.2). Rows through buffer resources, eight times four
 // scalar registers that spilled, 8 columns a thread: 142 us; scalar bases and 16 columns, 448 threads
 // a token: 121; at most 256 threads, two rounds a row and more tokens on a CU: 107 (192: 114, 128: 114,
 // 64: 108; batches of four pairs: 109). One size for every batch: a token's sums do not depend on T.
-template <int RK, int Q, int S>
+template <int RK, int Q, int NB, int S>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
-    constexpr int NB = 8, U = RK == R_FP8 || RK == R_INT8 ? 2 : 1, W = 8 * U, LG = 16 / U;   // lanes of a group
+    constexpr int U = (RK == R_FP8 || RK == R_INT8) && Q >= 0 ? 2 : 1, W = 8 * U, LG = 16 / U;   // lanes of a group
     typedef RowChunk<RK == R_NONE ? (int)R_BF16 : RK, S> Chunk;
     typedef unsigned int v2u __attribute__((ext_vector_type(2)));
     const int64_t t = blockIdx.x, K = p.K, G = K / 128;
@@ -397,6 +403,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
     __shared__ float part[4][NB];
     if constexpr (Q >= 0) {
         if (t >= p.T) {                                  // uniform: a padding row of packed words
+            if (blockIdx.y != 0) return;
             for (int64_t w = tid; w < (G + 3) / 4; w += blockDim.x) p.out.scales[w * p.out.stride_g + p.at.R + (t - p.T)] = 0.f;
             return;
         }
@@ -405,8 +412,8 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
     const uint64_t there = __ballot(place >= 0);         // bit j: pair j has a row
     const float weight = p.weights && lane < p.at.topk ? p.weights[t * p.at.topk + lane] : 1.f;
     const uint32_t chunks = (uint32_t)(K / W);
-    for (int j0 = 0; j0 < p.at.topk; j0 += NB) {
-        const uint32_t alive = (uint32_t)(there >> j0) & 0xFFu;
+    for (int j0 = blockIdx.y * NB; j0 < p.at.topk; j0 += gridDim.y * NB) {
+        const uint32_t alive = (uint32_t)(there >> j0) & ((1u << NB) - 1);
         float acc[NB];
         int r[NB];
         // lane k of a group stores pair k's scale (taken here, where every lane of the wave takes part)
@@ -421,7 +428,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
             const uint32_t c = c0 + tid;
             if (c >= chunks) continue;                   // whole groups: K is a multiple of 128 with codes
             float d[W];
-            v4u v[NB][RK == R_FP32 ? 2 : 1];
+            typename Load<Chunk::size * W>::type v[NB][RK == R_FP32 ? 2 : 1];
             float sv[NB];
             if constexpr (RK != R_NONE) {
 #pragma unroll
@@ -429,7 +436,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
                     const int64_t ri = here(r[i]);
                     const uint8_t* row = static_cast<const uint8_t*>(p.rows) + ri * (K * Chunk::size);
                     const uint32_t at = c * (W * Chunk::size);
-                    v[i][0] = stream_load<S, v4u>(row + at);
+                    v[i][0] = stream_load<S, typename Load<Chunk::size * W>::type>(row + at);
                     if constexpr (RK == R_FP32) v[i][1] = stream_load<S, v4u>(row + at + 16);
                     if constexpr (Chunk::codes) sv[i] = (p.rows_scales + ri * G)[c / LG];
                 }
@@ -461,6 +468,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
                         float x[8];
                         Chunk chunk;
                         if constexpr (U == 2) chunk.a = u ? v4u{v[i][0].z, v[i][0].w, 0, 0} : v[i][0];
+                        else if constexpr (Chunk::codes) chunk.a = v4u{v[i][0].x, v[i][0].y, 0, 0};
                         else chunk.a = v[i][0];
                         if constexpr (RK == R_FP32) chunk.b = v[i][1];
                         chunk.get(x);
@@ -477,7 +485,8 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         const uint4 b = pack8(z + 8 * u);
-                        stream_store<S>(row + c * (2 * W) + 16 * u, v4u{b.x, b.y, b.z, b.w});
+                        // halves of a line leave together: not past the caches
+                        stream_store<U == 2 ? 0 : S>(row + c * (2 * W) + 16 * u, v4u{b.x, b.y, b.z, b.w});
                     }
                 }
                 if constexpr (Q >= 0) {
@@ -517,13 +526,19 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
     }
 }
 
+// Two pairs at a time where a token has no more (4096 tokens, 2 pairs: 52 -> 38 us), and, as workgroups of
+// their own, where tokens are few (212 tokens, 8 pairs: 16 -> 11 us; at 2000 tokens the gradient that each of
+// them reads again makes it 58 -> 68). A pair's sum is the same either way.
 template <int RK, int Q> static void combine_bwd_s(const CombineBwdArgs& a, hipStream_t stream) {
-    const int64_t chunks = a.K / (RK == R_FP8 || RK == R_INT8 ? 16 : 8), rounds = (chunks + 255) / 256;
+    const int64_t chunks = a.K / ((RK == R_FP8 || RK == R_INT8) && Q >= 0 ? 16 : 8), rounds = (chunks + 255) / 256;
     const dim3 block((unsigned)(((chunks + rounds - 1) / rounds + 63) / 64 * 64));
-    const dim3 grid((unsigned)(a.T + (Q >= 0 && a.out.packed ? (4 - a.at.R % 4) % 4 : 0)));
-    if (past_caches(a.at.R * a.K * ((a.d_rows ? 2 : 0) + (Q >= 0 ? 1 : 0))))
-        hipLaunchKernelGGL((combine_bwd_kernel<RK, Q, 1>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((combine_bwd_kernel<RK, Q, 0>), grid, block, 0, stream, a);
+    const bool two = a.at.topk <= 2 || a.T < 1024;
+    const dim3 grid((unsigned)(a.T + (Q >= 0 && a.out.packed ? (4 - a.at.R % 4) % 4 : 0)), two ? (a.at.topk + 1) / 2 : 1);
+    const bool past = past_caches(a.at.R * a.K * ((a.d_rows ? 2 : 0) + (Q >= 0 ? 1 : 0)));
+    if (two && past) hipLaunchKernelGGL((combine_bwd_kernel<RK, Q, 2, 1>), grid, block, 0, stream, a);
+    else if (two) hipLaunchKernelGGL((combine_bwd_kernel<RK, Q, 2, 0>), grid, block, 0, stream, a);
+    else if (past) hipLaunchKernelGGL((combine_bwd_kernel<RK, Q, 8, 1>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((combine_bwd_kernel<RK, Q, 8, 0>), grid, block, 0, stream, a);
 }
 template <int RK> static void combine_bwd_rk(const CombineBwdArgs& a, hipStream_t stream) {
     if (!a.out.q) combine_bwd_s<RK, -1>(a, stream);

@@ -85,23 +85,31 @@ template <typename R> __device__ __forceinline__ R wave_total(R x) {
 }
 
 // Experts lane*V .. of a token's row; those past E count as masked. +inf counts as the largest
-// finite value, so that a softmax over it is defined.
+// finite value, so that a softmax over it is defined. Every load is issued before the first is looked at
+// (past E: the last expert's, unused); with a branch around each, one waited for the other.
 template <int V>
 __device__ __forceinline__ void load_logits(const RouteArgs& p, int64_t t, int lane, float* x) {
     const int64_t at = t * p.E;
-    const int e0 = lane * V;
+    const int e0 = lane * V, last = p.E - 1;
+    if (p.otype == O_FP32) {
+        const float* row = static_cast<const float*>(p.logits) + at;
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = row[min(e0 + i, last)];
+    } else {
+        const uint16_t* row = static_cast<const uint16_t*>(p.logits) + at;
+        uint16_t h[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) h[i] = row[min(e0 + i, last)];
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = p.otype == O_BF16 ? bf16_lo(h[i]) : (float)__builtin_bit_cast(_Float16, h[i]);
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int e = e0 + i;
-        x[i] = -__builtin_inff();
-        if (e < p.E) {
-            if (p.otype == O_FP32) x[i] = static_cast<const float*>(p.logits)[at + e];
-            else if (p.otype == O_BF16) x[i] = bf16_lo(static_cast<const uint16_t*>(p.logits)[at + e]);
-            else x[i] = (float)static_cast<const _Float16*>(p.logits)[at + e];
-            if (x[i] == __builtin_inff()) x[i] = 0x1.fffffep127f;
-        }
+        x[i] = x[i] == __builtin_inff() ? 0x1.fffffep127f : x[i];
+        x[i] = e0 + i > last ? -__builtin_inff() : x[i];
     }
 }
+
 // The wave's largest logit (a NaN wins); 0 where all are masked, whose exponentials are then 0.
 template <int V> __device__ __forceinline__ float wave_top(const float* x) {
     uint32_t m = 0;
@@ -113,7 +121,14 @@ template <int V> __device__ __forceinline__ float wave_top(const float* x) {
     return m <= kNone32 ? 0.f : top;
 }
 
-__device__ __forceinline__ double sigmoid_f64(double x) { return 1.0 / (1.0 + exp(-x)); }
+// 1 / d of a positive d: two Newton steps on the hardware's estimate (about 2^-26), each squaring the
+// error; a division where d is near the range's end.
+__device__ __forceinline__ double inverse_f64(double d) {
+    if (!(d < 0x1p1000)) return 1.0 / d;
+    double r = __builtin_amdgcn_rcp(d);
+    r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+    return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+}
 
 // K64: keys are scores plus bias in 64 bits (bias or groups), else the logits.
 template <int V, int SG, int K64>
@@ -125,28 +140,36 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
     typedef typename std::conditional<K64 != 0, uint64_t, uint32_t>::type Key;
     typedef typename std::conditional<K64 != 0, double, float>::type Real;
     const Key none = K64 ? (Key)kNone64 : (Key)kNone32;
-    float x[V];
+    float x[V], bias[V];
     load_logits<V>(p, t, lane, x);
-    Real top = 0, sum = 1;
+    if constexpr (K64) {
+        if (p.bias) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) bias[i] = p.bias[min(lane * V + i, p.E - 1)];
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) bias[i] = 0.f;
+        }
+    }
+    Real top = 0, rsum = 1, s[V];                        // scores; K64 only where they are keys
     if constexpr (!SG) {
         top = wave_top<V>(x);
-        Real s = 0;
+        Real sum = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if constexpr (K64) s += exp((double)x[i] - top);
-            else s += expf(x[i] - top);
+            if constexpr (K64) s[i] = exp((double)x[i] - top);
+            else s[i] = expf(x[i] - top);
+            sum += s[i];
         }
-        sum = wave_total(s);
+        sum = wave_total(sum);
+        if constexpr (K64) rsum = inverse_f64(sum);
+        else rsum = 1.f / sum;
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] *= rsum;
+    } else if constexpr (K64) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = inverse_f64(1.0 + exp(-(double)x[i]));
     }
-    auto score = [&](float v) -> Real {
-        if constexpr (SG) {
-            if constexpr (K64) return sigmoid_f64((double)v);
-            else return sigmoid_f32(v);
-        } else {
-            if constexpr (K64) return exp((double)v - top) / sum;
-            else return expf(v - top) / sum;
-        }
-    };
     Key key[V];
     if constexpr (!K64) {
 #pragma unroll
@@ -155,9 +178,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
         double k[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
-            k[i] = score(x[i]) + (p.bias && e < p.E ? (double)p.bias[e] : 0.0);
-            if (x[i] == -__builtin_inff()) k[i] = -__builtin_inf();
+            k[i] = x[i] == -__builtin_inff() ? -__builtin_inf() : s[i] + (double)bias[i];
         }
         uint64_t kept = ~0ull;                           // groups that stay
         int size = p.E;                                  // experts of a group
@@ -213,8 +234,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
             key[i] = in ? order_bits(k[i]) : 0;
         }
     }
-    // Up to four experts a lane are sorted once (stable), so that a choice takes the head of a list.
-    constexpr bool kSorted = V <= 4;
+    // Up to six experts a lane are sorted once (stable), so that a choice takes the head of a list.
+    constexpr bool kSorted = V <= 6;
     int e[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) e[i] = lane * V + i;
@@ -270,7 +291,13 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
             }
         }
     }
-    Real w = id >= 0 ? score(xj) : (Real)0;
+    Real w = 0;
+    if (id >= 0) {
+        if constexpr (SG && K64) w = inverse_f64(1.0 + exp(-(double)xj));
+        else if constexpr (SG) w = sigmoid_f32(xj);
+        else if constexpr (K64) w = exp((double)xj - top) * rsum;
+        else w = expf(xj - top) * rsum;
+    }
     if (p.renorm) {
         w = w / (wave_total(w) + (Real)kRouteEps);
     }
@@ -285,15 +312,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_bwd_kernel(RouteArgs p
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
     if (t >= p.T) return;
-    float x[V];
+    const int64_t pair = t * p.topk + (lane < p.topk ? lane : 0);
+    int id = p.ids[pair];
+    float g = p.d_weights[pair], x[V];
     load_logits<V>(p, t, lane, x);
-    int id = -1;
-    float g = 0.f;
-    if (lane < p.topk) {
-        id = p.ids[t * p.topk + lane];
-        if (id < 0 || id >= p.E) id = -1;
-        g = p.d_weights[t * p.topk + lane];
-    }
+    if (lane >= p.topk) g = 0.f;
+    if (lane >= p.topk || id < 0 || id >= p.E) id = -1;
     // the chosen logits from the lanes that hold them
     float xj = -__builtin_inff();
 #pragma unroll
@@ -337,16 +361,21 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_bwd_kernel(RouteArgs p
         for (int i = 0; i < V; ++i)
             if (lane * V + i == e) d[i] += dk;
     }
+    if constexpr (!SG) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane * V + i;
-        if (e >= p.E) continue;
-        float r = d[i];
-        if constexpr (!SG) r = x[i] == -__builtin_inff() ? 0.f : pe[i] * rsum * (d[i] - inner);
-        const int64_t at = t * p.E + e;
-        if (p.otype == O_FP32) static_cast<float*>(p.d_logits)[at] = r;
-        else static_cast<uint16_t*>(p.d_logits)[at] =
-            (uint16_t)(p.otype == O_BF16 ? f32_to_bf16_bits(r) : f32_to_f16_bits(r));
+        for (int i = 0; i < V; ++i) d[i] = x[i] == -__builtin_inff() ? 0.f : pe[i] * rsum * (d[i] - inner);
+    }
+    const int64_t at = t * p.E + lane * V;
+    if (p.otype == O_FP32) {
+        float* row = static_cast<float*>(p.d_logits) + at;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (lane * V + i < p.E) row[i] = d[i];
+    } else {
+        uint16_t* row = static_cast<uint16_t*>(p.d_logits) + at;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (lane * V + i < p.E) row[i] = (uint16_t)(p.otype == O_BF16 ? f32_to_bf16_bits(d[i]) : f32_to_f16_bits(d[i]));
     }
 }
 
@@ -369,7 +398,9 @@ template <int V> static void route_bwd(const RouteArgs& a, hipStream_t stream) {
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
     if (a.E <= 64) route_fwd<1>(a, stream);
     else if (a.E <= 128) route_fwd<2>(a, stream);
+    else if (a.E <= 192) route_fwd<3>(a, stream);
     else if (a.E <= 256) route_fwd<4>(a, stream);
+    else if (a.E <= 384) route_fwd<6>(a, stream);
     else if (a.E <= 512) route_fwd<8>(a, stream);
     else route_fwd<16>(a, stream);
     return hipGetLastError();
@@ -377,7 +408,9 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
 hipError_t launch_route_bwd(const RouteArgs& a, hipStream_t stream) {
     if (a.E <= 64) route_bwd<1>(a, stream);
     else if (a.E <= 128) route_bwd<2>(a, stream);
+    else if (a.E <= 192) route_bwd<3>(a, stream);
     else if (a.E <= 256) route_bwd<4>(a, stream);
+    else if (a.E <= 384) route_bwd<6>(a, stream);
     else if (a.E <= 512) route_bwd<8>(a, stream);
     else route_bwd<16>(a, stream);
     return hipGetLastError();

@@ -85,12 +85,13 @@ template <int RK, int S> struct RowChunk {
     }
 };
 
-// Eight values as bf16, fp16 or fp32 (uniform) at column 8c of a row.
+// Eight values as bf16, fp16 or fp32 (uniform) at column 8c of a row. Those of fp32 are two halves of a
+// line, which meet in L2: never past the caches.
 template <int S>
 __device__ __forceinline__ void row_store(__amdgpu_buffer_rsrc_t r, uint32_t c, int otype, const float* x) {
     if (otype == O_FP32) {
-        row_store16<S>(r, c * 32, __builtin_bit_cast(v4u, v4f{x[0], x[1], x[2], x[3]}));
-        row_store16<S>(r, c * 32, __builtin_bit_cast(v4u, v4f{x[4], x[5], x[6], x[7]}), 16);
+        row_store16<0>(r, c * 32, __builtin_bit_cast(v4u, v4f{x[0], x[1], x[2], x[3]}));
+        row_store16<0>(r, c * 32, __builtin_bit_cast(v4u, v4f{x[4], x[5], x[6], x[7]}), 16);
         return;
     }
     v4u v;
