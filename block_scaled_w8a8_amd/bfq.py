@@ -956,6 +956,10 @@ def _scale_ptr(t, name, layout, ld, m, groups, write, dev):
     """The same for scales in `layout`."""
     if t is None:
         return 0
+    if layout != BFQ_SCALES_PACKED_UE8M0 and t.__class__ is _Tensor and t.get_device() == dev and t.dtype in _T_F32:
+        need = (m, groups) if layout == BFQ_SCALES_ROW_MAJOR else (groups, m)
+        if t.shape == need and ld == need[1] and t.is_contiguous():
+            return t.data_ptr()
     _scales(t, name, layout, ld, m, groups, write)
     return t if isinstance(t, int) else t.data_ptr() if t.get_device() == dev else None
 

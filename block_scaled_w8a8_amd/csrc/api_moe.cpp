@@ -145,13 +145,14 @@ bfq_status bfq_moe_dispatch(const void* x, bfq_dtype x_dtype, const float* x_sca
                             float* scales, bfq_scale_layout layout, int64_t scale_ld, float q_eps,
                             bfq_scale_format scale_fmt, int64_t T, int32_t topk, int64_t K, int64_t R,
                             void* stream) {
+    const bool some = T != 0 && R != 0;                  // a row to write; else its tensors may be NULL
     if (T != 0 && (!x || !pair_rows)) return fail(BFQ_ERR_NULL, "x and pair_rows must be non-NULL");
-    if (T != 0 && !rows && !q) return fail(BFQ_ERR_NULL, "one of rows and q must be non-NULL");
-    if (T != 0 && (q != nullptr) != (scales != nullptr))
+    if (some && !rows && !q) return fail(BFQ_ERR_NULL, "one of rows and q must be non-NULL");
+    if (some && (q != nullptr) != (scales != nullptr))
         return fail(BFQ_ERR_NULL, "q and scales must both be given or both be NULL");
     const bool copy = code_type(x_dtype);
     if (!copy && x_dtype != BFQ_BF16) return fail(BFQ_ERR_DTYPE, "x must be BF16, or codes E4M3FN or INT8");
-    if (T != 0 && copy && (!q || !x_scales || rows))
+    if (some && copy && (!q || !x_scales || rows))
         return fail(BFQ_ERR_NULL, "codes are dispatched as codes: x_scales, q and scales non-NULL, rows NULL");
     if (T != 0 && !copy && x_scales) return fail(BFQ_ERR_NULL, "bf16 rows have no x_scales");
     bfq_status s = check_tokens(T, topk, K, R);
@@ -182,7 +183,7 @@ bfq_status bfq_moe_dispatch(const void* x, bfq_dtype x_dtype, const float* x_sca
             return fail(BFQ_ERR_ARG, "unknown scale layout");
         }
     }
-    if (T == 0) return BFQ_OK;
+    if (!some) return BFQ_OK;
     a.x = x;
     a.x_scales = copy ? x_scales : nullptr;
     a.T = T;
@@ -196,8 +197,8 @@ bfq_status bfq_moe_combine(const void* rows, bfq_dtype rows_dtype, const float* 
                            const int32_t* topk_ids, int32_t E, const void* base, void* out, bfq_dtype out_dtype,
                            void* ckpt, bfq_dtype ckpt_dtype, float* ckpt_scales, float q_eps, int64_t T,
                            int32_t topk, int64_t K, int64_t R, void* stream) {
-    if (T != 0 && (!rows || !out)) return fail(BFQ_ERR_NULL, "rows and out must be non-NULL");
-    if (T != 0 && (ckpt != nullptr) != (ckpt_scales != nullptr))
+    if (T != 0 && ((!rows && R != 0) || !out)) return fail(BFQ_ERR_NULL, "rows and out must be non-NULL");
+    if (T != 0 && R != 0 && (ckpt != nullptr) != (ckpt_scales != nullptr))
         return fail(BFQ_ERR_NULL, "ckpt and ckpt_scales must both be given or both be NULL");
     if (!float_type(rows_dtype) || !float_type(out_dtype))
         return fail(BFQ_ERR_DTYPE, "rows and out must be BF16, FP16 or FP32");
@@ -237,17 +238,18 @@ bfq_status bfq_moe_combine_backward(const void* dout, bfq_dtype dout_dtype, cons
                                     bfq_scale_format scale_fmt, float* d_weights, int64_t T, int32_t topk,
                                     int64_t K, int64_t R, void* stream) {
     if (T != 0 && !dout) return fail(BFQ_ERR_NULL, "dout must be non-NULL");
-    if (T != 0 && !d_rows && !q && !d_weights) return fail(BFQ_ERR_NULL, "one of d_rows, q and d_weights must be non-NULL");
-    if (T != 0 && (q != nullptr) != (scales != nullptr))
+    const bool some = T != 0 && R != 0;                  // a row to read or write; else its tensors may be NULL
+    if (some && !d_rows && !q && !d_weights) return fail(BFQ_ERR_NULL, "one of d_rows, q and d_weights must be non-NULL");
+    if (some && (q != nullptr) != (scales != nullptr))
         return fail(BFQ_ERR_NULL, "q and scales must both be given or both be NULL");
-    if (T != 0 && (rows != nullptr) != (d_weights != nullptr))
+    if (some && (rows != nullptr) != (d_weights != nullptr))
         return fail(BFQ_ERR_NULL, "d_weights needs rows, and rows are read for it only");
     if (dout_dtype != BFQ_BF16 && dout_dtype != BFQ_FP32) return fail(BFQ_ERR_DTYPE, "dout must be BF16 or FP32");
     CombineBwdArgs a{};
     if (rows) {
         if (!float_type(rows_dtype) && !code_type(rows_dtype))
             return fail(BFQ_ERR_DTYPE, "rows must be BF16, FP16, FP32, or codes E4M3FN or INT8");
-        if (code_type(rows_dtype) != (rows_scales != nullptr))
+        if (some && code_type(rows_dtype) != (rows_scales != nullptr))
             return fail(BFQ_ERR_NULL, "rows_scales go with rows of codes");
         a.row_kind = rows_dtype == BFQ_BF16 ? R_BF16 : rows_dtype == BFQ_FP16 ? R_FP16 : rows_dtype == BFQ_FP32 ? R_FP32
                    : rows_dtype == BFQ_E4M3FN ? R_FP8 : R_INT8;
@@ -264,7 +266,12 @@ bfq_status bfq_moe_combine_backward(const void* dout, bfq_dtype dout_dtype, cons
     if (!aligned(dout, 16) || !aligned(rows, 16) || !aligned(d_rows, 16) || !aligned(q, 16) || !aligned(scales, 4) ||
         !aligned(rows_scales, 4) || !aligned(weights, 4) || !aligned(d_weights, 4))
         return fail(BFQ_ERR_ALIGN, "row tensors must be 16-byte aligned, weights and scales 4-byte");
-    if (T == 0) return BFQ_OK;
+    if (!some) {                                         // without a row the weights have no gradient
+        if (T == 0 || !d_weights) return BFQ_OK;
+        a.row_kind = R_BF16;
+        a.out = CodesOut{};
+        d_rows = nullptr;
+    }
     a.dout = dout;
     a.dout_f32 = dout_dtype == BFQ_FP32;
     a.weights = weights;

@@ -376,6 +376,22 @@ def test_dispatch_and_combine_are_transposes(bfq):
     assert float((rows[:n].double() * g[:n].double()).sum()) == float((x.double() * dx.double()).sum())
 
 
+def test_no_rows(bfq):
+    """R = 0: the base or zeros come back, the weights have no gradient, nothing else happens."""
+    T, topk, K = 5, 3, 256
+    x, at = _randn(1, T, K).bfloat16(), torch.randint(-2, 3, (T, topk), generator=_gen(2), device=DEV, dtype=torch.int32)
+    none, w = torch.empty((0, K), dtype=torch.bfloat16, device=DEV), torch.full((T, topk), math.nan, device=DEV)
+    assert bfq.moe_dispatch(x, at, R=0).shape == (0, K) and bfq.moe_dispatch(x, at, R=0, codes=True)[0].shape == (0, K)
+    assert torch.equal(bfq.moe_combine(none, topk, weights=w, pair_rows=at, base=x), x)
+    out, q, s = bfq.moe_combine(none, topk, weights=w, pair_rows=at, ckpt_dtype=bfq.BFQ_E4M3FN)
+    assert not bool(out.any()) and q.numel() == 0
+    for codes in (False, True):
+        assert not bool(bfq.moe_combine_backward(x, topk, weights=w, rows=none, pair_rows=at, codes=codes)["d_weights"].any())
+    scales = torch.empty((0, K // 128), device=DEV)
+    assert not bool(bfq.moe_combine_backward(x, topk, rows=none.view(torch.uint8)[:, :K].contiguous(), rows_scales=scales,
+                                             pair_rows=at)["d_weights"].any())
+
+
 def test_empty_batches(bfq):
     for T in (0,):
         x, at = torch.empty((T, 256), dtype=torch.bfloat16, device=DEV), torch.empty((T, 2), dtype=torch.int32, device=DEV)

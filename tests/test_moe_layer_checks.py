@@ -12,7 +12,8 @@ NAN, INF = float("nan"), float("inf")
 
 
 def _caller(fn, defaults):
-    def call(bfq, **kw):
+    def call(bfq, extra=None, **kw):
+        kw = {**(extra or {}), **kw}
         assert set(kw) <= set(defaults), kw
         return getattr(bfq.lib, fn)(*{**defaults, **kw}.values(), None)
     return call
@@ -95,6 +96,16 @@ def test_dispatch_refusals(bfq):
     _refuses(E, dispatch, E.BFQ_ERR_ALIGN, dict(x=P + 8), dict(q=P + 8), dict(rows=P + 2), dict(s=P + 2), dict(places=P + 1),
              dict(COPY, xs=P + 2))
     assert dispatch(E, T=0, R=0, x=None, places=None, q=None, s=None) == E.BFQ_OK
+
+
+def test_no_rows(bfq):
+    """A GPU that was given no row: tensors over rows may be missing, and nothing is to be written to them."""
+    E = bfq
+    assert dispatch(E, R=0, q=None, s=None) == E.BFQ_OK and dispatch(E, COPY, R=0, q=None, s=None) == E.BFQ_OK
+    _refuses(E, dispatch, E.BFQ_ERR_NULL, dict(R=0, x=None), dict(R=0, places=None))
+    _refuses(E, combine, E.BFQ_ERR_NULL, dict(R=0, rows=None, out=None))
+    _refuses(E, combine_bwd, E.BFQ_ERR_NULL, dict(R=0, dout=None))
+    assert combine_bwd(E, R=0, rows=None, d_rows=None, q=None, s=None, dw=None) == E.BFQ_OK
 
 
 def test_combine_refusals(bfq):
