@@ -2,8 +2,13 @@
 // the checkpoint:
 //   h = act(g) u, as bf16 or as codes;  the checkpoint: codes of g and u, one scale per 128 columns
 //   dg = dh u act'(g),  du = dh act(g) from the checkpoint's values, as bf16 or codes; h again
-// Bytes bound both: eight columns of both halves a thread, read once and written once, 16 lanes a
-// group. Rows from *live on (what no expert was given) are neither read nor written.
+// Eight columns of both halves a thread, read once and written once, 16 lanes a group. Rows from *live
+// on (what no expert was given) are neither read nor written. Bytes bound both, and the arithmetic is close
+// behind: 32768 x 2048 with codes of h, 476 MB in 78 us (6.1 TB/s), its gradient 411 MB in 79 us (5.2),
+// a large copy 5.2; over a hundred calls back to back, at the clock they then leave, 90 to 99 us, and 90
+// with the encoder's correction left out (some 360 instructions a thread forward). Sixteen columns a thread,
+// sharing maxima and scales between more: 4 % less there, 7 % more in single calls, and 14 to 17 % more with
+// bf16 outputs. SILU as a kernel of its own, without the cubic term: no difference.
 #include "activation.h"
 #include "row_access.h"
 

@@ -180,7 +180,7 @@ hipError_t launch_moe_sort(const int32_t* ids, int64_t pairs, int E, int32_t* of
 
 // --------------------------------------------------------------------- dispatch ----
 
-// Rows as they are: eight columns a thread.
+// Rows as they are: eight columns a thread (4096 x 7168 to eight rows each: 529 MB in 109 us, 4.9 TB/s).
 template <int S>
 __global__ __launch_bounds__(256) void dispatch_rows_kernel(DispatchArgs p) {
     const int64_t t = blockIdx.x;
@@ -197,7 +197,9 @@ __global__ __launch_bounds__(256) void dispatch_rows_kernel(DispatchArgs p) {
 // Codes of a token's row, formed or copied (Q < 0) once and written to each of its rows: 16 columns
 // a thread, so 8 lanes hold a group and every lane knows its scale; lane k of the group stores the
 // scale of pair k, k + 8, ..: one store for eight rows. Packed scales: 32 lanes hold a word. Blocks
-// past the tokens write the zero words of rows R .. round_up(R, 4) - 1.
+// past the tokens write the zero words of rows R .. round_up(R, 4) - 1. Bytes bound it: 4096 x 7168 to
+// eight rows each, 301 MB in 61 us (4.9 TB/s; a large copy 5.2) with row-major scales, 69 us with
+// column-major ones, whose neighbours belong to other tokens.
 template <int Q, int S>
 __global__ __launch_bounds__(256) void dispatch_codes_kernel(DispatchArgs p) {
     const int64_t t = blockIdx.x, K = p.K, G = K / 128;
@@ -290,7 +292,9 @@ hipError_t launch_dispatch_codes(const DispatchArgs& a, hipStream_t stream) {
 // ---------------------------------------------------------------------- combine ----
 
 // NB rows in flight a thread. CK: -1, or the code type of the rows' checkpoint: 16 lanes hold a
-// group, and lane k of them stores the scale of the batch's k-th row.
+// group, and lane k of them stores the scale of the batch's k-th row. Bytes bound it: 4096 x 7168, eight
+// rows each and a base, 588 MB in 113 us (5.2 TB/s, a large copy's rate), with the checkpoint 830 MB in
+// 163 us (5.1); one token 2.9 us.
 template <int RK, int CK, int NB, int S>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs p) {
     const int64_t t = blockIdx.x, K = p.K;
