@@ -307,7 +307,7 @@ bfq_status bfq_get_tile_candidate(const int32_t block_shape[2], bfq_dtype in_dty
  * expert count E in the key. Token t routed to experts topk_ids[t][0..topk-1] forms pairs
  * q = t*topk + j; out[q][n] (pair order, [T*topk][N]) = the block-scaled GEMM (as
  * bfq_block_gemm) of token row t of a_q with row n of expert topk_ids[t][j]'s weights.
- * e4m3fn codes, block_shape {128, 128}; the combine over a token's experts is not part of it.
+ * e4m3fn codes, block_shape {128, 128}; bfq_moe_combine adds up a token's experts.
  */
 
 /* Group the pairs by expert (stable: ascending pair id within an expert), the routing step

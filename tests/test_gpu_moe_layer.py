@@ -236,6 +236,18 @@ def test_tokens_do_not_depend_on_the_batch(bfq):
         assert torch.equal(g2["q"], g["q"][a * TOPK:b * TOPK]) and torch.equal(g2["d_weights"], g["d_weights"][a:b])
 
 
+def test_readme_example(bfq):
+    """The README's blocks run as they stand, one after the other."""
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(__file__), "..", "README.md")).read()
+    env = {}
+    for block in re.findall(r"```python\n(.*?)```", text, re.S):
+        exec(block, env)
+    assert env["moe"].shape == env["dx_moe"].shape == (64, 7168) and env["dlogits"].shape == (64, 16)
+    assert all(bool(env[n].float().isfinite().all()) and bool(env[n].any()) for n in ("moe", "dx_moe", "dlogits"))
+
+
 def test_host_and_other_device_tensors_are_refused(bfq):
     x = torch.zeros((4, 256), dtype=torch.bfloat16, device=DEV)
     at = torch.zeros((4, 2), dtype=torch.int32)
