@@ -187,6 +187,7 @@ __global__ __launch_bounds__(256) void dispatch_rows_kernel(DispatchArgs p) {
     const int lane = threadIdx.x & 63;
     const uint32_t voff = (blockIdx.y * blockDim.x + threadIdx.x) * 16, bytes = (uint32_t)(2 * p.K);
     const int place = pair_place(p.at, t, lane);
+    if (!__ballot(place >= 0)) return;                   // uniform: a token of other GPUs' experts
     const v4u v = row_load16<S>(pair_row(p.x, t, bytes), voff);
     for (int j = 0; j < p.at.topk; ++j) {
         const int r = __builtin_amdgcn_readlane(place, j);
@@ -213,6 +214,7 @@ __global__ __launch_bounds__(256) void dispatch_codes_kernel(DispatchArgs p) {
     const int64_t c = (int64_t)blockIdx.y * blockDim.x + threadIdx.x, g = c >> 3;
     const bool live = g < G;
     const int place = pair_place(p.at, t, lane);
+    if (!__ballot(place >= 0)) return;                   // uniform: a token of other GPUs' experts
     v4u code, raw0, raw1;
     float s = 0.f;                                       // packed: the bits of the group's word
     if constexpr (Q >= 0) {

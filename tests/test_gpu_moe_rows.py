@@ -376,6 +376,24 @@ def test_dispatch_and_combine_are_transposes(bfq):
     assert float((rows[:n].double() * g[:n].double()).sum()) == float((x.double() * dx.double()).sum())
 
 
+def test_pairs_that_share_a_row(bfq):
+    """Reading, a row may be several pairs'; a token may name one twice."""
+    T, topk, K, R = 40, 4, 264, 5
+    rows = _randn(1, R, K).bfloat16()
+    at = torch.randint(0, R, (T, topk), generator=_gen(2), device=DEV, dtype=torch.int32)
+    at[3] = 2
+    w = torch.rand((T, topk), generator=_gen(3), device=DEV)
+    out = bfq.moe_combine(rows, topk, weights=w, pair_rows=at)
+    terms = rows[at.long()].double() * w.double().unsqueeze(2)
+    tol = terms.abs().sum(dim=1) * U * (topk + 1) + terms.sum(dim=1).abs() * HALF[torch.bfloat16]
+    assert bool(((out.double() - terms.sum(dim=1)).abs() <= tol).all())
+    d = _randn(4, T, K).bfloat16()
+    dw = torch.empty((T, topk), device=DEV)
+    bfq.bfq_moe_combine_backward(d, topk, rows=rows, pair_rows=at, d_weights=dw)         # the weights' alone
+    terms = rows[at.long()].double() * d.double().unsqueeze(1)
+    assert bool(((dw.double() - terms.sum(dim=2)).abs() <= terms.abs().sum(dim=2) * U * 25).all())
+
+
 def test_no_rows(bfq):
     """R = 0: the base or zeros come back, the weights have no gradient, nothing else happens."""
     T, topk, K = 5, 3, 256
