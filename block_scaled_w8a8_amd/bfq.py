@@ -907,28 +907,25 @@ def bfq_norm_residual_backward(res_out, d_res, y=None, w_post=None, gate=None,
 # `_devices` names it once all the others have been looked at.
 
 ROW_DTYPES = OUT_DTYPES + CODE_DTYPES
-_T_I32 = _T_F32 = _T_BF16 = _T_OUT = _T_RES = _T_CODES = _T_ROWS = frozenset()   # torch dtypes, by _current_device
-_TYPE_NAMES: dict = {}                                                           # and their names
-_ready = False          # torch's GPU runtime is initialised (it stays so)
+_T_I32 = _T_F32 = _T_BF16 = _T_OUT = _T_RES = _T_CODES = _T_ROWS = frozenset()   # torch dtypes, by _runtime
+_TYPE_NAMES: dict = {}  # and their names
+_KINDS: dict = {}       # torch dtype -> bfq_dtype
+_device_now = _stream_now = None    # torch's calls for them, once its GPU runtime is initialised (it stays so)
 
 
-def _current_device() -> int:
+def _runtime() -> int:
     """The current GPU; -2, which no tensor is on, while the runtime is not initialised."""
-    global _ready, _T_I32, _T_F32, _T_BF16, _T_OUT, _T_RES, _T_CODES, _T_ROWS
-    if _ready:
-        return _torch._C._cuda_getDevice()
+    global _device_now, _stream_now, _T_I32, _T_F32, _T_BF16, _T_OUT, _T_RES, _T_CODES, _T_ROWS
     torch = _torch_module()
     if not _TYPE_NAMES:
         for names in (("int32",), ("float32",), ("bfloat16",), OUT_DTYPES, RES_DTYPES, CODE_DTYPES, ROW_DTYPES):
             _TYPE_NAMES[frozenset(getattr(torch, n) for n in names)] = names
         _T_I32, _T_F32, _T_BF16, _T_OUT, _T_RES, _T_CODES, _T_ROWS = _TYPE_NAMES
-    _ready = torch.cuda.is_initialized()
-    return torch._C._cuda_getDevice() if _ready else -2
-
-
-def _launch_stream(stream, dev):
-    """The handle to launch on: torch's current stream of the current device, or the one given."""
-    return _torch._C._cuda_getCurrentRawStream(dev) if stream is None and dev >= 0 else _stream(stream)
+        _KINDS.update((getattr(torch, n), k) for n, k in (*_CODE_TYPES.items(), *_OUT_TYPES.items()))
+    if not torch.cuda.is_initialized():
+        return -2
+    _device_now, _stream_now = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    return _device_now()
 
 
 def _mat(t, name, types, rows, cols, dev):
@@ -975,13 +972,14 @@ def bfq_moe_route(logits, topk_ids, topk_weights, bias=None, score=BFQ_SCORE_SOF
                   topk_groups=1, renorm=False, weight_scale=1.0, stream=None) -> int:
     """logits [T, E] bf16 / fp16 / fp32; topk_ids int32 and topk_weights fp32 [T, topk] receive each
     token's experts, best first, and their weights. bias fp32 [E] moves the choice only."""
-    dev = _current_device()
+    dev = _device_now() if _device_now else _runtime()
     T, E, topk, pl, pi, pw = _route_operands(logits, topk_ids, topk_weights, "topk_weights", dev)
     pb = _vec(bias, "bias", _T_F32, E, dev)
     if pl is None or pi is None or pw is None or pb is None:
         _devices(logits=logits, bias=bias, topk_ids=topk_ids, topk_weights=topk_weights)
-    st = lib.bfq_moe_route(pl, _OUT_TYPES[_dt(logits)], pb, T, E, topk, score, n_groups, topk_groups,
-                           1 if renorm else 0, weight_scale, pi, pw, _launch_stream(stream, dev))
+    handle = _stream_now(dev) if stream is None and dev >= 0 else _stream(stream)
+    st = lib.bfq_moe_route(pl, _KINDS[logits.dtype], pb, T, E, topk, score, n_groups, topk_groups,
+                           1 if renorm else 0, weight_scale, pi, pw, handle)
     return st if st == 0 else _check(st, "bfq_moe_route")
 
 
@@ -989,13 +987,14 @@ def bfq_moe_route_backward(logits, topk_ids, d_weights, d_logits, score=BFQ_SCOR
                            renorm=False, weight_scale=1.0, stream=None) -> int:
     """d_logits ([T, E], logits' dtype) receives the gradient of the weights of topk_ids at the
     logits, for d_weights fp32 [T, topk]."""
-    dev = _current_device()
+    dev = _device_now() if _device_now else _runtime()
     T, E, topk, pl, pi, pw = _route_operands(logits, topk_ids, d_weights, "d_weights", dev)
     pd = _same(d_logits, "d_logits", logits, T, E, dev)
     if pl is None or pi is None or pw is None or pd is None:
         _devices(logits=logits, topk_ids=topk_ids, d_weights=d_weights, d_logits=d_logits)
-    st = lib.bfq_moe_route_backward(pl, _OUT_TYPES[_dt(logits)], pi, pw, T, E, topk, score, 1 if renorm else 0,
-                                    weight_scale, pd, _launch_stream(stream, dev))
+    handle = _stream_now(dev) if stream is None and dev >= 0 else _stream(stream)
+    st = lib.bfq_moe_route_backward(pl, _KINDS[logits.dtype], pi, pw, T, E, topk, score,
+                                    1 if renorm else 0, weight_scale, pd, handle)
     return st if st == 0 else _check(st, "bfq_moe_route_backward")
 
 
@@ -1018,7 +1017,7 @@ def bfq_moe_sort(topk_ids, E, expert_offsets, sorted_pairs, pair_rows, workspace
                  workspace_bytes=None, stream=None) -> int:
     """The outputs of bfq_moe_align, and pair_rows int32 [T, topk]: each pair's place in
     sorted_pairs, -1 for an id outside [0, E)."""
-    dev = _current_device()
+    dev = _device_now() if _device_now else _runtime()
     T, topk = _shape2(topk_ids, "topk_ids")
     pi = _mat(topk_ids, "topk_ids", _T_I32, T, topk, dev)
     pp = _mat(pair_rows, "pair_rows", _T_I32, T, topk, dev)
@@ -1032,7 +1031,8 @@ def bfq_moe_sort(topk_ids, E, expert_offsets, sorted_pairs, pair_rows, workspace
     if pi is None or pp is None or po is None or ps is None or pw is None:
         _devices(topk_ids=topk_ids, expert_offsets=expert_offsets, sorted_pairs=sorted_pairs,
                  pair_rows=pair_rows, workspace=workspace)
-    st = lib.bfq_moe_sort(pi, T, topk, E, po, ps, pp, pw, workspace_bytes or 0, _launch_stream(stream, dev))
+    handle = _stream_now(dev) if stream is None and dev >= 0 else _stream(stream)
+    st = lib.bfq_moe_sort(pi, T, topk, E, po, ps, pp, pw, workspace_bytes or 0, handle)
     return st if st == 0 else _check(st, "bfq_moe_sort")
 
 
@@ -1045,7 +1045,7 @@ def _codes_out(q, scales, layout, scale_ld, R, N, dev):
     pq = _mat(q, "q", _T_CODES, R, N, dev)
     if scale_ld is None:
         scale_ld = scales.stride(0)
-    return pq, _scale_ptr(scales, "scales", layout, scale_ld, R, N // 128, True, dev), _qdtype(q), scale_ld
+    return pq, _scale_ptr(scales, "scales", layout, scale_ld, R, N // 128, True, dev), _KINDS[q.dtype], scale_ld
 
 
 def bfq_moe_dispatch(x, pair_rows, rows=None, q=None, scales=None, x_scales=None,
@@ -1053,7 +1053,7 @@ def bfq_moe_dispatch(x, pair_rows, rows=None, q=None, scales=None, x_scales=None
                      scale_ld=None, q_eps=DEFAULT_EPS, scale_fmt=BFQ_SCALE_FP32, stream=None) -> int:
     """Row pair_rows[t, j] of the outputs receives row t of x: bf16 [T, K] as rows (bf16 [R, K]) and
     / or as codes q [R, K] with scales; or codes x with x_scales as codes."""
-    dev = _current_device()
+    dev = _device_now() if _device_now else _runtime()
     T, K = _shape2(x, "x")
     topk = _shape2(pair_rows, "pair_rows")[1]
     R = _shape2(q if q is not None else rows, "q" if q is not None else "rows")[0]
@@ -1069,9 +1069,9 @@ def bfq_moe_dispatch(x, pair_rows, rows=None, q=None, scales=None, x_scales=None
     pq, ps, qt, scale_ld = _codes_out(q, scales, layout, scale_ld, R, K, dev)
     if px is None or pp is None or pxs is None or pr is None or pq is None or ps is None:
         _devices(x=x, x_scales=x_scales, pair_rows=pair_rows, rows=rows, q=q, scales=scales)
-    st = lib.bfq_moe_dispatch(px, _qdtype(x) if copy else BFQ_BF16, pxs, x_layout, x_scale_ld or 0, pp, pr,
-                              pq, qt, ps, layout, scale_ld, q_eps, scale_fmt, T, topk, K, R,
-                              _launch_stream(stream, dev))
+    handle = _stream_now(dev) if stream is None and dev >= 0 else _stream(stream)
+    st = lib.bfq_moe_dispatch(px, _KINDS[x.dtype], pxs, x_layout, x_scale_ld or 0, pp, pr, pq, qt,
+                              ps, layout, scale_ld, q_eps, scale_fmt, T, topk, K, R, handle)
     return st if st == 0 else _check(st, "bfq_moe_dispatch")
 
 
@@ -1081,7 +1081,7 @@ def bfq_moe_combine(rows, out, topk, weights=None, pair_rows=None, topk_ids=None
     of rows [R, K]: row pair_rows[t, j], or (None) row t*topk + j unless topk_ids [T, topk] has an id
     outside [0, E) there. base: out's dtype, None for zeros, may be out. ckpt (codes [R, K]) and
     ckpt_scales (fp32 [R, K/128]) receive the rows in 8 bits."""
-    dev = _current_device()
+    dev = _device_now() if _device_now else _runtime()
     T, K = _shape2(out, "out")
     R = _shape2(rows, "rows")[0]
     pr = _mat(rows, "rows", _T_OUT, R, K, dev)
@@ -1097,12 +1097,13 @@ def bfq_moe_combine(rows, out, topk, weights=None, pair_rows=None, topk_ids=None
             raise BfqArgumentError("ckpt and ckpt_scales go together")
         pc = _mat(ckpt, "ckpt", _T_CODES, R, K, dev)
         pcs = _mat(ckpt_scales, "ckpt_scales", _T_F32, R, K // 128, dev)
-        ct = _qdtype(ckpt)
-    if None in (pr, po, pw, pp, pi, pb, pc, pcs):
+        ct = _KINDS[ckpt.dtype]
+    if pr is None or po is None or pw is None or pp is None or pi is None or pb is None or pc is None or pcs is None:
         _devices(rows=rows, out=out, weights=weights, pair_rows=pair_rows, topk_ids=topk_ids, base=base,
                  ckpt=ckpt, ckpt_scales=ckpt_scales)
-    st = lib.bfq_moe_combine(pr, _OUT_TYPES[_dt(rows)], pw, pp, pi, E, pb, po, _OUT_TYPES[_dt(out)], pc, ct, pcs, q_eps, T,
-                             topk, K, R, _launch_stream(stream, dev))
+    handle = _stream_now(dev) if stream is None and dev >= 0 else _stream(stream)
+    st = lib.bfq_moe_combine(pr, _KINDS[rows.dtype], pw, pp, pi, E, pb, po, _KINDS[out.dtype], pc,
+                             ct, pcs, q_eps, T, topk, K, R, handle)
     return st if st == 0 else _check(st, "bfq_moe_combine")
 
 
@@ -1113,7 +1114,7 @@ def bfq_moe_combine_backward(dout, topk, weights=None, rows=None, rows_scales=No
     """Gradients of bfq_moe_combine for dout bf16 / fp32 [T, K]: weights times dout as d_rows (bf16
     [R, K]) and / or codes q [R, K] with scales; d_weights fp32 [T, topk] from rows [R, K] (bf16, fp16,
     fp32, or codes with rows_scales fp32 [R, K/128])."""
-    dev = _current_device()
+    dev = _device_now() if _device_now else _runtime()
     T, K = _shape2(dout, "dout")
     if rows is not None:
         R = _shape2(rows, "rows")[0]
@@ -1133,21 +1134,20 @@ def bfq_moe_combine_backward(dout, topk, weights=None, rows=None, rows_scales=No
         if rows is None or d_weights is None:
             raise BfqArgumentError("rows and d_weights go together")
         pr = _mat(rows, "rows", _T_ROWS, R, K, dev)
-        rt = _OUT_TYPES.get(_dt(rows))
-        if rt is None:
-            rt = _qdtype(rows)
-            if rows_scales is None:
-                raise BfqArgumentError("rows of codes need rows_scales")
+        rt = _KINDS[rows.dtype]
+        if rows_scales is None and rows.dtype in _T_CODES:
+            raise BfqArgumentError("rows of codes need rows_scales")
         prs = _mat(rows_scales, "rows_scales", _T_F32, R, K // 128, dev)
         pdw = _mat(d_weights, "d_weights", _T_F32, T, topk, dev)
     pdr = _mat(d_rows, "d_rows", _T_BF16, R, K, dev)
     pq, ps, qt, scale_ld = _codes_out(q, scales, layout, scale_ld, R, K, dev)
-    if None in (pd, pw, pp, pi, pr, prs, pdw, pdr, pq, ps):
+    if pd is None or pw is None or pp is None or pi is None or pr is None or prs is None or pdw is None or pdr is None or pq is None or ps is None:
         _devices(dout=dout, weights=weights, rows=rows, rows_scales=rows_scales, pair_rows=pair_rows,
                  topk_ids=topk_ids, d_rows=d_rows, q=q, scales=scales, d_weights=d_weights)
-    st = lib.bfq_moe_combine_backward(pd, _OUT_TYPES[_dt(dout)], pw, pr, rt, prs, pp, pi, E, pdr, pq, qt,
-                                      ps, layout, scale_ld, q_eps, scale_fmt, pdw, T, topk, K, R,
-                                      _launch_stream(stream, dev))
+    handle = _stream_now(dev) if stream is None and dev >= 0 else _stream(stream)
+    st = lib.bfq_moe_combine_backward(pd, _KINDS[dout.dtype], pw, pr, rt, prs, pp, pi, E, pdr, pq,
+                                      qt, ps, layout, scale_ld, q_eps, scale_fmt, pdw, T, topk, K,
+                                      R, handle)
     return st if st == 0 else _check(st, "bfq_moe_combine_backward")
 
 
@@ -1158,7 +1158,7 @@ def bfq_gated_checkpoint(preact, act=BFQ_ACT_SILU, h=None, q=None, scales=None,
     """From preact = (g, u) bf16 [M, 2F]: act(g) * u as h (bf16 [M, F]) and / or codes q [M, F] with
     scales, and preact in 8 bits as ckpt (codes [M, 2F]) with ckpt_scales (fp32 [M, 2F/128]).
     live_rows: int32 tensor of one element, the rows that exist (None: all)."""
-    dev = _current_device()
+    dev = _device_now() if _device_now else _runtime()
     M, F2 = _shape2(preact, "preact")
     F = F2 // 2
     pp = _mat(preact, "preact", _T_BF16, M, 2 * F, dev)
@@ -1170,14 +1170,15 @@ def bfq_gated_checkpoint(preact, act=BFQ_ACT_SILU, h=None, q=None, scales=None,
             raise BfqArgumentError("ckpt and ckpt_scales go together")
         pc = _mat(ckpt, "ckpt", _T_CODES, M, 2 * F, dev)
         pcs = _mat(ckpt_scales, "ckpt_scales", _T_F32, M, 2 * F // 128, dev)
-        ct = _qdtype(ckpt)
+        ct = _KINDS[ckpt.dtype]
     pl = _vec(live_rows, "live_rows", _T_I32, 1, dev)
     pq, ps, qt, scale_ld = _codes_out(q, scales, layout, scale_ld, M, F, dev)
-    if None in (pp, ph, pc, pcs, pl, pq, ps):
+    if pp is None or ph is None or pc is None or pcs is None or pl is None or pq is None or ps is None:
         _devices(preact=preact, h=h, q=q, scales=scales, ckpt=ckpt, ckpt_scales=ckpt_scales,
                  live_rows=live_rows)
-    st = lib.bfq_gated_checkpoint(pp, act, ph, pq, qt, ps, layout, scale_ld, q_eps, scale_fmt, pc, ct, pcs,
-                                  pl, M, F, _launch_stream(stream, dev))
+    handle = _stream_now(dev) if stream is None and dev >= 0 else _stream(stream)
+    st = lib.bfq_gated_checkpoint(pp, act, ph, pq, qt, ps, layout, scale_ld, q_eps, scale_fmt, pc,
+                                  ct, pcs, pl, M, F, handle)
     return st if st == 0 else _check(st, "bfq_gated_checkpoint")
 
 
@@ -1188,7 +1189,7 @@ def bfq_gated_checkpoint_backward(ckpt, ckpt_scales, dh, act=BFQ_ACT_SILU, dpre=
     """bfq_gated_backward from the 8-bit checkpoint ckpt [M, 2F] with ckpt_scales [M, 2F/128]: for dh
     bf16 [M, F], dpre (bf16 [M, 2F]) and / or codes q [M, 2F] with scales; h (bf16 [M, F]) receives the
     product again."""
-    dev = _current_device()
+    dev = _device_now() if _device_now else _runtime()
     M, F = _shape2(dh, "dh")
     pc = _mat(ckpt, "ckpt", _T_CODES, M, 2 * F, dev)
     pcs = _mat(ckpt_scales, "ckpt_scales", _T_F32, M, 2 * F // 128, dev)
@@ -1197,11 +1198,13 @@ def bfq_gated_checkpoint_backward(ckpt, ckpt_scales, dh, act=BFQ_ACT_SILU, dpre=
     ph = _mat(h, "h", _T_BF16, M, F, dev)
     pl = _vec(live_rows, "live_rows", _T_I32, 1, dev)
     pq, ps, qt, scale_ld = _codes_out(q, scales, layout, scale_ld, M, 2 * F, dev)
-    if None in (pc, pcs, pd, pdp, ph, pl, pq, ps):
+    if pc is None or pcs is None or pd is None or pdp is None or ph is None or pl is None or pq is None or ps is None:
         _devices(ckpt=ckpt, ckpt_scales=ckpt_scales, dh=dh, dpre=dpre, q=q, scales=scales, h=h,
                  live_rows=live_rows)
-    st = lib.bfq_gated_checkpoint_backward(pc, _qdtype(ckpt), pcs, pd, act, pdp, pq, qt, ps, layout,
-                                           scale_ld, q_eps, scale_fmt, ph, pl, M, F, _launch_stream(stream, dev))
+    handle = _stream_now(dev) if stream is None and dev >= 0 else _stream(stream)
+    st = lib.bfq_gated_checkpoint_backward(pc, _KINDS[ckpt.dtype], pcs, pd, act, pdp, pq, qt, ps,
+                                           layout, scale_ld, q_eps, scale_fmt, ph, pl, M, F,
+                                           handle)
     return st if st == 0 else _check(st, "bfq_gated_checkpoint_backward")
 
 
