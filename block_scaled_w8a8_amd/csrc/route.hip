@@ -13,10 +13,10 @@
 // A wave takes a token: lane l holds experts l*V .. l*V + V-1, so the lowest index among equal keys is
 // the lowest lane's, and a choice costs one wave maximum (DPP within rows of 16 lanes, v_readlane
 // across them) and one ballot. No workgroup barrier anywhere. Latency and instructions bound it, not bytes:
-// 8 tokens of 256 experts in 8 groups 6.3 us, most of it the chain of eight choices and the fp64 scores
-// behind a launch; 4096 tokens of 256 logits 6.2 us (softmax; the bytes alone 0.5), with fp64 keys 10.9; the
-// gradient 6.2. Choices by 64-bit maxima over unsorted keys, sums through LDS and loads behind branches: 7.4,
-// 6.9 and 7.0 us.
+// 8 tokens of 256 experts in 8 groups 5.8 us, most of it the chain of eight choices and the fp64 scores
+// behind a launch; 4096 tokens of 256 logits 5.8 us (softmax; the bytes alone 0.5), with fp64 keys 10.2, with
+// groups 11.6; the gradient 6.0. Choices by 64-bit maxima over unsorted keys, logits carried along, sums
+// through LDS and loads behind branches: 7.4, 6.9 and 7.0 us.
 #include "activation.h"
 #include "moe_layer.h"
 #include "quant_device.h"
@@ -184,8 +184,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
         for (int i = 0; i < V; ++i) {
             k[i] = x[i] == -__builtin_inff() ? -__builtin_inf() : s[i] + (double)bias[i];
         }
-        uint64_t kept = ~0ull;                           // groups that stay
-        int size = p.E;                                  // experts of a group
+        uint64_t kept = ~0ull;                           // bit g * first: group g stays
+        int size = p.E, first = 0;                       // experts of a group
         if (p.groups > 1) {
             size = p.E / p.groups;
             double* keys = group_keys + wave * p.E;
@@ -222,20 +222,22 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
             };
             uint64_t total = a;
             if (a > kNone64 && b > kNone64) total = order_bits(value(a) + value(b));
-            kept = 0;
-            for (int n = 0; n < p.topk_groups; ++n) {    // the best one left, lowest index first
-                const uint64_t mine = g < p.groups && lane % L == 0 && !((kept >> g) & 1) ? total : 0;
-                uint64_t best;
-                const int at = __builtin_ctzll(wave_best(mine, best));
-                if (best <= kNone64) break;
-                kept |= 1ull << (at / L);
+            // a group stays if fewer than topk_groups come before it: a larger sum, or an equal one and a
+            // lower index
+            int before = 0;
+            for (int n = 0; n < p.groups; ++n) {
+                const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(total >> 32), n * L),
+                               lo = __builtin_amdgcn_readlane((uint32_t)total, n * L);
+                const uint64_t other = ((uint64_t)hi << 32) | lo;
+                before += other > total || (other == total && n < g) ? 1 : 0;
             }
+            first = L;
+            kept = __ballot(g < p.groups && total > kNone64 && before < p.topk_groups);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int g = p.groups > 1 ? (lane * V + i) / size : 0;
-            const bool in = g < 64 && ((kept >> (g & 63)) & 1);
-            key[i] = in ? order_bits(k[i]) : 0;
+            const int e = lane * V + i;                  // past E: masked
+            key[i] = e < p.E && (kept >> (e / size * first)) & 1 ? order_bits(k[i]) : 0;
         }
     }
     // Up to six experts a lane are sorted once (stable), so that a choice takes the head of a list.
@@ -250,12 +252,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
             for (int i = 0; i < n; ++i) {
                 const bool swap = key[i + 1] > key[i];
                 const Key k0 = key[i], k1 = key[i + 1];
-                const float x0 = x[i], x1 = x[i + 1];
                 const int e0 = e[i], e1 = e[i + 1];
                 key[i] = swap ? k1 : k0;
                 key[i + 1] = swap ? k0 : k1;
-                x[i] = swap ? x1 : x0;
-                x[i + 1] = swap ? x0 : x1;
                 e[i] = swap ? e1 : e0;
                 e[i + 1] = swap ? e0 : e1;
             }
@@ -263,7 +262,6 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
     }
     // lane j keeps the j-th choice
     int id = -1;
-    float xj = 0.f;
     for (int j = 0; j < p.topk; ++j) {
         Key m = key[0], best;
         if constexpr (!kSorted) {
@@ -274,19 +272,17 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
         if (best <= none) break;                         // uniform: only masked experts are left
         const int at = __builtin_ctzll(lanes);
         int pick = kSorted ? 0 : V - 1;
-        float v = x[pick];
         if constexpr (!kSorted) {
 #pragma unroll
             for (int i = V - 2; i >= 0; --i)
-                if (key[i] == best) { pick = i; v = x[i]; }
+                if (key[i] == best) pick = i;
         }
         const int chosen = __builtin_amdgcn_readlane(kSorted ? e[0] : lane * V + pick, at);
-        const float xe = row_of(v, at);
-        if (lane == j) { id = chosen; xj = xe; }
+        if (lane == j) id = chosen;
         if (lane == at) {
             if constexpr (kSorted) {
 #pragma unroll
-                for (int i = 0; i < V - 1; ++i) { key[i] = key[i + 1]; x[i] = x[i + 1]; e[i] = e[i + 1]; }
+                for (int i = 0; i < V - 1; ++i) { key[i] = key[i + 1]; e[i] = e[i + 1]; }
                 key[V - 1] = 0;
             } else {
 #pragma unroll
@@ -295,13 +291,16 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
             }
         }
     }
+    // its score (a sigmoid of fp32 keys: its logit) from the lane that holds it
+    constexpr bool kFromLogit = SG && !K64;
     Real w = 0;
-    if (id >= 0) {
-        if constexpr (SG && K64) w = inverse_f64(1.0 + exp(-(double)xj));
-        else if constexpr (SG) w = sigmoid_f32(xj);
-        else if constexpr (K64) w = exp((double)xj - top) * rsum;
-        else w = expf(xj - top) * rsum;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const Real v = __shfl(kFromLogit ? (Real)x[i] : s[i], (id < 0 ? 0 : id) / V, 64);
+        if (id % V == i) w = v;
     }
+    if constexpr (kFromLogit) w = sigmoid_f32(w);
+    if (id < 0) w = 0;
     if (p.renorm) {
         w = w / (wave_total(w) + (Real)kRouteEps);
     }
