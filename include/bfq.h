@@ -487,7 +487,8 @@ bfq_status bfq_norm_residual_backward(const void* y, const void* res_out, bfq_dt
  * A pair without a row (pair_rows[q] outside [0, R), or in pair order an id outside [0, E)) is left
  * out: it adds nothing, whatever its weight, and its row is neither read nor written. In what is
  * written, each row is some pair's at most once, as bfq_moe_sort's places are; where two pairs share
- * one, its contents are those of either, mixed. With R = 0 every tensor over rows may be NULL. K a positive multiple of 8, of 128 where codes are
+ * one, its contents are those of either, mixed. With R = 0 every tensor over rows may be NULL. What belongs to
+ * a token does not depend on T, and equal calls give equal bits. K a positive multiple of 8, of 128 where codes are
  * read or written, at most 2^23. */
 
 /* Router: s = score(logits) over a token's E experts, the topk largest keys in descending order

@@ -165,6 +165,23 @@ def test_backward_from_exact_checkpoint_equals_the_plain_one(bfq, act):
     assert float((dpre2 != dpre).float().mean()) < 1e-3 and float((h2 != h).float().mean()) < 1e-3
 
 
+@pytest.mark.parametrize("act", [0, 1])
+def test_large_calls_equal_small_ones(bfq, act):
+    """Calls that write more than the L2s hold store past them: their rows are those of a small call, bit for bit."""
+    M, F = 9000, 2048
+    pre = (_randn(1, M, 2 * F) * 2).bfloat16()
+    dh = (_randn(2, M, F) * 1e-2).bfloat16()
+    some = torch.linspace(0, M - 1, 40, device=DEV).long()
+    for codes in (False, True):
+        for ct in (bfq.BFQ_E4M3FN, bfq.BFQ_INT8):
+            a = bfq.gated_checkpoint(pre, act=act, codes=codes, ckpt_dtype=ct)
+            b = bfq.gated_checkpoint(pre[some], act=act, codes=codes, ckpt_dtype=ct)
+            assert len(a) == len(b) and all(torch.equal(x[some], y) for x, y in zip(a, b))
+            ga = bfq.gated_checkpoint_backward(a[-2], a[-1], dh, act=act, codes=codes, want_h=True)
+            gb = bfq.gated_checkpoint_backward(b[-2], b[-1], dh[some], act=act, codes=codes, want_h=True)
+            assert len(ga) == len(gb) and all(torch.equal(x[some], y) for x, y in zip(ga, gb))
+
+
 def test_checkpoint_extremes(bfq):
     """Zeros, infinities, NaN, saturated gates; fewer live rows than none and more than all."""
     pre = torch.zeros((4, 512), dtype=torch.bfloat16, device=DEV)

@@ -376,6 +376,99 @@ def test_dispatch_and_combine_are_transposes(bfq):
     assert float((rows[:n].double() * g[:n].double()).sum()) == float((x.double() * dx.double()).sum())
 
 
+@pytest.mark.parametrize("T,topk,K", [(1100, 8, 4096), (5000, 2, 4096), (1030, 64, 640)])
+def test_large_calls_equal_small_ones(bfq, T, topk, K):
+    """Calls that write more than the L2s hold store past them and take eight pairs at a time: the rows of a few
+    tokens are those of a call of their own, bit for bit."""
+    R, G = T * topk, K // 128
+    assert R * K > 32 << 20
+    ids = torch.randint(-8, 24, (T, topk), generator=_gen(1), device=DEV, dtype=torch.int32)
+    _, _, at = bfq.moe_sort(ids, 16)
+    some = torch.tensor([0, 1, T // 2, T - 2, T - 1], device=DEV)
+    live = at[some] >= 0
+    rows_of = at[some][live].long()
+    # the same pairs in a call of five tokens: their rows in a small tensor
+    few = torch.where(live, torch.arange(5 * topk, device=DEV, dtype=torch.int32).view(5, topk), -1).int()
+    few_rows = few[live].long()
+    x = _randn(2, T, K).bfloat16()
+    w = torch.rand((T, topk), generator=_gen(3), device=DEV)
+
+    def small(big):
+        t = torch.zeros((5 * topk, *big.shape[1:]), dtype=big.dtype, device=DEV)
+        t[few_rows] = big[rows_of]
+        return t
+
+    def same(a, b, what):
+        assert torch.equal(_bits(a), _bits(b)), what
+
+    rows, rq, rs = torch.zeros((R, K), dtype=torch.bfloat16, device=DEV), torch.zeros((R, K), dtype=torch.uint8, device=DEV), torch.zeros((R, G), device=DEV)
+    bfq.bfq_moe_dispatch(x, at, rows=rows)
+    same(rows[rows_of], bfq.moe_dispatch(x[some], few)[few_rows], "dispatch")
+    bfq.bfq_moe_dispatch(x, at, rows=rows, q=rq, scales=rs)
+    q2, s2 = bfq.moe_dispatch(x[some], few, codes=True)
+    same(rq[rows_of], q2[few_rows], "codes")
+    same(rs[rows_of], s2[few_rows], "scales")
+    same(rows[rows_of], bfq.moe_dispatch(x[some], few)[few_rows], "rows beside codes")
+    xq, xs = bfq.quant_tokens(x)
+    cq = torch.zeros_like(rq)
+    bfq.bfq_moe_dispatch(xq, at, q=cq, scales=torch.zeros_like(rs), x_scales=xs)
+    same(cq, rq, "copied codes")
+    wide = rows.float() if R * K < 40 << 20 else None
+    for r in (rows,) if wide is None else (rows, wide):
+        for ct in (None, bfq.BFQ_E4M3FN, bfq.BFQ_INT8):
+            a = bfq.moe_combine(r, topk, weights=w, pair_rows=at, base=x, ckpt_dtype=ct)
+            b = bfq.moe_combine(small(r), topk, weights=w[some], pair_rows=few, base=x[some], ckpt_dtype=ct)
+            a, b = ((a,), (b,)) if ct is None else (a, b)
+            same(a[0][some], b[0], "combine")
+            for u, v in zip(a[1:], b[1:]):
+                same(u[rows_of], v[few_rows], "checkpoint")
+    for kw, kws in ((dict(rows=rows), dict(rows=small(rows))), (dict(rows=rq, rows_scales=rs), dict(rows=small(rq), rows_scales=small(rs)))):
+        for codes in (False, True):
+            a = bfq.moe_combine_backward(x, topk, weights=w, pair_rows=at, codes=codes, **kw)
+            b = bfq.moe_combine_backward(x[some], topk, weights=w[some], pair_rows=few, codes=codes, **kws)
+            same(a["d_weights"][some], b["d_weights"], "d_weights")
+            for k in set(a) - {"d_weights"}:
+                same(a[k][rows_of], b[k][few_rows], k)
+
+
+@pytest.mark.parametrize("T", [9, 1300])
+@pytest.mark.parametrize("kind", ["bf16", "codes", "none"])
+def test_gradient_as_rows_and_codes_at_once(bfq, T, kind):
+    topk, K = 5, 640
+    rows, w, at, live, used, kw = _combine_inputs(T, topk, K, "expert", torch.bfloat16, True, 31)
+    d = _randn(8, T, K).bfloat16()
+    R = rows.shape[0]
+    more = {}
+    if kind != "none":
+        more = dict(rows=rows, d_weights=torch.empty((T, topk), device=DEV))
+    if kind == "codes":
+        q, s = bfq.quant_tokens(torch.nan_to_num(rows))
+        more.update(rows=q, rows_scales=s)
+    dr, q, s = torch.zeros((R, K), dtype=torch.bfloat16, device=DEV), torch.zeros((R, K), dtype=torch.uint8, device=DEV), torch.zeros((R, K // 128), device=DEV)
+    bfq.bfq_moe_combine_backward(d, topk, weights=w, d_rows=dr, q=q, scales=s, **kw, **more)
+    z = (w.unsqueeze(2) * d.float().unsqueeze(1))[live]
+    zq, zs = _quant(z, False, False)
+    assert torch.equal(_bits(dr[at[live]]), _bits(z.bfloat16())) and torch.equal(q[at[live]], zq) and torch.equal(s[at[live]], zs)
+    assert not bool(dr[~used].any()) and not bool(q[~used].any()) and not bool(s[~used].any())
+
+
+def test_scale_floor(bfq):
+    """q_eps floors every scale that is written."""
+    x = (_randn(1, 6, 256) * 0.01).bfloat16()
+    at = torch.arange(6, device=DEV, dtype=torch.int32).view(6, 1)
+    tq, ts = torch.empty((6, 256), dtype=torch.uint8, device=DEV), torch.empty((6, 2), device=DEV)
+    bfq.bfq_quant_tokens(x, tq, ts, eps=0.5)
+    assert bool((ts == 0.5 / torch.full_like(ts, 448.0)).all())
+    out = torch.empty_like(x)
+    for call in (lambda q, s: bfq.bfq_moe_dispatch(x, at, q=q, scales=s, q_eps=0.5),
+                 lambda q, s: bfq.bfq_moe_combine(x, out, 1, ckpt=q, ckpt_scales=s, q_eps=0.5),
+                 lambda q, s: bfq.bfq_moe_combine_backward(x, 1, q=q, scales=s, q_eps=0.5),
+                 lambda q, s: bfq.bfq_gated_checkpoint(x, ckpt=q, ckpt_scales=s, q_eps=0.5)):
+        q, s = torch.zeros_like(tq), torch.zeros_like(ts)
+        call(q, s)
+        assert torch.equal(q, tq) and torch.equal(s, ts)
+
+
 def test_pairs_that_share_a_row(bfq):
     """Reading, a row may be several pairs'; a token may name one twice."""
     T, topk, K, R = 40, 4, 264, 5
