@@ -389,7 +389,7 @@ __device__ __forceinline__ int here(int x) {
     return x;
 }
 
-// A workgroup takes a token's whole row, because the weights' gradients are sums over it; eight pairs
+// A workgroup takes a token's whole row, because the weights' gradients are sums over it; NB pairs
 // at a time, their rows in flight together. The codes of w * dout come from one maximum for all
 // pairs: rounding is monotone, so the largest |w * dout| is |w| times the largest |dout|, rounded.
 // Columns of a thread: 16 where rows of codes are read and written (16-byte loads and stores), else 8. A pair
@@ -398,7 +398,7 @@ __device__ __forceinline__ int here(int x) {
 // in 107 to 113 us (4.8 to 5.1 TB/s; a large copy 5.2). Rows through buffer resources, eight times four
 // scalar registers that spilled, 8 columns a thread: 142 us; scalar bases and 16 columns, 448 threads
 // a token: 121; at most 256 threads, two rounds a row and more tokens on a CU: 107 (192: 114, 128: 114,
-// 64: 108; batches of four pairs: 109). One size for every batch: a token's sums do not depend on T.
+// 64: 108). The block depends on the width and the types alone: a token's sums do not depend on T.
 template <int RK, int Q, int NB, int S>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
     constexpr int U = (RK == R_FP8 || RK == R_INT8) && Q >= 0 ? 2 : 1, W = 8 * U, LG = 16 / U;   // lanes of a group
@@ -532,19 +532,28 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
     }
 }
 
-// Two pairs at a time where a token has no more (4096 tokens, 2 pairs: 52 -> 38 us), and, as workgroups of
-// their own, where tokens are few (212 tokens, 8 pairs: 16 -> 11 us; at 2000 tokens the gradient that each of
-// them reads again makes it 58 -> 68). A pair's sum is the same either way.
-template <int RK, int Q> static void combine_bwd_s(const CombineBwdArgs& a, hipStream_t stream) {
+template <int RK, int Q, int NB> static void combine_bwd_nb(const CombineBwdArgs& a, unsigned ys, hipStream_t stream) {
     const int64_t chunks = a.K / ((RK == R_FP8 || RK == R_INT8) && Q >= 0 ? 16 : 8), rounds = (chunks + 255) / 256;
     const dim3 block((unsigned)(((chunks + rounds - 1) / rounds + 63) / 64 * 64));
-    const bool two = a.at.topk <= 2 || a.T < 1024;
-    const dim3 grid((unsigned)(a.T + (Q >= 0 && a.out.packed ? (4 - a.at.R % 4) % 4 : 0)), two ? (a.at.topk + 1) / 2 : 1);
-    const bool past = past_caches(a.at.R * a.K * ((a.d_rows ? 2 : 0) + (Q >= 0 ? 1 : 0)));
-    if (two && past) hipLaunchKernelGGL((combine_bwd_kernel<RK, Q, 2, 1>), grid, block, 0, stream, a);
-    else if (two) hipLaunchKernelGGL((combine_bwd_kernel<RK, Q, 2, 0>), grid, block, 0, stream, a);
-    else if (past) hipLaunchKernelGGL((combine_bwd_kernel<RK, Q, 8, 1>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((combine_bwd_kernel<RK, Q, 8, 0>), grid, block, 0, stream, a);
+    const dim3 grid((unsigned)(a.T + (Q >= 0 && a.out.packed ? (4 - a.at.R % 4) % 4 : 0)), ys);
+    if (past_caches(a.at.R * a.K * ((a.d_rows ? 2 : 0) + (Q >= 0 ? 1 : 0))))
+        hipLaunchKernelGGL((combine_bwd_kernel<RK, Q, NB, 1>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((combine_bwd_kernel<RK, Q, NB, 0>), grid, block, 0, stream, a);
+}
+// Pairs at a time, and with them the workgroups a token gets: each reads the token's gradient again, and more
+// of them fill the card where tokens are few. 7168 columns, rows and codes of 8 bits, 2 | 4 | 8 at a time:
+// 8 pairs a token, 300 tokens 13.5 | 15.5 us, 500: 20.1 | 18.6, 1100: 40.2 | 36.8 | 40.8, 2000: 67 | 58.9 | 58.5,
+// 4096: 130 | 110.6 | 109.4; 4 pairs a token, 600 tokens 13.4 | 15.6, 1100: 21.9 | 19.9, 4096: 68.6 | 59.9 | 70.6.
+// Without the weights' gradient 8192 tokens of 8 pairs: 162 | 146 | 141; rows or output in bf16 take 4 or 8 alike
+// (4096 tokens, bf16 in, codes out: 153 | 150 | 153). A pair's sum is the same in each.
+template <int RK, int Q> static void combine_bwd_s(const CombineBwdArgs& a, hipStream_t stream) {
+    const int64_t pairs = a.T * a.at.topk;
+    if (a.at.topk <= 2 || pairs < 3600) combine_bwd_nb<RK, Q, 2>(a, (a.at.topk + 1) / 2, stream);
+    else {
+        if constexpr (Q >= 0 && (RK == R_FP8 || RK == R_INT8 || RK == R_NONE))
+            if (a.at.topk > 4 && pairs >= 24000) return combine_bwd_nb<RK, Q, 8>(a, 1, stream);
+        combine_bwd_nb<RK, Q, 4>(a, (a.at.topk + 3) / 4, stream);
+    }
 }
 template <int RK> static void combine_bwd_rk(const CombineBwdArgs& a, hipStream_t stream) {
     if (!a.out.q) combine_bwd_s<RK, -1>(a, stream);

@@ -378,7 +378,7 @@ def test_dispatch_and_combine_are_transposes(bfq):
 
 @pytest.mark.parametrize("T,topk,K", [(1100, 8, 4096), (5000, 2, 4096), (1030, 64, 640)])
 def test_large_calls_equal_small_ones(bfq, T, topk, K):
-    """Calls that write more than the L2s hold store past them and take eight pairs at a time: the rows of a few
+    """Calls that write more than the L2s hold store past them and take more pairs at a time: the rows of a few
     tokens are those of a call of their own, bit for bit."""
     R, G = T * topk, K // 128
     assert R * K > 32 << 20
@@ -450,6 +450,38 @@ def test_gradient_as_rows_and_codes_at_once(bfq, T, kind):
     zq, zs = _quant(z, False, False)
     assert torch.equal(_bits(dr[at[live]]), _bits(z.bfloat16())) and torch.equal(q[at[live]], zq) and torch.equal(s[at[live]], zs)
     assert not bool(dr[~used].any()) and not bool(q[~used].any()) and not bool(s[~used].any())
+
+
+@pytest.mark.parametrize("kind", ["none", "bf16", "codes"])
+@pytest.mark.parametrize("topk", [3, 6, 9])
+def test_gradients_do_not_depend_on_the_tokens_beside(bfq, kind, topk):
+    """Calls of few and of many pairs take two, four or eight of a token's at a time, some batches short: a
+    token's gradients are the same bits in each."""
+    T, K, G = 4100, 256, 2
+    w = torch.rand((T, topk), generator=_gen(1), device=DEV) - 0.3
+    d = _randn(2, T, K)
+    at = _places(T, topk, T * topk, True, 3)
+    rows = _randn(4, T * topk, K).bfloat16()
+    kw = {} if kind == "none" else dict(rows=rows) if kind == "bf16" else dict(zip(("rows", "rows_scales"), bfq.quant_tokens(rows)))
+
+    def run(n, codes):
+        dw = torch.full((n, topk), 7.0, device=DEV) if kw else None
+        q, s = torch.full((T * topk, K), 9, dtype=torch.uint8, device=DEV), torch.full((T * topk, G), 9.0, device=DEV)
+        dr = torch.full((T * topk, K), 9.0, dtype=torch.bfloat16, device=DEV)
+        form = dict(q=q, scales=s) if codes else dict(d_rows=dr)
+        bfq.bfq_moe_combine_backward(d[:n], topk, weights=w[:n].contiguous(), pair_rows=at[:n].contiguous(), d_weights=dw, **form, **kw)
+        return dw, (q, s) if codes else (dr,)
+
+    for codes in (False, True):
+        dw, full = run(T, codes)
+        for n in (1, 100, 1300, 2900):
+            dn, part = run(n, codes)
+            live = at[:n][(at[:n] >= 0) & (at[:n] < T * topk)].long()
+            assert dw is None or torch.equal(_bits(dn), _bits(dw[:n]))
+            for a, b in zip(part, full):
+                assert torch.equal(_bits(a[live]), _bits(b[live]))
+                a[live] = 9
+                assert bool((a.float() == 9).all())
 
 
 def test_scale_floor(bfq):
