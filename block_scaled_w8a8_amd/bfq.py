@@ -914,17 +914,23 @@ _device_now = _stream_now = None    # torch's calls for them, once its GPU runti
 
 
 def _runtime() -> int:
-    """The current GPU; -2, which no tensor is on, while the runtime is not initialised."""
-    global _device_now, _stream_now, _T_I32, _T_F32, _T_BF16, _T_OUT, _T_RES, _T_CODES, _T_ROWS
+    """The current GPU; -2, which no tensor is on, while the runtime is not initialised.
+
+    Threads may make their first calls at once: what tells that the tables are there is assigned after
+    them (_TYPE_NAMES), and _device_now, by which later calls skip this, last of all. Two threads that
+    both fill them assign equal ones."""
+    global _device_now, _stream_now, _TYPE_NAMES, _T_I32, _T_F32, _T_BF16, _T_OUT, _T_RES, _T_CODES, _T_ROWS
     torch = _torch_module()
     if not _TYPE_NAMES:
-        for names in (("int32",), ("float32",), ("bfloat16",), OUT_DTYPES, RES_DTYPES, CODE_DTYPES, ROW_DTYPES):
-            _TYPE_NAMES[frozenset(getattr(torch, n) for n in names)] = names
-        _T_I32, _T_F32, _T_BF16, _T_OUT, _T_RES, _T_CODES, _T_ROWS = _TYPE_NAMES
+        kinds = (("int32",), ("float32",), ("bfloat16",), OUT_DTYPES, RES_DTYPES, CODE_DTYPES, ROW_DTYPES)
+        types = {frozenset(getattr(torch, n) for n in names): names for names in kinds}
         _KINDS.update((getattr(torch, n), k) for n, k in (*_CODE_TYPES.items(), *_OUT_TYPES.items()))
+        _T_I32, _T_F32, _T_BF16, _T_OUT, _T_RES, _T_CODES, _T_ROWS = types
+        _TYPE_NAMES = types
     if not torch.cuda.is_initialized():
         return -2
-    _device_now, _stream_now = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _stream_now = torch._C._cuda_getCurrentRawStream
+    _device_now = torch._C._cuda_getDevice
     return _device_now()
 
 
