@@ -420,15 +420,18 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
     const uint32_t chunks = (uint32_t)(K / W);
     for (int j0 = blockIdx.y * NB; j0 < p.at.topk; j0 += gridDim.y * NB) {
         const uint32_t alive = (uint32_t)(there >> j0) & ((1u << NB) - 1);
-        float acc[NB];
+        float acc[NB], w[NB];
         int r[NB];
-        // lane k of a group stores pair k's scale (taken here, where every lane of the wave takes part)
+        // lane k of a group stores pair k's scale (taken here, where every lane of the wave takes part, as the
+        // pairs' rows and weights are: below, lanes past the row's end are switched off, and what a register
+        // holds for such a lane is the compiler's to lose)
         const int k = lane & (LG - 1), rs = __shfl(place, (j0 + k) & 63, 64);
         const int some = alive ? __builtin_amdgcn_readlane(place, j0 + __builtin_ctz(alive)) : 0;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             acc[i] = 0.f;
             r[i] = (alive >> i) & 1 ? __builtin_amdgcn_readlane(place, (j0 + i) & 63) : some;
+            w[i] = lane_f32(weight, (j0 + i) & 63);
         }
         for (uint32_t c0 = 0; alive && c0 < chunks; c0 += blockDim.x) {
             const uint32_t c = c0 + tid;
@@ -465,7 +468,6 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 if (!((alive >> i) & 1)) continue;       // uniform
-                const float w = lane_f32(weight, (j0 + i) & 63);
                 const int64_t ri = here(r[i]);
                 if constexpr (RK != R_NONE) {
                     float s = 0.f;
@@ -485,7 +487,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
                 }
                 float z[W];
 #pragma unroll
-                for (int n = 0; n < W; ++n) z[n] = w * d[n];
+                for (int n = 0; n < W; ++n) z[n] = w[i] * d[n];
                 if (p.d_rows) {
                     uint8_t* row = static_cast<uint8_t*>(p.d_rows) + ri * (2 * K);
 #pragma unroll
@@ -496,7 +498,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
                     }
                 }
                 if constexpr (Q >= 0) {
-                    uint32_t mx = __float_as_uint(w * __uint_as_float(md)) & 0x7FFFFFFFu;
+                    uint32_t mx = __float_as_uint(w[i] * __uint_as_float(md)) & 0x7FFFFFFFu;
                     if (mx >= 0x7F800000u)               // the lanes of a group agree
                         mx = group_max<LG>(U == 2 ? max(amax8(z), amax8(z + W - 8)) : amax8(z));
                     const float s = group_scale<Q>(mx, p.out.eps, p.out.ue8m0);
