@@ -44,7 +44,8 @@ bfq_status check_places(const int32_t* pair_rows, const int32_t* topk_ids, int32
                         int64_t R, PairPlaces* at) {
     if (pair_rows && topk_ids) return fail(BFQ_ERR_ARG, "pair_rows says which pairs exist: topk_ids must be NULL");
     if (topk_ids && E < 1) return fail(BFQ_ERR_SHAPE, "topk_ids need E >= 1");
-    if (!pair_rows && R != T * topk) return fail(BFQ_ERR_SHAPE, "rows in pair order: R must be T * topk");
+    // of an empty batch the places are an empty tensor, NULL: both orders are the same there
+    if (!pair_rows && T != 0 && R != T * topk) return fail(BFQ_ERR_SHAPE, "rows in pair order: R must be T * topk");
     if (!aligned(pair_rows, 4) || !aligned(topk_ids, 4)) return fail(BFQ_ERR_ALIGN, "int32 buffers must be 4-byte aligned");
     *at = PairPlaces{pair_rows, topk_ids, E, topk, R};
     return BFQ_OK;
