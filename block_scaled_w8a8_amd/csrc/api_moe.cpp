@@ -30,6 +30,9 @@ bfq_status check_codes(void* q, bfq_dtype q_dtype, float* scales, bfq_scale_layo
     return BFQ_OK;
 }
 
+// An empty batch still writes the zero words of rows R .. round_up(R, 4) - 1.
+bool only_padding(const CodesOut& o, int64_t T, int64_t R) { return T == 0 && o.packed && o.scales && R % 4 != 0; }
+
 bfq_status check_tokens(int64_t T, int32_t topk, int64_t K, int64_t R) {
     if (T < 0 || T >= kMoeMaxTokens) return fail(BFQ_ERR_SHAPE, "need 0 <= T < 2^22");
     if (topk < 1 || topk > kMoeMaxTopk) return fail(BFQ_ERR_SHAPE, "need 1 <= topk <= 64");
@@ -184,7 +187,7 @@ bfq_status bfq_moe_dispatch(const void* x, bfq_dtype x_dtype, const float* x_sca
             return fail(BFQ_ERR_ARG, "unknown scale layout");
         }
     }
-    if (!some) return BFQ_OK;
+    if (!some && !only_padding(a.out, T, R)) return BFQ_OK;
     a.x = x;
     a.x_scales = copy ? x_scales : nullptr;
     a.T = T;
@@ -267,7 +270,7 @@ bfq_status bfq_moe_combine_backward(const void* dout, bfq_dtype dout_dtype, cons
     if (!aligned(dout, 16) || !aligned(rows, 16) || !aligned(d_rows, 16) || !aligned(q, 16) || !aligned(scales, 4) ||
         !aligned(rows_scales, 4) || !aligned(weights, 4) || !aligned(d_weights, 4))
         return fail(BFQ_ERR_ALIGN, "row tensors must be 16-byte aligned, weights and scales 4-byte");
-    if (!some) {                                         // without a row the weights have no gradient
+    if (!some && !only_padding(a.out, T, R)) {           // without a row the weights have no gradient
         if (T == 0 || !d_weights) return BFQ_OK;
         a.row_kind = R_BF16;
         a.out = CodesOut{};

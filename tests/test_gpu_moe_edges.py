@@ -55,3 +55,24 @@ def test_weights_of_lanes_past_the_row(bfq, T, topk, K, kind):
         zq, zs = _codes(z.view(R, K))
         p = at.reshape(-1).long()
         assert torch.equal(g["q"][p], zq) and torch.equal(g["scales"][p], zs)
+
+
+@pytest.mark.parametrize("R", [1, 6, 8])
+def test_empty_batch_writes_the_words_past_the_last_row(bfq, R):
+    """Packed scales of a batch without tokens: the rows' words stay, those up to the next multiple of four are zero."""
+    K, R4 = 640, (R + 3) // 4 * 4
+    at = torch.empty((0, 2), dtype=torch.int32, device=DEV)
+    q = torch.full((R, K), 9, dtype=torch.uint8, device=DEV)
+    form = dict(layout=bfq.BFQ_SCALES_PACKED_UE8M0, scale_fmt=bfq.BFQ_SCALE_UE8M0)
+    x, w = torch.empty((0, K), dtype=torch.bfloat16, device=DEV), torch.empty((0, 2), device=DEV)
+    xs = torch.empty((2, 4), dtype=torch.int32, device=DEV)
+    for call in (lambda s: bfq.bfq_moe_dispatch(x, at, q=q, scales=s, **form),
+                 lambda s: bfq.bfq_moe_dispatch(x.view(torch.uint8)[:, :K].contiguous(), at, q=q, scales=s, x_scales=xs, x_layout=form["layout"],
+                                                x_scale_ld=4, **form),
+                 lambda s: bfq.bfq_moe_combine_backward(x, 2, pair_rows=at, q=q, scales=s, **form),
+                 lambda s: bfq.bfq_moe_combine_backward(x, 2, weights=w, pair_rows=at, rows=torch.zeros((R, K), dtype=torch.bfloat16, device=DEV),
+                                                        d_weights=w, q=q, scales=s, **form)):
+        s = torch.full((2, R4 + 4), 0x0BADBEEF, dtype=torch.int32, device=DEV)
+        call(s)
+        assert bool((s[:, :R] == 0x0BADBEEF).all()) and not bool(s[:, R:R4].any()) and bool((s[:, R4:] == 0x0BADBEEF).all())
+        assert bool((q == 9).all())
