@@ -1,7 +1,11 @@
 """GPU tests of the mixture-of-experts operators where rows are narrow or end inside a wave, batches empty,
 experts many: calls that the documentation allows and that are seldom made."""
+import math
+
 import pytest
 import torch
+
+import test_gpu_moe_route as route
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -76,3 +80,69 @@ def test_empty_batch_writes_the_words_past_the_last_row(bfq, R):
         call(s)
         assert bool((s[:, :R] == 0x0BADBEEF).all()) and not bool(s[:, R:R4].any()) and bool((s[:, R4:] == 0x0BADBEEF).all())
         assert bool((q == 9).all())
+
+
+# ------------------------------------------------------------------ routers of many experts
+
+@pytest.mark.parametrize("E,topk", [(300, 8), (384, 64), (385, 2), (448, 8), (512, 6), (512, 64), (513, 8)])
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("form", ["plain", "bias", "groups", "ties"])
+def test_route_of_many_experts(bfq, E, topk, score, form):
+    """Every choice after the first from lists of six, eight and sixteen experts a lane, logits that repeat,
+    masked experts."""
+    T, groups, kept = 21, 1, 1
+    x = _randn(E, T, E) * 2
+    if form == "ties":                                       # eight values for all the experts
+        x = torch.randint(-4, 4, (T, E), generator=_gen(1), device=DEV).float()
+    if form == "groups":
+        groups = next(g for g in (8, 7, 5, 3) if E % g == 0)
+        kept = -(-topk * groups // E) + 1
+    x[:, 3::11] = -math.inf
+    x[5, topk // 2 + 1:] = -math.inf                          # fewer than topk are left (of two: both)
+    b = 0.2 * _randn(4, E) if form == "bias" else None
+    renorm = topk > 2
+    ids, w = bfq.moe_route(x, topk, bias=b, score=score, n_groups=groups, topk_groups=kept, renorm=renorm, weight_scale=2.5)
+    rid, rw = route._reference(x, topk, b, score, groups, kept, renorm, 2.5)
+    assert torch.equal(ids.long(), rid)
+    assert bool((ids[5] == -1).any()) == (topk > 2) and bool((ids[0] >= 0).any())
+    assert bool(((w.double() - rw).abs() <= rw.abs() * U * (2 * route._spread(x) + 32)).all())
+
+
+@pytest.mark.parametrize("E,topk", [(65, 6), (100, 8), (128, 64), (257, 8), (300, 6), (384, 64), (385, 2), (448, 8), (512, 64)])
+@pytest.mark.parametrize("score,renorm", [(0, False), (0, True), (1, False), (1, True)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_route_backward_of_many_experts(bfq, E, topk, score, renorm, dt):
+    """Against the formula in 64 bits, by autograd; an expert named twice, pairs that went elsewhere."""
+    T = 19
+    x = (_randn(E, T, E) * 2).to(dt)
+    x[:, 5::13] = -math.inf
+    ids, _ = bfq.moe_route(x, topk, score=score, renorm=renorm)
+    ids[::3, -1] = -1
+    ids[4, 1] = ids[4, 0]
+    ids[3, 0] = E
+    gw = _randn(5, T, topk)
+    gw[ids < 0] = math.nan
+    d = bfq.moe_route_backward(x, ids, gw, score=score, renorm=renorm, weight_scale=1.5)
+    live = (ids >= 0) & (ids < E)
+    at, g = ids.long().clamp(0, E - 1), torch.where(live, gw, 0.0).double()
+    x64 = x.double().requires_grad_()
+    s = torch.sigmoid(x64) if score else torch.softmax(x64, dim=1)
+    w = s.gather(1, at) * live
+    if renorm:
+        w = w / (w.sum(dim=1, keepdim=True) + 1e-20)
+    (1.5 * w * g).sum().backward()
+    p, ref = s.detach(), x64.grad
+    sj = p.gather(1, at) * live
+    # the terms that are summed: A_j of ds_j, and their mean under the softmax
+    A = 1.5 * g.abs()
+    if renorm:
+        D = sj.sum(dim=1, keepdim=True) + 1e-20
+        A = A * sj.sum(dim=1, keepdim=True) / D ** 2 + 1.5 * (g.abs() * sj).sum(dim=1, keepdim=True) / D ** 2 + A * 1e-20 / D ** 2
+    A = torch.where(live, A, 0.0)
+    dense = torch.zeros_like(p).scatter_add_(1, at, A)
+    terms = dense * p * (1 - p) if score else p * (dense + (A * sj).sum(dim=1, keepdim=True))
+    # a score: the difference to the largest (u of it in the exponential), 16 additions in a lane, 6 over the wave,
+    # a division, some 32 u in all, three times over in ds; then topk additions; one rounding to the output
+    tol = terms * U * ((0 if score else 4) * route._spread(x) + 96 + 2 * topk) + torch.finfo(dt).eps / 2 * ref.abs() + 2.0 ** -133
+    assert bool(((d.double() - ref).abs() <= tol).all()), float(((d.double() - ref).abs() / tol).max())
+    assert bool((ref.abs() > tol).any(dim=1)[1])              # zeros would not pass for the tokens left as they were
