@@ -5,8 +5,8 @@
 
 namespace bfq {
 
-// Experts a token may have, and rows a call may have: a pair is a lane of a wave, and a grid
-// dimension holds fewer than 2^32 threads at 1024 a token.
+// Experts a token may have, and tokens a call may have: a pair is a lane of a wave, a grid dimension
+// holds fewer than 2^32 threads (at most 256 a token), and a pair's number (below 2^28) fits an int32.
 constexpr int kMoeMaxTopk = 64;
 constexpr int64_t kMoeMaxTokens = int64_t(1) << 22;
 constexpr int64_t kMoeMaxK = int64_t(1) << 23;

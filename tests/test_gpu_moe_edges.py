@@ -146,3 +146,32 @@ def test_route_backward_of_many_experts(bfq, E, topk, score, renorm, dt):
     tol = terms * U * ((0 if score else 4) * route._spread(x) + 96 + 2 * topk) + torch.finfo(dt).eps / 2 * ref.abs() + 2.0 ** -133
     assert bool(((d.double() - ref).abs() <= tol).all()), float(((d.double() - ref).abs() / tol).max())
     assert bool((ref.abs() > tol).any(dim=1)[1])              # zeros would not pass for the tokens left as they were
+
+
+# -------------------------------------------------------------- sums of the weights' gradient
+
+@pytest.mark.parametrize("T,topk,K", [(2, 3, 264), (2, 3, 2048), (3, 9, 2056), (3, 10, 12288), (2, 5, 16384), (500, 9, 4224)])
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32", "codes"])
+@pytest.mark.parametrize("codes", [False, True])
+def test_roundings_of_the_weights_gradient(bfq, T, topk, K, kind, codes):
+    """Counted on the kernel's sum: a thread takes W = 8 columns a round (16 from codes to codes), W products, one
+    addition to what earlier rounds gave, for rows of codes one product with the scale; at most 256 threads, so
+    ceil(K / (256 W)) rounds; 6 additions over a wave and one less than the waves over them."""
+    if K % 128 and (codes or kind == "codes"):
+        K = K // 128 * 128 + 128
+    R = T * topk
+    at = torch.randperm(R, generator=_gen(1), device=DEV).int().view(T, topk)
+    d, w = _randn(2, T, K), torch.rand((T, topk), generator=_gen(3), device=DEV)
+    rows = _randn(4, R, K).to({"fp16": torch.float16, "fp32": torch.float32}.get(kind, torch.bfloat16))
+    kw, value = dict(rows=rows), rows.double()
+    if kind == "codes":
+        q, s = bfq.quant_tokens(rows)
+        kw = dict(rows=q, rows_scales=s)
+        value = q.view(torch.float8_e4m3fn).double() * s.double().repeat_interleave(128, dim=1)
+    dw = bfq.moe_combine_backward(d, topk, weights=w, pair_rows=at, codes=codes, **kw)["d_weights"]
+    W = 16 if kind == "codes" and codes else 8
+    count = W + (kind == "codes") + (-(-K // (256 * W)) - 1) + 6 + 3
+    terms = value[at.long()] * d.double().unsqueeze(1)
+    ref, tol = terms.sum(dim=2), terms.abs().sum(dim=2) * U * count * (1 + 64 * U)
+    assert bool(((dw.double() - ref).abs() <= tol).all()), float(((dw.double() - ref).abs() / tol).max())
+    assert float((ref.abs() > tol).float().mean()) > 0.9
