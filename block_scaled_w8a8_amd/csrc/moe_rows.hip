@@ -7,8 +7,9 @@
 //   d_rows[r(t, j)] = w[t][j] dout[t],  dw[t][j] = <dout[t], rows[r(t, j)]>
 //
 // All but the sort are bound by bytes. A workgroup takes a token, not a row: what belongs to the
-// token (its row, its codes, its gradient) is read and formed once and written topk times, or read
-// topk times and summed in registers in pair order: no atomics, equal calls give equal bits.
+// token (its row, its codes) is read and formed once and written topk times, or topk rows are read
+// and summed in registers in pair order: no atomics, equal calls give equal bits. In the combine's
+// gradient a workgroup takes two, four or eight of a token's pairs, and each reads the token's gradient.
 #include "row_access.h"
 
 namespace bfq {
@@ -199,7 +200,7 @@ __global__ __launch_bounds__(256) void dispatch_rows_kernel(DispatchArgs p) {
 // a thread, so 8 lanes hold a group and every lane knows its scale; lane k of the group stores the
 // scale of pair k, k + 8, ..: one store for eight rows. Packed scales: 32 lanes hold a word. Blocks
 // past the tokens write the zero words of rows R .. round_up(R, 4) - 1. Bytes bound it: 4096 x 7168 to
-// eight rows each, 301 MB in 61 us (4.9 TB/s; a large copy 5.2) with row-major scales, 69 us with
+// eight rows each, 301 MB in 61 us (4.9 TB/s; a large copy 4.8 to 5.4) with row-major scales, 69 us with
 // column-major ones, whose neighbours belong to other tokens.
 template <int Q, int S>
 __global__ __launch_bounds__(256) void dispatch_codes_kernel(DispatchArgs p) {
@@ -262,13 +263,20 @@ __global__ __launch_bounds__(256) void dispatch_codes_kernel(DispatchArgs p) {
     }
 }
 
-// A row's chunks as near to equal blocks of at most 256 threads, whole waves.
+// A row's chunks as near to equal blocks of at most 256 threads, whole waves. Rows of fewer chunks leave
+// lanes idle: 4096 tokens to eight rows each, 256 columns as bf16 5.1 us (3.7 TB/s), as codes 5.5 (2.0); 512:
+// 7.6 (5.0) and 6.5 (3.3); 1024: 15.7 (4.8) and 8.8 (4.9).
 static void row_grid(int64_t rows, int64_t chunks, dim3* grid, dim3* block) {
     const int64_t ny = (chunks + 255) / 256;
     *block = dim3((unsigned)(((chunks + ny - 1) / ny + 63) / 64 * 64));
     *grid = dim3((unsigned)rows, (unsigned)ny);
 }
 
+// Stores past the caches go by R, the rows that there may be, because the rows that are written are known
+// on the GPU alone. Where a GPU holds a share of the experts and R is one row a pair, ordinary stores would
+// be faster. 7168 columns, 8 pairs a token, codes copied, ordinary | past the caches: all pairs here 777
+// tokens 10.0 | 11.2 us, a quarter 4.9 | 5.5, an eighth 3.8 | 4.4, an eighth of 4096 tokens 10.2 | 13.8. With the grouped
+// GEMM that reads them (4096 outputs) the two are alike: 777 tokens, a quarter 220 | 217, an eighth 209 | 205.
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t stream) {
     dim3 grid, block;
     row_grid(a.T, a.K / 8, &grid, &block);
@@ -296,7 +304,8 @@ hipError_t launch_dispatch_codes(const DispatchArgs& a, hipStream_t stream) {
 // NB rows in flight a thread. CK: -1, or the code type of the rows' checkpoint: 16 lanes hold a
 // group, and lane k of them stores the scale of the batch's k-th row. Bytes bound it: 4096 x 7168, eight
 // rows each and a base, 588 MB in 113 us (5.2 TB/s, a large copy's rate), with the checkpoint 830 MB in
-// 163 us (5.1); one token 2.9 us.
+// 163 us (5.1); one token 2.9 us. fp32 rows to bf16 without a base 999 MB in 196 us (5.1), 2048 tokens with
+// the checkpoint 617 MB in 114 us (5.4). 4096 tokens of 256 columns 4.5 us (4.2), of 512 7.5 (5.0).
 template <int RK, int CK, int NB, int S>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs p) {
     const int64_t t = blockIdx.x, K = p.K;
@@ -398,7 +407,8 @@ __device__ __forceinline__ int here(int x) {
 // in 107 to 113 us (4.8 to 5.1 TB/s; a large copy 5.2). Rows through buffer resources, eight times four
 // scalar registers that spilled, 8 columns a thread: 142 us; scalar bases and 16 columns, 448 threads
 // a token: 121; at most 256 threads, two rounds a row and more tokens on a CU: 107 (192: 114, 128: 114,
-// 64: 108). The block depends on the width and the types alone: a token's sums do not depend on T.
+// 64: 108). fp32 rows to bf16 1468 MB in 288 us (5.1), to codes 2048 tokens 617 MB in 128 us (4.8). Narrow rows
+// leave lanes idle: 4096 tokens of 256 columns, codes 15.2 us (1.3 TB/s), bf16 8.9 (4.0); 512: 17.0 (2.3) and 12.9 (5.5). The block depends on the width and the types alone: a token's sums do not depend on T.
 template <int RK, int Q, int NB, int S>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineBwdArgs p) {
     constexpr int U = (RK == R_FP8 || RK == R_INT8) && Q >= 0 ? 2 : 1, W = 8 * U, LG = 16 / U;   // lanes of a group
@@ -548,6 +558,12 @@ template <int RK, int Q, int NB> static void combine_bwd_nb(const CombineBwdArgs
 // 4096: 130 | 110.6 | 109.4; 4 pairs a token, 600 tokens 13.4 | 15.6, 1100: 21.9 | 19.9, 4096: 68.6 | 59.9 | 70.6.
 // Without the weights' gradient 8192 tokens of 8 pairs: 162 | 146 | 141; rows or output in bf16 take 4 or 8 alike
 // (4096 tokens, bf16 in, codes out: 153 | 150 | 153). A pair's sum is the same in each.
+// The rule counts T * topk pairs, absent ones too, and no columns; what it takes (marked) is at most 10 % behind
+// the fastest at other widths, from bf16 to bf16 14 %. 8 pairs a token, codes: 512 columns, 300 tokens 4.5* | 5.5 | 8.4 us, 1100: 7.2 | 7.8* |
+// 10.0, 4096: 17.5 | 16.3 | 17.6*; 1536 columns, 300: 5.5* | 6.7 | 9.8, 500: 6.9 | 7.5* | 10.6, 1100: 12.4 | 12.7* | 15.0,
+// 4096: 37.3 | 31.9 | 32.0*; 16384 columns, 300: 23.9* | 25.9 | 33.0, 500: 37.8 | 32.7* | 38.2, 1100: 72.9 | 67.1* | 76.2,
+// 4096: 253 | 242 | 253*. An eighth of the pairs here, 7168 columns: 500 tokens 8.7 | 9.5* | 10.6, 1100: 15.2 | 14.4* |
+// 15.4, 4096: 41.4 | 36.7 | 38.3*. bf16 to bf16, 1536 columns: 500 tokens 7.5 | 7.9* | 9.0, 2000: 22.2 | 22.7* | 20.0.
 template <int RK, int Q> static void combine_bwd_s(const CombineBwdArgs& a, hipStream_t stream) {
     const int64_t pairs = a.T * a.at.topk;
     if (a.at.topk <= 2 || pairs < 3600) combine_bwd_nb<RK, Q, 2>(a, (a.at.topk + 1) / 2, stream);

@@ -487,7 +487,8 @@ bfq_status bfq_norm_residual_backward(const void* y, const void* res_out, bfq_dt
  * A pair without a row (pair_rows[q] outside [0, R), or in pair order an id outside [0, E)) is left
  * out: it adds nothing, whatever its weight, and its row is neither read nor written. In what is
  * written, each row is some pair's at most once, as bfq_moe_sort's places are; where two pairs share
- * one, its contents are those of either, mixed. With R = 0 every tensor over rows may be NULL. What belongs to
+ * one, its contents are those of either, mixed. With R = 0 every tensor over rows may be NULL; with T = 0 every
+ * tensor over tokens or pairs, beside rows of any number (both orders are the same then). What belongs to
  * a token does not depend on T, and equal calls give equal bits. K a positive multiple of 8, of 128 where codes are
  * read or written, at most 2^23. */
 
@@ -500,6 +501,7 @@ bfq_status bfq_norm_residual_backward(const void* y, const void* res_out, bfq_dt
  * the lowest group). A logit of -inf masks an expert, as does a key of -inf: it is never taken, and
  * where fewer than topk are left (in the groups that take part) the last ids are -1 with weight 0. A
  * logit of +inf counts as the largest finite value; a NaN counts as larger than any key.
+ * Scores that are no keys are formed in fp32, and so are their sums; a sigmoid below 2^-126 counts as 0 there.
  *   logits [T][E] BF16 | FP16 | FP32; topk_ids [T][topk] int32; topk_weights [T][topk] fp32.
  * 1 <= E <= 1023, topk <= min(E, 64, the experts of topk_groups groups), n_groups <= 64. */
 bfq_status bfq_moe_route(const void* logits, bfq_dtype logits_dtype, const float* bias, int64_t T,
